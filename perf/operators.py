@@ -278,7 +278,8 @@ def _ours(s):
         return {**_named(r, case), "dlogits": _grads(r, s, [s["logits"]])[0]}
     if op == "linear_train":
         r = itl.linear_token_logp(s["hidden"], s["weight"], s["tokens"], top_k=case["k"], ignore_index=IGNORE,
-                                  temperature=case["temperature"], return_entropy=case["entropy"])
+                                  temperature=case["temperature"], return_entropy=case["entropy"],
+                                  save_logits=True)  # 1.2 GB of 288 until the backward, which then computes one product less
         dhidden, dweight = _grads(r, s, [s["hidden"], s["weight"]])
         return {**_named(r, case), "dhidden": dhidden, "dweight": dweight}
     hidden, weight = s["hidden"], s["weight"]
