@@ -19,3 +19,19 @@ from .ops import (  # noqa: F401
     logp_fwd,
     prepare_weight,
 )
+from .token_ops import (  # noqa: F401
+    QuantizedRows,
+    TokenLogp,
+    batch_invariant_token_logp,
+    linear_token_logp,
+    linear_token_logp_bwd,
+    linear_token_logp_fwd,
+    norm_linear_token_logp,
+    quantize_rows,
+    rms_norm,
+    rms_norm_bwd,
+    rms_norm_fwd,
+    rms_norm_quantized,
+    token_logp_bwd,
+    token_logp_fwd,
+)

@@ -38,6 +38,12 @@ LOGP_BWD_PREPARED = 4
 LOGP_BWD_SAVED_LOGITS = 8
 LOGP_BWD_BF16_OUT = 16
 
+LOGP_MAX_TOKENS = 256
+LOGP_MAX_TOP = 64
+LOGP_TOKEN_KEEPS_LOGITS = 1
+LOGP_TOKEN_ROUND_BF16 = 2
+LOGP_TOKEN_Q8 = 4
+
 _i32, _i64, _sz, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
 _f32 = ctypes.c_float
 
@@ -60,6 +66,30 @@ _SIGNATURES = {
                                _i32, _vp, _i64, _vp, _i64, _i64, _vp, _sz, _vp]),
     "linear_logp_prepared_bytes": (_sz, [_i64, _i64]),
     "linear_logp_prepare_weight": (_i32, [_vp, _i64, _i64, _i64, _vp, _sz, _vp]),
+    "token_logp_fwd_workspace_bytes": (_sz, [_i64, _i64, _i32, _i32, _i32]),
+    "token_logp_fwd": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i32, _i64, _i64, _i32, _i32,
+                              _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "token_logp_bwd": (_i32, [_vp, _i32, _i64, _i64, _i64, _vp, _i32, _i64, _i64, _vp, _i32,
+                              _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "linear_token_logp_fwd_workspace_bytes": (_sz, [_i64, _i64, _i64, _i64, _i32, _i32, _i64]),
+    "linear_token_logp_fwd": (_i32, [_vp, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _i32, _i64,
+                                     _i64, _f32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32,
+                                     _i64, _vp, _sz, _i64, _vp, _sz, _vp]),
+    "linear_token_logp_bwd_workspace_bytes": (_sz, [_i64, _i64, _i64, _i32, _i64]),
+    "linear_token_logp_bwd": (_i32, [_vp, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _i32, _i64,
+                                     _i64, _vp, _i32, _f32, _i32, _vp, _i32, _i64, _vp, _sz, _vp,
+                                     _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i64, _vp, _i64,
+                                     _i64, _vp, _sz, _vp]),
+    "linear_token_logp_q8_fwd": (_i32, [_vp, _i64, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _vp,
+                                        _i32, _i64, _i64, _f32, _i32, _vp, _vp, _vp, _vp, _vp,
+                                        _i64, _vp, _sz, _vp]),
+    "rms_norm_fwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _i32, _i64, _i64, _f32, _vp, _i64, _vp,
+                            _i64, _vp, _vp]),
+    "rms_norm_q8_fwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _i32, _i64, _i64, _f32, _vp, _i64, _vp,
+                               _vp, _i64, _vp]),
+    "rms_norm_bwd_workspace_bytes": (_sz, [_i64, _i64]),
+    "rms_norm_bwd": (_i32, [_vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _i32, _i64, _i64, _vp,
+                            _i64, _vp, _vp, _sz, _vp]),
     "logp_status_str": (ctypes.c_char_p, [_i32]),
     "logp_contract_id": (ctypes.c_char_p, []),
 }

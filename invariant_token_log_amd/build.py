@@ -11,6 +11,8 @@ import os
 import shutil
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -18,7 +20,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libinvariant_logp.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
-SOURCES = ["api.hip", "logp_kernels.hip", "linear_logp.hip", "linear_bwd.hip"]
+SOURCES = ["api.hip", "logp_kernels.hip", "linear_logp.hip", "linear_bwd.hip",
+           "token_api.hip", "token_logp.hip", "linear_q8.hip", "rms_norm.hip"]
 # bandwidth probes that bench.py times next to the kernels (not part of the
 # library's C ABI)
 PROBE_PATH = os.path.join(HERE, "libitl_ceiling.so")
@@ -46,10 +49,7 @@ def hipcc():
     raise RuntimeError("hipcc not found (ROCm is required to build the library)")
 
 
-def _compile(sources, out, verbose):
-    tmp = out + ".tmp"
-    cmd = [hipcc(), *FLAGS, "-I", INCLUDE, "-I", CSRC,
-           *[os.path.join(CSRC, s) for s in sources], "-o", tmp]
+def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
@@ -63,6 +63,18 @@ def _compile(sources, out, verbose):
             if "-packed-fp32-ops' is not a recognized feature" not in ln]
     if verbose and rest:
         sys.stderr.write("\n".join(rest) + "\n")
+
+
+def _compile(sources, out, verbose):
+    """Compile every source to an object (side by side) and link them."""
+    tmp = out + ".tmp"
+    flags = [f for f in FLAGS if f != "-shared"]
+    with tempfile.TemporaryDirectory() as objs:
+        pairs = [(os.path.join(CSRC, s), os.path.join(objs, s + ".o")) for s in sources]
+        with ThreadPoolExecutor(4) as pool:
+            list(pool.map(lambda p: _run([hipcc(), *flags, "-I", INCLUDE, "-I", CSRC, "-c", p[0],
+                                          "-o", p[1]], verbose), pairs))
+        _run([hipcc(), *FLAGS, *[o for _, o in pairs], "-o", tmp], verbose)
     os.replace(tmp, out)
     return out
 

@@ -5,6 +5,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "token_launch.h"
+
 namespace itl {
 
 enum { kF32 = 0, kBF16 = 1, kF16 = 2 };
@@ -95,14 +97,18 @@ LinearBwdLayout linear_bwd_layout(int64_t n, int64_t h, int64_t v, int32_t flags
 // product and its W^T the dh product as K-contiguous operands (without it,
 // the dh product reads W's rows in place as a K-outer operand, with the same
 // bits).  vocab_chunk: columns per chunk (0 = kDefaultChunk), any value
-// gives the same bits; ws: linear_bwd_layout(...).total bytes.
+// gives the same bits; ws: linear_bwd_layout(...).total bytes.  tokens (or
+// null): the row's target is replaced by a list of entries; targets then hold
+// the activity of launch_token_rows, grad its sums, and every chunk's dz gets
+// the entries' columns from launch_token_dz.
 void launch_linear_bwd(const uint16_t* hidden, int64_t ld_h, const uint16_t* weight, int64_t ld_w,
                        int64_t n, int64_t h, int64_t v, Targets targets, int64_t ignore,
                        const void* zsaved, int32_t z_bf16, int64_t ld_z,
                        const uint16_t* prepared, const float* lse,
                        const float* grad, float inv_t, int32_t round_bf16, const float* ent,
                        const float* gent, bool bf16_out, void* dh, int64_t ld_dh, void* dw,
-                       int64_t ld_dw, int64_t vocab_chunk, char* ws, hipStream_t s);
+                       int64_t ld_dw, int64_t vocab_chunk, char* ws, hipStream_t s,
+                       const TokenDz* tokens = nullptr);
 
 // Prepared weight, bf16, both parts K32-blocked (mfma_gemm.h) with vp =
 // round_up(v, 256): W [vp rows, K = h] (rows v.. zero), then W^T [h rows,

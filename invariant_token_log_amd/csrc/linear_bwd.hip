@@ -621,7 +621,8 @@ void launch_linear_bwd(const uint16_t* hidden, int64_t ld_h, const uint16_t* wei
                        const uint16_t* prepared, const float* lse,
                        const float* grad, float inv_t, int32_t round_bf16, const float* ent,
                        const float* gent, bool bf16_out, void* dh, int64_t ld_dh, void* dw,
-                       int64_t ld_dw, int64_t vocab_chunk, char* ws, hipStream_t s) {
+                       int64_t ld_dw, int64_t vocab_chunk, char* ws, hipStream_t s,
+                       const TokenDz* tokens) {
   if (n == 0) {
     // dh has no rows; dW is a sum over no tokens.
     if (dw) {
@@ -679,6 +680,7 @@ void launch_linear_bwd(const uint16_t* hidden, int64_t ld_h, const uint16_t* wei
                            v, l.np, targets.p, targets.is32, ignore, lse, grad, inv_t, round_bf16,
                            ent, gent, c0, cols, dz);
     }
+    if (tokens) launch_token_dz(*tokens, n, v, inv_t, ent, gent, c0, cols, dz, s);
     // dW[c0, c1) = dz_c^T h: K = every token, ascending (final rows); dz_c
     // read along its token axis (K-outer)
     if (dw && c0 < v) {
