@@ -160,9 +160,9 @@ int32_t linear_token_logp_bwd(const void* hidden, int64_t ld_h, const void* weig
  * The forward through an 8-bit LM head (frozen weights: scoring, decoding):
  *   logits[r, j] = (sum_k hidden[r, k] weight[j, k]) hidden_scale[r] weight_scale[j]
  * with hidden [n, ld_h] and weight [v, ld_w] in e4m3 (OCP 8-bit floating
- * point: 4 exponent bits, 3 mantissa bits, largest value 448), products on the
- * 8-bit matrix cores, fp32 sums over K in ascending order, no split.  h a
- * multiple of 64; 16-byte aligned rows; scales fp32 [n] and [v].  The rest: as
+ * point: 4 exponent bits, 3 mantissa bits, largest value 448), exact products
+ * and fp32 sums, no split.  h a multiple of 64; 16-byte aligned rows at most
+ * 2^23 bytes apart (LOGP_ERR_SHAPE); scales fp32 [n] and [v].  The rest: as
  * linear_token_logp_fwd (workspace flag LOGP_TOKEN_Q8); its own arithmetic, so
  * its bits are not linear_token_logp_fwd's, but they are batch invariant too.
  */

@@ -33,26 +33,42 @@ namespace itl {
 namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kV = kLinearTile;    // vocabulary columns per tile
 constexpr int kStep = 64;          // K bytes per matrix instruction
 constexpr int kQThreads = 512;     // 8 waves
-constexpr int kUnitScale = 0x7f7f7f7f;  // block scales of 2^0
 
-__device__ __forceinline__ f32x16 mfma_q8(i32x8 a, i32x8 b, f32x16 c) {
-  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a, b, c, 0, 0, 0, kUnitScale, 0,
-                                                         kUnitScale);
+// Eight e4m3 values (two dwords of a chunk) as bf16, exactly.
+__device__ __forceinline__ bf16x8 widen_q8(int lo, int hi) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true);
+  const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true);
+  return bf16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
-// Two 16-byte chunks as one operand.  Which K index a byte of a lane stands
-// for does not matter as long as both operands agree: lane (row l % 32, half
-// hf = l / 32) holds chunks 2 hf and 2 hf + 1 of its row's 64 bytes.
-__device__ __forceinline__ i32x8 join(const uint8_t* lo, const uint8_t* hi) {
-  const i32x4 a = *reinterpret_cast<const i32x4*>(lo);
-  const i32x4 b = *reinterpret_cast<const i32x4*>(hi);
-  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+// acc[i][j] += the 32 products of the 16-byte chunks w[i] and h[j] that the two
+// halves of the wave hold, 16 at a time.  Which K index a byte stands for does
+// not matter as long as both operands agree.
+template <int NI, int NJ>
+__device__ __forceinline__ void mfma_q8(const i32x4 (&w)[NI], const i32x4 (&h)[NJ],
+                                        f32x16 (&acc)[NI][NJ]) {
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    bf16x8 b[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) b[j] = widen_q8(h[j][2 * t], h[j][2 * t + 1]);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const bf16x8 a = widen_q8(w[i][2 * t], w[i][2 * t + 1]);
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b[j], acc[i][j], 0, 0, 0);
+    }
+  }
 }
 
 // What the epilogue needs of the tile's hidden rows and vocabulary columns.
@@ -196,142 +212,118 @@ __device__ __forceinline__ void q8_epilogue(f32x16 (&acc)[NI][NJ], Q8Reduce<ROWS
 }
 
 // ---------------------------------------------------------------------------
-// Wide: the staging of mfma_gemm.h's mainloop_pairs in bytes.  Hidden rows
-// come K32-blocked in its sense (16 rows x 64 bytes contiguous) into four
-// slots of 256 x 64 bytes, weight rows row-major into two slots of 256 x 128
-// bytes (whole lines), three steps in flight; waves 0-3 issue the loads, each
-// wave's fragments of the next step are read while the matrix instructions of
-// this one run.
+// Staging, for both kernels: slots of [256 weight rows | R hidden rows] x 128
+// bytes, a "pair" of K steps, whole lines of row-major operands; chunk c (16
+// bytes) of row r sits in place c ^ swzp(r), which puts the 16 rows of a read
+// on different banks.  A load fills 8 rows; rows past the data read the last
+// row, and the missing second half of an odd last pair the first half: every
+// load stays in bounds, and what it brings is masked or not read.
 // ---------------------------------------------------------------------------
-constexpr int kHSlot = 256 * kStep;      // bytes
-constexpr int kWSlot = 256 * 2 * kStep;
-
-struct SmemWide {
-  uint8_t h[4][kHSlot];
-  uint8_t w[2][kWSlot];
-  Q8Reduce<256> rd;
-  int slot;
-};
-
-using gemm::swz;
 using gemm::swzp;
 using gemm::wait_vm;
 using gemm::wait_vm_lgkm0;
 
+constexpr int kPair = 2 * kStep;  // bytes of a row per pair
+
+// One direct 16-byte load a lane, global -> LDS at dst + 16 * lane; NT: past
+// the caches.
+template <bool NT>
+__device__ __forceinline__ void load_lds16(const uint8_t* src, uint8_t* dst) {
+  __builtin_amdgcn_global_load_lds(src, dst, 16, 0, NT ? 2 : 0);
+}
+
+// Offset from row row0 of this lane's chunk of row block `blk` (8 rows) at
+// pair 0; at most 256 rows of at most kMaxQ8Stride bytes, so 32 bits hold it.
+__device__ __forceinline__ uint32_t pair_source(int64_t ld, int64_t row0, int64_t rows, int blk,
+                                                int lane) {
+  const int r = blk * 8 + lane / 8;
+  const int64_t last = rows - 1 - row0;
+  return static_cast<uint32_t>((r < last ? r : last) * ld) + ((lane % 8) ^ swzp(r)) * 16;
+}
+// How far the lane steps back in an odd last pair (blocks 4 apart agree).
+__device__ __forceinline__ int pair_back(int ksteps, int blk, int lane) {
+  return (ksteps & 1) && ((lane % 8) ^ swzp(blk * 8 + lane / 8)) >= 4 ? kStep : 0;
+}
+
+// ---------------------------------------------------------------------------
+// Wide: two slots of 64 KiB; while a pair is multiplied the next one loads,
+// issued by waves 0-3 right after the barrier.
+// ---------------------------------------------------------------------------
+struct SmemWide {
+  uint8_t s[2][(kV + 256) * kPair];
+  Q8Reduce<256> rd;
+  int slot;
+};
+
 template <bool LOADER>
 __device__ __forceinline__ void q8_mainloop(SmemWide& sm, const uint8_t* __restrict__ H,
-                                            int64_t m0, const uint8_t* __restrict__ W,
-                                            int64_t ld_w, int64_t v0, int64_t v, int ksteps,
+                                            int64_t ld_h, int64_t m0, int64_t n,
+                                            const uint8_t* __restrict__ W, int64_t ld_w,
+                                            int64_t v0, int64_t v, int ksteps,
                                             f32x16 (&acc)[4][2]) {
-  const int tid = threadIdx.x;
-  const int lane = tid % kWave;
-  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int wm = wave / 4, wn = wave % 4;
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int row = lane % 32, hf = lane / 32;
   const int npairs = (ksteps + 1) / 2;
-  // loader sources: hidden blocks wave + 4u (1 KiB, 16 rows), weight rows
-  // (wave + 4u) * 8 + lane / 8
-  const uint8_t* hp[4];
-  const uint8_t* wp[8];
-  int wback = 0;  // an odd last pair has no second half: those lanes read the first
+  uint32_t wp[8], hp[8];
+  int back = 0;
   if constexpr (LOADER) {
-    const int lrow = lane / 4;
-    const int lofs = lrow * kStep + ((lane % 4) ^ swz(lrow)) * 16;
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      hp[u] = H + (m0 / 16 + wave + 4 * u) * (static_cast<int64_t>(ksteps) * 1024) + lofs;
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      const int r = (wave + 4 * u) * 8 + lane / 8;
-      wp[u] = W + min(v0 + r, v - 1) * ld_w + ((lane % 8) ^ swzp(r)) * 16;
+      wp[u] = pair_source(ld_w, v0, v, wave + 4 * u, lane);
+      hp[u] = pair_source(ld_h, m0, n, wave + 4 * u, lane);
     }
-    // swzp depends on u only through multiples of 32 rows, which it ignores
-    if (((lane % 8) ^ swzp(wave * 8 + lane / 8)) >= 4 && (ksteps & 1)) wback = kStep;
+    back = pair_back(ksteps, wave, lane);
   }
-#define ITL_ISSUE_H(SLOT, STEP)                                                                 \
-  if constexpr (LOADER) {                                                                       \
-    const int64_t k_ = static_cast<int64_t>(STEP) * 1024;                                       \
-    _Pragma("unroll") for (int u = 0; u < 4; ++u) __builtin_amdgcn_global_load_lds(             \
-        hp[u] + k_, sm.h[SLOT] + (wave + 4 * u) * 1024, 16, 0, 0);                              \
+  auto issue = [&](int p) {
+    if constexpr (LOADER) {
+      const uint8_t* w0 = W + v0 * ld_w + static_cast<int64_t>(p) * kPair;
+      const uint8_t* h0 = H + m0 * ld_h + static_cast<int64_t>(p) * kPair;
+      const int b = p == npairs - 1 ? back : 0;
+      uint8_t* d = sm.s[p % 2] + wave * 1024;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) load_lds16<false>(w0 + (wp[u] - b), d + u * 4096);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) load_lds16<false>(h0 + (hp[u] - b), d + kV * kPair + u * 4096);
+    }
+  };
+  const int sw = swzp(row);  // repeats every 16 rows
+  const int wofs = ((wave / 4) * 128 + row) * kPair;
+  const int hofs = (kV + (wave % 4) * 64 + row) * kPair;
+  issue(0);
+  for (int p = 0; p < npairs; ++p) {
+    // pair p has landed (it is all that was in flight), and nobody reads the
+    // other slot any more
+    wait_vm_lgkm0<0>();
+    __builtin_amdgcn_s_barrier();
+    if (p + 1 < npairs) issue(p + 1);
+    const uint8_t* w_ = sm.s[p % 2] + wofs;
+    const uint8_t* h_ = sm.s[p % 2] + hofs;
+    i32x4 cw[2][4], ch[2][2];
+    auto read = [&](int u, i32x4 (&fw)[4], i32x4 (&fh)[2]) {
+      const int c = ((2 * u + hf) ^ sw) * 16;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) fh[j] = *reinterpret_cast<const i32x4*>(h_ + 32 * j * kPair + c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) fw[i] = *reinterpret_cast<const i32x4*>(w_ + 32 * i * kPair + c);
+    };
+    read(0, cw[0], ch[0]);
+    read(1, cw[1], ch[1]);
+    mfma_q8<4, 2>(cw[0], ch[0], acc);
+    if (2 * p + 1 < ksteps) {
+      read(2, cw[0], ch[0]);
+      mfma_q8<4, 2>(cw[1], ch[1], acc);
+      read(3, cw[1], ch[1]);
+      mfma_q8<4, 2>(cw[0], ch[0], acc);
+    }
+    mfma_q8<4, 2>(cw[1], ch[1], acc);
   }
-#define ITL_ISSUE_W(SLOT, PAIR)                                                                 \
-  if constexpr (LOADER) {                                                                       \
-    const int p_ = (PAIR);                                                                      \
-    const int64_t k_ = static_cast<int64_t>(p_) * (2 * kStep) - (p_ == npairs - 1 ? wback : 0); \
-    _Pragma("unroll") for (int u = 0; u < 8; ++u) __builtin_amdgcn_global_load_lds(             \
-        wp[u] + k_, sm.w[SLOT] + (wave + 4 * u) * 1024, 16, 0, 0);                              \
-  }
-  const int wrow = wm * 128 + row, hrow = wn * 64 + row;
-  const int wsw = swzp(wrow), hsw = swz(hrow);  // both repeat every 32 rows
-  constexpr int NH = LOADER ? 4 : 0, NW = LOADER ? 8 : 0;
-  ITL_ISSUE_H(0, 0);
-  ITL_ISSUE_H(1, 1 < ksteps ? 1 : ksteps - 1);
-  ITL_ISSUE_W(0, 0);
-  ITL_ISSUE_H(2, 2 < ksteps ? 2 : ksteps - 1);
-  ITL_ISSUE_H(3, 3 < ksteps ? 3 : ksteps - 1);
-  ITL_ISSUE_W(1, 1 < npairs ? 1 : npairs - 1);
-  wait_vm<2 * NH + NW>();
-  __builtin_amdgcn_s_barrier();
-  i32x8 xw[4], xh[2], yw[4], yh[2];
-#define ITL_READ(FW, FH, STEP)                                                                  \
-  {                                                                                             \
-    const uint8_t* h_ = sm.h[(STEP) % 4];                                                       \
-    const uint8_t* w_ = sm.w[((STEP) / 2) % 2];                                                 \
-    const int c_ = 4 * ((STEP) % 2) + 2 * hf;                                                   \
-    _Pragma("unroll") for (int j = 0; j < 2; ++j)                                               \
-      FH[j] = join(h_ + (hrow + 32 * j) * kStep + ((2 * hf) ^ hsw) * 16,                        \
-                   h_ + (hrow + 32 * j) * kStep + ((2 * hf + 1) ^ hsw) * 16);                   \
-    _Pragma("unroll") for (int i = 0; i < 4; ++i)                                               \
-      FW[i] = join(w_ + (wrow + 32 * i) * 2 * kStep + (c_ ^ wsw) * 16,                          \
-                   w_ + (wrow + 32 * i) * 2 * kStep + ((c_ + 1) ^ wsw) * 16);                   \
-  }
-#define ITL_MFMA(CW, CH)                                                                        \
-  _Pragma("unroll") for (int i = 0; i < 4; ++i)                                                 \
-    _Pragma("unroll") for (int j = 0; j < 2; ++j) acc[i][j] = mfma_q8(CW[i], CH[j], acc[i][j]);
-  ITL_READ(xw, xh, 0)
-  // Waits as in mainloop_pairs: before an even step KT the hidden block of
-  // KT + 1 (issued at KT - 3) has landed once only the loads issued after it
-  // are in flight, before an odd one the weight pair of KT + 1 too.
-#define ITL_QSTEP(CW, CH, NXW, NXH, KT, ODD)                                                    \
-  {                                                                                             \
-    if constexpr (ODD)                                                                          \
-      wait_vm_lgkm0<NH>();                                                                      \
-    else                                                                                        \
-      wait_vm_lgkm0<2 * NH + NW>();                                                             \
-    __builtin_amdgcn_s_barrier();                                                               \
-    ITL_ISSUE_H((KT) % 4, (KT) + 4 < ksteps ? (KT) + 4 : ksteps - 1);                           \
-    if constexpr (ODD) {                                                                        \
-      const int q_ = ((KT) + 3) / 2;                                                            \
-      ITL_ISSUE_W(q_ % 2, q_ < npairs ? q_ : npairs - 1);                                       \
-    }                                                                                           \
-    ITL_READ(NXW, NXH, (KT) + 1)                                                                \
-    ITL_MFMA(CW, CH)                                                                            \
-    if constexpr (LOADER) __builtin_amdgcn_sched_group_barrier(0x020, ODD ? NH + NW : NH, 0);   \
-    _Pragma("unroll") for (int u = 0; u < 6; ++u) {                                             \
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                                        \
-      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);                                        \
-    }                                                                                           \
-    __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);                                          \
-  }
-  int kt = 0;
-  for (; kt + 1 < ksteps; kt += 2) {
-    ITL_QSTEP(xw, xh, yw, yh, kt, false)
-    ITL_QSTEP(yw, yh, xw, xh, kt + 1, true)
-  }
-  if (kt < ksteps) {
-    ITL_MFMA(xw, xh)
-  }
-#undef ITL_QSTEP
-#undef ITL_MFMA
-#undef ITL_READ
-#undef ITL_ISSUE_W
-#undef ITL_ISSUE_H
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
 template <bool ENT>
 __global__ __launch_bounds__(kQThreads) void q8_stats_wide(
-    const uint8_t* __restrict__ hidden, const float* __restrict__ hs,
+    const uint8_t* __restrict__ hidden, int64_t ld_h, const float* __restrict__ hs,
     const uint8_t* __restrict__ weight, int64_t ld_w, const float* __restrict__ ws, int64_t n,
     int64_t v, int ksteps, int mblocks, int vblocks, const void* __restrict__ tgt, int32_t tgt32,
     int64_t ignore, float inv_t, float* __restrict__ pm, float* __restrict__ ps,
@@ -355,31 +347,24 @@ __global__ __launch_bounds__(kQThreads) void q8_stats_wide(
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
   if (gemm::loader_wave())
-    q8_mainloop<true>(sm, hidden, m0, weight, ld_w, v0, v, ksteps, acc);
+    q8_mainloop<true>(sm, hidden, ld_h, m0, n, weight, ld_w, v0, v, ksteps, acc);
   else
-    q8_mainloop<false>(sm, hidden, m0, weight, ld_w, v0, v, ksteps, acc);
+    q8_mainloop<false>(sm, hidden, ld_h, m0, n, weight, ld_w, v0, v, ksteps, acc);
   __syncthreads();
   q8_epilogue<4, 2, 256, ENT>(acc, sm.rd, (wave / 4) * 4, (wave % 4) * 64, tid, m0, v0, vb,
                               vblocks, n, v, inv_t, pm, ps, pw, pt, z, ld_z);
 }
 
 // ---------------------------------------------------------------------------
-// Narrow: S slots of [256 weight rows | 32 NB hidden rows] x 128 bytes, both
-// row-major, every wave loading; wave w computes vocabulary group w for all
-// 32 NB rows.
+// Narrow: three or four slots with 32 NB hidden rows, every wave loading; wave
+// w computes vocabulary group w for all hidden rows.
 // ---------------------------------------------------------------------------
-// One direct 16-byte load a lane, global -> LDS at dst + 16 * lane; NT: past the caches.
-template <bool NT>
-__device__ __forceinline__ void load_lds16(const uint8_t* src, uint8_t* dst) {
-  __builtin_amdgcn_global_load_lds(src, dst, 16, 0, NT ? 2 : 0);
-}
-
 template <int NB>
 constexpr int kNarrowSlots = NB == 1 ? 4 : 3;
 
 template <int NB>
 struct SmemNarrowQ8 {
-  uint8_t s[kNarrowSlots<NB>][(kV + 32 * NB) * 2 * kStep];
+  uint8_t s[kNarrowSlots<NB>][(kV + 32 * NB) * kPair];
   Q8Reduce<32 * NB> rd;
 };
 
@@ -391,50 +376,39 @@ __device__ __forceinline__ void q8_mainloop_narrow(SmemNarrowQ8<NB>& sm,
                                                    int64_t ld_w, int64_t v0, int64_t v, int ksteps,
                                                    f32x16 (&acc)[1][NB]) {
   constexpr int S = kNarrowSlots<NB>;
-  const int tid = threadIdx.x;
-  const int lane = tid % kWave;
-  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int npairs = (ksteps + 1) / 2;
-  // A load fills 8 rows x 128 bytes; weight loads wave + 8 u (u < 4), and a
-  // hidden load for the waves below 4 NB.  Chunk c of row r sits in slot c ^
-  // swzp(r).
-  const bool has_h = wave < 4 * NB;
+  constexpr int kHBlocks = 4 * NB;              // hidden blocks of 8 rows
+  constexpr int NH = kHBlocks > 8 ? 2 : 1;      // loads of them a wave
+  const bool has_h = wave < kHBlocks;
   const uint8_t* wp[4];
-  int back_w = 0, back_h = 0;
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int r = (wave + 8 * u) * 8 + lane / 8;
-    wp[u] = weight + min(v0 + r, v - 1) * ld_w + ((lane % 8) ^ swzp(r)) * 16;
-  }
-  constexpr int kHLoads = 4 * NB;  // hidden loads per pair: one or two a wave
-  constexpr int NH = kHLoads > 8 ? 2 : 1;
   const uint8_t* hp[NH];
 #pragma unroll
-  for (int u = 0; u < NH; ++u) {
-    const int r = (wave % kHLoads + 8 * u) * 8 + lane / 8;
-    hp[u] = hidden + min(static_cast<int64_t>(r), n - 1) * ld_h + ((lane % 8) ^ swzp(r)) * 16;
-  }
-  if (ksteps & 1) {  // no second half in the last pair: its lanes read the first
-    if (((lane % 8) ^ swzp(wave * 8 + lane / 8)) >= 4) back_w = kStep;
-    if (((lane % 8) ^ swzp((wave % kHLoads) * 8 + lane / 8)) >= 4) back_h = kStep;
-  }
-#define ITL_ISSUE_PAIR(SLOT, PAIR)                                                              \
-  {                                                                                             \
-    const int s_ = (SLOT);                                                                      \
-    const int p_ = (PAIR) < npairs ? (PAIR) : npairs - 1;                                       \
-    const int64_t k_ = static_cast<int64_t>(p_) * 2 * kStep;                                    \
-    const bool end_ = p_ == npairs - 1;                                                         \
-    _Pragma("unroll") for (int u = 0; u < 4; ++u) load_lds16<true>(                             \
-        wp[u] + k_ - (end_ ? back_w : 0), sm.s[s_] + (wave + 8 * u) * 1024);          \
-    if (has_h) {                                                                                \
-      _Pragma("unroll") for (int u = 0; u < NH; ++u) load_lds16<false>(                         \
-          hp[u] + k_ - (end_ ? back_h : 0),                                                     \
-          sm.s[s_] + kV * 2 * kStep + (wave + 8 * u) * 1024);                         \
-    }                                                                                           \
-  }
+  for (int u = 0; u < 4; ++u)
+    wp[u] = weight + v0 * ld_w + pair_source(ld_w, v0, v, wave + 8 * u, lane);
+#pragma unroll
+  for (int u = 0; u < NH; ++u)
+    hp[u] = hidden + pair_source(ld_h, 0, n, wave % kHBlocks + 8 * u, lane);
+  const int back_w = pair_back(ksteps, wave, lane);
+  const int back_h = pair_back(ksteps, wave % kHBlocks, lane);
+  auto issue = [&](int slot, int pair) {
+    const int p = pair < npairs ? pair : npairs - 1;
+    const int64_t k = static_cast<int64_t>(p) * kPair;
+    const bool end = p == npairs - 1;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      load_lds16<true>(wp[u] + k - (end ? back_w : 0), sm.s[slot] + (wave + 8 * u) * 1024);
+    if (has_h) {
+#pragma unroll
+      for (int u = 0; u < NH; ++u)
+        load_lds16<false>(hp[u] + k - (end ? back_h : 0),
+                          sm.s[slot] + kV * kPair + (wave + 8 * u) * 1024);
+    }
+  };
   const int row = lane % 32, hf = lane / 32;
   const int sw = swzp(row);
-  for (int p = 0; p < S - 1; ++p) ITL_ISSUE_PAIR(p, p)
+  for (int p = 0; p < S - 1; ++p) issue(p, p);
   // Before pair p is read its loads have landed once only those of the S - 2
   // pairs issued after it are in flight; after the barrier that holds for
   // every wave, and nobody reads slot (p - 1) % S any more, which the pair
@@ -445,23 +419,21 @@ __device__ __forceinline__ void q8_mainloop_narrow(SmemNarrowQ8<NB>& sm,
     else
       wait_vm_lgkm0<(S - 2) * 4>();
     __builtin_amdgcn_s_barrier();
-    ITL_ISSUE_PAIR((p + S - 1) % S, p + S - 1)
-    const uint8_t* w_ = sm.s[p % S] + (wave * 32 + row) * 2 * kStep;
-    const uint8_t* h_ = sm.s[p % S] + (kV + row) * 2 * kStep;
+    issue((p + S - 1) % S, p + S - 1);
+    const uint8_t* w_ = sm.s[p % S] + (wave * 32 + row) * kPair;
+    const uint8_t* h_ = sm.s[p % S] + (kV + row) * kPair;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      if (half == 1 && 2 * p + 1 >= ksteps) break;
-      const int c0 = ((4 * half + 2 * hf) ^ sw) * 16, c1 = ((4 * half + 2 * hf + 1) ^ sw) * 16;
-      const i32x8 a = join(w_ + c0, w_ + c1);
+    for (int u = 0; u < 4; ++u) {
+      if (u == 2 && 2 * p + 1 >= ksteps) break;
+      const int c = ((2 * u + hf) ^ sw) * 16;
+      const i32x4 a[1] = {*reinterpret_cast<const i32x4*>(w_ + c)};
+      i32x4 b[NB];
 #pragma unroll
-      for (int j = 0; j < NB; ++j) {
-        const uint8_t* hj = h_ + 32 * j * 2 * kStep;
-        acc[0][j] = mfma_q8(a, join(hj + c0, hj + c1), acc[0][j]);
-      }
+      for (int j = 0; j < NB; ++j) b[j] = *reinterpret_cast<const i32x4*>(h_ + 32 * j * kPair + c);
+      mfma_q8<1, NB>(a, b, acc);
     }
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-#undef ITL_ISSUE_PAIR
 }
 
 template <int NB, bool ENT>
@@ -489,10 +461,14 @@ __global__ __launch_bounds__(kQThreads) void q8_stats_narrow(
                                     ps, pw, pt, z, ld_z);
 }
 
+// The tile queue's counters, before the wide kernel.
+__global__ void clear_queue(int* queue) { queue[threadIdx.x] = 0; }
+
 }  // namespace
 
 int64_t q8_fwd_scratch_bytes(int64_t n, int64_t h) {
-  return n > 128 ? (n + 255) / 256 * 256 * h + gemm::kQueueBytes : 0;
+  (void)h;
+  return n > 128 ? gemm::kQueueBytes : 0;
 }
 
 void launch_q8_partials(const uint8_t* hidden, int64_t ld_h, const float* hs,
@@ -512,16 +488,12 @@ void launch_q8_partials(const uint8_t* hidden, int64_t ld_h, const float* hs,
     return;
   }
   const int mblocks = static_cast<int>((n + 255) / 256);
-  const int64_t np = static_cast<int64_t>(mblocks) * 256;
-  // The re-laid hidden rows: pieces of 16 rows x 64 bytes, which is the bf16
-  // blocking of rows of h / 2 two-byte elements.
-  int* queue = reinterpret_cast<int*>(scratch + np * h);
-  launch_block_rows(reinterpret_cast<const uint16_t*>(hidden), ld_h / 2, n, np, h / 2,
-                    reinterpret_cast<uint16_t*>(scratch), s, queue, gemm::kQueueBytes / 4);
+  int* queue = reinterpret_cast<int*>(scratch);
+  hipLaunchKernelGGL(clear_queue, dim3(1), dim3(gemm::kQueueBytes / 4), 0, s, queue);
   const gemm::QueuePlan qp = gemm::queue_plan(mblocks * vblocks, xcd_cus());
   auto kern = pw ? q8_stats_wide<true> : q8_stats_wide<false>;
   hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(qp.grid)), dim3(kQThreads), 0, s,
-                     reinterpret_cast<const uint8_t*>(scratch), hs, weight, ld_w, ws, n, v, ksteps,
+                     hidden, ld_h, hs, weight, ld_w, ws, n, v, ksteps,
                      mblocks, vblocks, targets.p, targets.is32, ignore, inv_t, pm, ps, pw, pt, z,
                      ld_z, queue, qp.queued);
 }

@@ -334,7 +334,8 @@ int32_t linear_token_logp_q8_fwd(const void* hidden, int64_t ld_h, const float* 
                                  size_t workspace_bytes, void* hip_stream) {
   int32_t st = check_head_sizes(n, h, v, m, top_k, row_chunk);
   if (st != LOGP_OK) return st;
-  if (ld_h < h || ld_w < h) return LOGP_ERR_SHAPE;
+  if (ld_h < h || ld_w < h || ld_h > itl::kMaxQ8Stride || ld_w > itl::kMaxQ8Stride)
+    return LOGP_ERR_SHAPE;
   if (!itl::usable_temperature(temperature)) return LOGP_ERR_VALUE;
   if (n == 0) return LOGP_OK;
   if ((st = check_tokens(tokens, token_dtype, m)) != LOGP_OK) return st;
