@@ -222,7 +222,7 @@ int32_t token_logp_fwd(const void* logits, int32_t dtype, int64_t n, int64_t v, 
   float* pm = reinterpret_cast<float*>(ws + l.pm);
   float* ps = reinterpret_cast<float*>(ws + l.ps);
   float* pw = entropy_out ? reinterpret_cast<float*>(ws + l.pw) : nullptr;
-  float* gm = top_k > 0 ? reinterpret_cast<float*>(ws + l.gm) : nullptr;
+  uint32_t* gm = top_k > 0 ? reinterpret_cast<uint32_t*>(ws + l.gm) : nullptr;
   const int chunks = itl::tile_chunks(dtype, tile_width);
   const int ntiles = static_cast<int>((v + tile_width - 1) / tile_width);
   const bool vec = rows_aligned16(logits, ld, dtype_size(dtype));

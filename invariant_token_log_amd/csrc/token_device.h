@@ -24,20 +24,38 @@ struct __attribute__((packed, aligned(2))) AnyChunk {
   uint32_t w[4];
 };
 
+// A whole chunk as it is in memory: unlike load_row_chunk it has no branch, so
+// that several of them wait together.
+template <typename T, bool VEC>
+__device__ __forceinline__ uint4 load_whole_chunk(const T* p) {
+  if constexpr (VEC) {
+    return load_stream(p);
+  } else {
+    const AnyChunk q = *reinterpret_cast<const AnyChunk*>(p);
+    return make_uint4(q.w[0], q.w[1], q.w[2], q.w[3]);
+  }
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_whole_chunk(T* p, const uint4 q) {
+  if constexpr (VEC) {
+    store_stream(p, q);
+  } else {
+    AnyChunk a;
+    a.w[0] = q.x; a.w[1] = q.y; a.w[2] = q.z; a.w[3] = q.w;
+    *reinterpret_cast<AnyChunk*>(p) = a;
+  }
+}
+
 template <typename T, bool VEC>
 __device__ __forceinline__ void load_row_chunk(const T* row, int64_t c, int64_t v,
                                                float (&x)[Elt<T>::kPerChunk]) {
   constexpr int E = Elt<T>::kPerChunk;
-  if constexpr (VEC) {
-    load_chunk<T, true>(row, c, v, x);
+  if (c + E <= v) {
+    widen_chunk<T>(load_whole_chunk<T, VEC>(row + c), x);
   } else {
-    if (c + E <= v) {
-      const AnyChunk q = *reinterpret_cast<const AnyChunk*>(row + c);
-      widen_chunk<T>(make_uint4(q.w[0], q.w[1], q.w[2], q.w[3]), x);
-    } else {
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[e] = (c + e < v) ? Elt<T>::load(row, c + e) : -INFINITY;
-    }
+    for (int e = 0; e < E; ++e) x[e] = (c + e < v) ? Elt<T>::load(row, c + e) : -INFINITY;
   }
 }
 
@@ -77,14 +95,7 @@ __device__ __forceinline__ void store_row_chunk(T* row, int64_t c, int64_t v,
                                                 const float (&x)[Elt<T>::kPerChunk]) {
   constexpr int E = Elt<T>::kPerChunk;
   if (c + E <= v) {
-    const uint4 q = round_chunk<T>(x);
-    if constexpr (VEC) {
-      store_stream(row + c, q);
-    } else {
-      AnyChunk a;
-      a.w[0] = q.x; a.w[1] = q.y; a.w[2] = q.z; a.w[3] = q.w;
-      *reinterpret_cast<AnyChunk*>(row + c) = a;
-    }
+    store_whole_chunk<T, VEC>(row + c, round_chunk<T>(x));
   } else {
 #pragma unroll
     for (int e = 0; e < E; ++e)
@@ -173,17 +184,25 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// The k-th greatest (1-based, k <= 64) of the 64 lanes' keys.
-__device__ __forceinline__ uint32_t wave_kth(uint32_t key, int k, int lane) {
-  int rank = 0;
+__device__ __forceinline__ uint32_t lane_u32(uint32_t x, int lane) {
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(x), lane));
+}
+
+// A key that at least k of the wave's 256 keys (four a lane) reach: the k-th
+// greatest, or a smaller one that exactly k reach; 0 when fewer than k are not
+// 0.  Bit by bit from the top.
+__device__ __forceinline__ uint32_t wave_bound(const uint32_t (&key)[4], int k) {
+  uint32_t bound = 0;
+#pragma unroll 1
+  for (uint32_t bit = 0x80000000u; bit; bit >>= 1) {
+    const uint32_t t = bound | bit;
+    int reach = 0;
 #pragma unroll
-  for (int j = 0; j < kWave; ++j) {
-    const uint32_t o = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(key), j));
-    rank += (o > key) | ((o == key) & (j < lane));
+    for (int i = 0; i < 4; ++i) reach += __popcll(__builtin_amdgcn_ballot_w64(key[i] >= t));
+    if (reach >= k) bound = t;
+    if (reach == k) break;
   }
-  const uint64_t at = __builtin_amdgcn_ballot_w64(rank == k - 1);
-  return static_cast<uint32_t>(
-      __builtin_amdgcn_readlane(static_cast<int>(key), __builtin_ctzll(at)));
+  return bound;
 }
 
 // A wave's candidate list in LDS.  top_push appends the composites of the
@@ -193,40 +212,89 @@ __device__ __forceinline__ uint32_t wave_kth(uint32_t key, int k, int lane) {
 constexpr int kTopCap = 256;
 struct TopStage {
   uint64_t e[kTopCap];
+  uint32_t group[kWave];  // the greatest groups, best first
+  int used;
 };
 struct TopList {
   int n;           // entries (uniform)
   uint64_t floor;  // composites at or below it are out (uniform)
 };
 
+// Adds to rank[c] the entries of `from` (one a lane, n of them) that are
+// greater than mine[c]: a broadcast an entry, no LDS latency.
+template <int N>
+__device__ __forceinline__ void count_greater(uint64_t from, int n, const uint64_t (&mine)[N],
+                                              int (&rank)[N]) {
+  const uint32_t lo = static_cast<uint32_t>(from), hi = static_cast<uint32_t>(from >> 32);
+  for (int j0 = 0; j0 < n; j0 += 8) {  // past the end: zeros, greater than nothing
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint64_t o = (static_cast<uint64_t>(lane_u32(hi, j0 + j)) << 32) | lane_u32(lo, j0 + j);
+#pragma unroll
+      for (int c = 0; c < N; ++c) rank[c] += o > mine[c];
+    }
+  }
+}
+
 // Cut to the min(n, k) greatest, in descending order at e[0 ..).  The rank of
 // an entry is the number of greater ones; composites are distinct.
 __device__ __forceinline__ void top_rank(TopStage& st, TopList& list, int k) {
   const int lane = threadIdx.x & (kWave - 1);
   wave_lds_fence();
-  uint64_t mine[kTopCap / kWave];
-  int rank[kTopCap / kWave];
-#pragma unroll
-  for (int c = 0; c < kTopCap / kWave; ++c) {
-    const int i = c * kWave + lane;
-    mine[c] = i < list.n ? st.e[i] : 0;
-    rank[c] = 0;
-  }
   if (list.n <= kWave) {
-    for (int j = 0; j < list.n; ++j) rank[0] += st.e[j] > mine[0];
+    const uint64_t mine[1] = {lane < list.n ? st.e[lane] : 0};
+    int rank[1] = {0};
+    count_greater<1>(mine[0], list.n, mine, rank);
+    wave_lds_fence();
+    if (lane < list.n && rank[0] < k) st.e[rank[0]] = mine[0];
   } else {
-    for (int j = 0; j < list.n; ++j) {
-      const uint64_t o = st.e[j];
+    uint64_t mine[kTopCap / kWave];
+    int rank[kTopCap / kWave];
 #pragma unroll
-      for (int c = 0; c < kTopCap / kWave; ++c) rank[c] += o > mine[c];
+    for (int c = 0; c < kTopCap / kWave; ++c) {
+      const int i = c * kWave + lane;
+      mine[c] = i < list.n ? st.e[i] : 0;
+      rank[c] = 0;
     }
-  }
-  wave_lds_fence();
+    if (list.n <= 2 * kWave) {
+      const uint64_t two[2] = {mine[0], mine[1]};
+      int r2[2] = {0, 0};
+      count_greater<2>(mine[0], kWave, two, r2);
+      count_greater<2>(mine[1], list.n - kWave, two, r2);
+      rank[0] = r2[0];
+      rank[1] = r2[1];
+    } else {
+      for (int j = 0; j < list.n; ++j) {
+        const uint64_t o = st.e[j];
 #pragma unroll
-  for (int c = 0; c < kTopCap / kWave; ++c)
-    if (c * kWave + lane < list.n && rank[c] < k) st.e[rank[c]] = mine[c];
+        for (int c = 0; c < kTopCap / kWave; ++c) rank[c] += o > mine[c];
+      }
+    }
+    wave_lds_fence();
+#pragma unroll
+    for (int c = 0; c < kTopCap / kWave; ++c)
+      if (c * kWave + lane < list.n && rank[c] < k) st.e[rank[c]] = mine[c];
+  }
   wave_lds_fence();
   if (list.n > k) list.n = k;
+}
+
+// Append count (>= 0) composites of this lane, which the caller then writes at
+// the returned place on; false, with nothing appended, when those of all lanes
+// do not fit.  The places the lanes get are in no fixed order; ranking the list
+// gives it one.
+__device__ __forceinline__ bool top_reserve(TopStage& st, TopList& list, int count, int& place) {
+  const int lane = threadIdx.x & (kWave - 1);
+  if (lane == 0) st.used = list.n;
+  wave_lds_fence();
+  place = 0;
+  if (count > 0) place = atomicAdd(&st.used, count);
+  wave_lds_fence();
+  const int n = __builtin_amdgcn_readfirstlane(st.used);
+  wave_lds_fence();
+  if (n > kTopCap) return false;
+  list.n = n;
+  return true;
 }
 
 __device__ __forceinline__ void top_push(TopStage& st, TopList& list, int k, bool want,

@@ -42,19 +42,20 @@ struct TokenOut {
 int64_t token_groups(int chunks, int64_t ntiles);
 
 // Row-major [n, T] tile statistics of the streamed logits (pw null: no
-// entropy moment) and, unless gm is null, the group maxima [n, token_groups].
+// entropy moment) and, unless gm is null, the order keys of the group maxima
+// [n, token_groups].
 void launch_token_partials(int dtype, bool vec, int chunks, const void* logits, int64_t ld,
                            int64_t n, int64_t v, const TokenView& tok, int ntiles, float* pm,
-                           float* ps, float* pw, float* gm, hipStream_t s);
+                           float* ps, float* pw, uint32_t* gm, hipStream_t s);
 
 // Merge, alternatives and outputs.  vocab_tiles: gm is the [n, T] table of
 // the LM head's 256-column tile maxima (x then holds fp32 or bf16 logits);
-// else the streamed rows' group maxima.  x null: m = 1, top_k = 0, and pt
+// else the streamed rows' keys.  x null: m = 1, top_k = 0, and pt
 // holds the token's logit.
 void launch_token_finish(int dtype, bool vec, bool vocab_tiles, const void* x, int64_t ld,
                          float inv_t, const float* pt, int64_t n, int64_t v, const TokenView& tok,
                          int ntiles, const float* pm, const float* ps, const float* pw,
-                         const float* gm, int64_t groups, int top_k, const TokenOut& out,
+                         const void* gm, int64_t groups, int top_k, const TokenOut& out,
                          hipStream_t s);
 
 // Gradient of the logits (ent null: no entropy term; grad null: zero).

@@ -27,7 +27,7 @@ namespace itl {
 
 namespace {
 
-constexpr int kPartBlock = 512;  // 8 waves, one tile each at a time
+constexpr int kPartBlock = 256;  // 4 waves, one tile each at a time
 constexpr int kPartWaves = kPartBlock / kWave;
 constexpr int kFinBlock = 256;   // 4 waves, one row each
 constexpr int kFinWaves = kFinBlock / kWave;
@@ -42,13 +42,40 @@ constexpr int64_t kMaxRowsY = 65535;
 // so the split changes no bit.
 // ---------------------------------------------------------------------------
 
+// The maxima over each row of 16 lanes of C values, in every lane: xor 1, xor 2,
+// half mirror, mirror, each one vector maximum that takes its partner through
+// DPP (the compiler's own form is a move, a wait, a quieting and a maximum).
+// The leading s_nop covers the wait that a DPP read needs after the write of
+// its source; C values in turn cover the steps after it as well.
+#define ITL_ROW_MAX_STEP(CTRL)                                                                 \
+  if constexpr (C % 4 == 0) {                                                                  \
+    _Pragma("unroll") for (int j = 0; j < C; j += 4) asm(                                      \
+        "s_nop 1\n\tv_max_f32_dpp %0, %0, %0 " CTRL " row_mask:0xf bank_mask:0xf\n\t"          \
+        "v_max_f32_dpp %1, %1, %1 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                     \
+        "v_max_f32_dpp %2, %2, %2 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                     \
+        "v_max_f32_dpp %3, %3, %3 " CTRL " row_mask:0xf bank_mask:0xf"                         \
+        : "+v"(g[j]), "+v"(g[j + 1]), "+v"(g[j + 2]), "+v"(g[j + 3]));                         \
+  } else {                                                                                     \
+    _Pragma("unroll") for (int j = 0; j < C; ++j) asm(                                         \
+        "s_nop 1\n\tv_max_f32_dpp %0, %0, %0 " CTRL " row_mask:0xf bank_mask:0xf"              \
+        : "+v"(g[j]));                                                                         \
+  }
+template <int C>
+__device__ __forceinline__ void row16_max(float (&g)[C]) {
+  ITL_ROW_MAX_STEP("quad_perm:[1,0,3,2]")
+  ITL_ROW_MAX_STEP("quad_perm:[2,3,0,1]")
+  ITL_ROW_MAX_STEP("row_half_mirror")
+  ITL_ROW_MAX_STEP("row_mirror")
+}
+#undef ITL_ROW_MAX_STEP
+
 // tile_stats of logp_device.h (same sum tree, same bits; rows of any
 // alignment in 16-byte loads) that, with TOP, also leaves the maxima of the
 // tile's C * 4 groups in gm: the maximum is exact in any order, so it is taken
 // along the groups first (four lane moves a chunk), then over the chunks, then
 // over the four rows of 16 lanes.
 template <typename T, int C, bool VEC, bool ENT, bool TOP>
-__device__ __forceinline__ void token_tile_stats(const T* row, int64_t col0, int64_t v, float* gm,
+__device__ __forceinline__ void token_tile_stats(const T* row, int64_t col0, int64_t v, uint32_t* gm,
                                                   float& m_out, float& s_out, float& w_out) {
   constexpr int E = Elt<T>::kPerChunk;
   constexpr int W = C * kWave * E;
@@ -63,25 +90,24 @@ __device__ __forceinline__ void token_tile_stats(const T* row, int64_t col0, int
     for (int j = 0; j < C; ++j)
       load_row_chunk<T, VEC>(row, col0 + static_cast<int64_t>(j * kWave + lane) * E, v, x[j]);
   }
-  float m = -INFINITY, mine = -INFINITY;
+  float g[C];
 #pragma unroll
   for (int j = 0; j < C; ++j) {
-    float g = x[j][0];
+    g[j] = x[j][0];
 #pragma unroll
-    for (int e = 1; e < E; ++e) g = fmaxf(g, x[j][e]);
-    if constexpr (TOP) {
-      g = fmaxf(g, dpp_mov<kDppXor1>(g));
-      g = fmaxf(g, dpp_mov<kDppXor2>(g));
-      g = fmaxf(g, dpp_mov<kDppRowHalfMirror>(g));
-      g = fmaxf(g, dpp_mov<kDppRowMirror>(g));
-      mine = (lane & 15) == j ? g : mine;
-    }
-    m = fmaxf(m, g);
+    for (int e = 1; e < E; ++e) g[j] = fmaxf(g[j], x[j][e]);
+  }
+  if constexpr (TOP) row16_max<C>(g);
+  float m = g[0], mine = g[0];
+#pragma unroll
+  for (int j = 1; j < C; ++j) {
+    m = fmaxf(m, g[j]);
+    if constexpr (TOP) mine = (lane & 15) == j ? g[j] : mine;
   }
   constexpr bool kLds = C * E > 16;  // where the partners come from: as tile_stats
   if constexpr (TOP) {
     // lane (row r16, place j < C) stores group 4 j + r16 (ascending columns)
-    if ((lane & 15) < C) gm[(lane & 15) * 4 + (lane >> 4)] = mine;
+    if ((lane & 15) < C) gm[(lane & 15) * 4 + (lane >> 4)] = order_key(mine);
     m = swap_combine16(m, true);
     m = swap_combine32(m, true);
   } else {
@@ -110,7 +136,7 @@ template <typename T, int C, bool VEC, bool ENT, bool TOP>
 __global__ __launch_bounds__(kPartBlock) void token_partials_kernel(
     const T* __restrict__ logits, int64_t ld, int64_t n, int64_t v, TokenView tok, int ntiles,
     int segs, int tiles_per_seg, float* __restrict__ pm, float* __restrict__ ps,
-    float* __restrict__ pw, float* __restrict__ gm) {
+    float* __restrict__ pw, uint32_t* __restrict__ gm) {
   constexpr int W = C * kWave * Elt<T>::kPerChunk;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int lane = threadIdx.x % kWave;
@@ -136,122 +162,258 @@ __global__ __launch_bounds__(kPartBlock) void token_partials_kernel(
 }
 
 // ---------------------------------------------------------------------------
-// Finish: one wave a row merges the tile statistics (merge_lse_t: the bits of
-// logp_fwd), ranks the alternatives and writes every output of the row.
+// Finish.  One wave a row merges the tile statistics (merge_lse_t: the bits of
+// logp_fwd) and writes lse, entropy and the given tokens; with alternatives it
+// then selects them, or, with few rows (per = 2), a second wave does so
+// meanwhile and takes the lse at the end.
 //   x          the row's logits ([n, ld], row r at x + r * ld), or null: then
 //              M = 1, k = 0 and the token's logit is pt[r].
-//   inv_t      factor on the logits read from x (the tables hold scaled ones).
-//   gm         group maxima of row r at gm + r * groups, group g = columns
-//              [g * LPG * E, + LPG * E).
+//   gm         what orders the groups of row r, at gm + r * groups: the order
+//              keys of their maxima, or with HEAD the maxima themselves (the
+//              LM head's tile table).  Group g = columns [g GW, g GW + GW).
+//   inv_t      HEAD: factor on the logits read from x (the tables hold scaled
+//              ones).
+// Latency is what counts: a row is a chain of a few dependent loads, so all
+// loads of a stage are in flight together, and what is executed is kept short
+// (code that runs once is bound by its fetch): a lane marks its candidates in a
+// bit mask and reads the few marked ones again instead of carrying an unrolled
+// append.
 // ---------------------------------------------------------------------------
-template <typename T, int LPG, bool VEC, bool ENT>
+constexpr int kKeys = 20;  // groups a lane holds at once
+
+// Order keys of the groups b0 + 64 c + lane; 0 (below every key) past the last.
+template <bool HEAD>
+__device__ __forceinline__ uint32_t group_key(const uint32_t* g, int64_t i) {
+  return HEAD ? order_key(__uint_as_float(g[i])) : g[i];
+}
+template <bool HEAD>
+__device__ __forceinline__ void load_keys(const uint32_t* g, int64_t b0, int64_t groups, int lane,
+                                          uint32_t (&key)[kKeys]) {
+#pragma unroll
+  for (int c = 0; c < kKeys; ++c) {
+    const int64_t i = b0 + c * kWave + lane;
+    key[c] = g[i < groups ? i : 0];
+  }
+#pragma unroll
+  for (int c = 0; c < kKeys; ++c) {
+    const uint32_t k = HEAD ? order_key(__uint_as_float(key[c])) : key[c];
+    key[c] = b0 + c * kWave + lane < groups ? k : 0u;
+  }
+}
+
+// The select wave's part: the row's top_k greatest values, in order, as
+// composites at st.e[0 ..).  Returns when they are in LDS.
+template <typename T, int GW, bool VEC, bool HEAD>
+__device__ __forceinline__ void select_top(TopStage& st, const T* row, float inv_t, uint32_t v,
+                                           const uint32_t* g, int64_t groups, int top_k,
+                                           uint32_t (&key)[kKeys], int lane) {
+  constexpr int E = Elt<T>::kPerChunk;
+  constexpr int LPG = GW / E;            // lanes per group
+  constexpr int GPW = kWave / LPG;       // groups one wave load covers
+  constexpr int U = 8;                   // such loads in flight: 32, 16 or 8 groups
+  auto logit = [&](uint32_t c) {
+    const float z = Elt<T>::load(row, c);
+    return HEAD ? z * inv_t : z;
+  };
+  // 1. A bound: the k-th greatest of 256 maxima, four a lane, over disjoint
+  // sets of groups.  At least k groups reach it.
+  const bool one_block = groups <= kKeys * kWave;
+  uint32_t best[4] = {0, 0, 0, 0};
+  for (int64_t b0 = 0; b0 < groups; b0 += kKeys * kWave) {
+    if (b0 > 0) load_keys<HEAD>(g, b0, groups, lane, key);
+#pragma unroll
+    for (int c = 0; c < kKeys; ++c) best[c % 4] = max(best[c % 4], key[c]);
+  }
+  const uint32_t bound = max(wave_bound(best, top_k), 1u);
+  // 2. The k greatest groups (or all, when there are fewer).  Few groups
+  // reach the bound; the list is only cut in between when more than it holds
+  // do (plateaus), in a second walk.
+  TopList list{0, 0};
+  int reach = 0, place = 0;
+  if (one_block) {
+#pragma unroll
+    for (int c = 0; c < kKeys; ++c) reach += key[c] >= bound;
+  }
+  if (one_block && top_reserve(st, list, reach, place)) {
+#pragma unroll
+    for (int c = 0; c < kKeys; ++c)
+      if (key[c] >= bound)
+        st.e[place++] = compose(key[c], static_cast<uint32_t>(c * kWave + lane));
+  } else {
+    for (int64_t c0 = 0; c0 < groups; c0 += kWave) {
+      const int64_t c = c0 + lane;
+      const uint32_t one = c < groups ? group_key<HEAD>(g, c) : 0u;
+      top_push(st, list, top_k, one >= bound, compose(one, static_cast<uint32_t>(c)));
+    }
+  }
+  top_rank(st, list, top_k);
+  const int ng = list.n;
+  // a value below the k-th group's maximum is none of the k greatest
+  const uint64_t last = st.e[ng - 1];
+  const float floor_x = ng == top_k ? order_value(static_cast<uint32_t>(last >> 32)) : -INFINITY;
+  st.group[lane] = compose_index(st.e[lane < ng ? lane : 0]);
+  wave_lds_fence();
+  // 3. The values that are not below it: a register block of groups at a
+  // time while the list holds them, else value by value.
+  list = TopList{0, 0};
+  bool fits = true;
+  for (int b0 = 0; b0 < ng && fits; b0 += GPW * U) {
+    uint64_t mark = 0;
+    auto column = [&](int u) {
+      const int b = b0 + u * GPW + lane / LPG;
+      return b < ng ? min(st.group[b] * GW + (lane % LPG) * E, v) : v;
+    };
+    // Whole chunks (all but the row's last one) load without a branch, all
+    // of them in flight together.
+    bool part = false;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t c = column(u);
+      part |= c < v && v - c < E;
+    }
+    if (__builtin_amdgcn_ballot_w64(part) == 0 && v >= E) {
+      uint4 q[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const uint32_t c = column(u);
+        q[u] = load_whole_chunk<T, VEC>(row + (c < v ? c : 0));
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float xv[E];
+        widen_chunk<T>(q[u], xv);
+        uint32_t m = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          m |= (HEAD ? xv[e] * inv_t : xv[e]) < floor_x ? 0u : 1u << e;
+        if (column(u) >= v) m = 0;  // no such group, or past the row's end
+        mark |= static_cast<uint64_t>(m) << (u * E);
+      }
+    } else {
+#pragma unroll 1
+      for (int u = 0; u < U; ++u)
+#pragma unroll 1
+        for (int e = 0; e < E; ++e) {
+          const uint32_t c = column(u) + e;
+          if (c < v && c >= column(u) && !(logit(c) < floor_x)) mark |= uint64_t{1} << (u * E + e);
+        }
+    }
+    fits = top_reserve(st, list, __popcll(mark), place);
+    while (fits && mark) {
+      const int i = __builtin_ctzll(mark);
+      mark &= mark - 1;
+      const uint32_t c = column(i / E) + i % E;
+      st.e[place++] = compose(order_key(logit(c)), c);
+    }
+  }
+  if (!fits) {
+    list = TopList{0, 0};
+    for (int b = 0; b < ng; ++b) {
+      const uint32_t c0 = st.group[b] * GW;
+      for (int o = 0; o < GW; o += kWave) {
+        const uint32_t c = c0 + o + lane;
+        const float z = c < v ? logit(c) : 0.0f;
+        top_push(st, list, top_k, c < v && !(z < floor_x),
+                 compose(order_key(z), c));
+      }
+    }
+  }
+  top_rank(st, list, top_k);
+}
+
+template <typename T, int GW, bool VEC, bool ENT, bool HEAD>
 __global__ __launch_bounds__(kFinBlock) void token_finish_kernel(
     const T* __restrict__ x, int64_t ld, float inv_t, const float* __restrict__ pt, int64_t n,
     int64_t v, TokenView tok, int ntiles, const float* __restrict__ pm,
-    const float* __restrict__ ps, const float* __restrict__ pw, const float* __restrict__ gm,
-    int64_t groups, int top_k, TokenOut out) {
-  constexpr int E = Elt<T>::kPerChunk;
-  constexpr int GW = LPG * E;            // columns per group
-  constexpr int GPW = kWave / LPG;       // groups one wave load covers
-  __shared__ MergeStage merge[kFinWaves];
-  __shared__ TopStage top[kFinWaves];
+    const float* __restrict__ ps, const float* __restrict__ pw, const uint32_t* __restrict__ gm,
+    int64_t groups, int top_k, int per, TokenOut out) {
+  __shared__ union {
+    MergeStage merge;
+    TopStage top;
+  } stage[kFinWaves];
+  __shared__ float row_lse[kFinWaves];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int lane = threadIdx.x % kWave;
-  TopStage& st = top[wave];
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * kFinWaves + wave; r < n;
-       r += static_cast<int64_t>(gridDim.x) * kFinWaves) {
-    if (!row_active(tok, r, lane)) {
-      for (int64_t i = lane; i < tok.m; i += kWave) out.logp[r * tok.m + i] = 0.0f;
-      if (lane < top_k) {
-        out.top_logp[r * top_k + lane] = 0.0f;
-        out.top_ids[r * top_k + lane] = -1;
-      }
-      if (lane == 0) {
-        if (out.lse) out.lse[r] = 0.0f;
-        if constexpr (ENT) out.ent[r] = 0.0f;
-      }
-      continue;
-    }
-    float h = 0.0f;
-    const int64_t at = r * ntiles;
-    const float L = merge_lse_t<ENT, 4>(pm + at, ps + at, pw + at, ntiles, 1, merge[wave], &h);
-    if (lane == 0) {
-      if (out.lse) out.lse[r] = L;
-      if constexpr (ENT) out.ent[r] = h;
-    }
+  const int rows = kFinWaves / per;        // rows a workgroup
+  const int slot = wave / per;
+  const bool merges = wave % per == 0, selects = top_k > 0 && wave % per == per - 1;
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * rows; r0 < n;
+       r0 += static_cast<int64_t>(gridDim.x) * rows) {
+    const int64_t r = r0 + slot;
+    bool live = r < n;
+    // The group keys or the given tokens are on their way first.
+    uint32_t key[kKeys];
+    const uint32_t* g = gm + r * groups;
+    if (live && selects) load_keys<HEAD>(g, 0, groups, lane, key);
+    int64_t t0 = live && lane < tok.m ? tok.at(r, lane) : tok.ignore;
+    if (live && tok.m > 0 && __builtin_amdgcn_ballot_w64(t0 != tok.ignore) == 0)
+      live = row_active(tok, r, lane);
     const T* row = x + r * ld;
-    for (int64_t i = lane; i < tok.m; i += kWave) {
-      const int64_t t = tok.at(r, i);
-      float lp = 0.0f;
-      if (t != tok.ignore) {
-        const bool valid = t >= 0 && t < v;
-        const float xt = !valid ? 0.0f : x ? Elt<T>::load(row, t) * inv_t : pt[r];
-        lp = combine(xt, L, valid);
-      }
-      out.logp[r * tok.m + i] = lp;
-    }
-    if (top_k == 0) continue;
-
-    // 1. A bound: the k-th greatest of the 64 lanes' own greatest groups.  At
-    // least k groups reach it.
-    const float* g = gm + r * groups;
-    uint32_t best = 0;
-    for (int64_t c = lane; c < groups; c += kWave) best = max(best, order_key(g[c]));
-    const uint32_t bound = wave_kth(best, top_k, lane);
-    // 2. The k greatest groups (or all, when there are fewer).
-    TopList list{0, 0};
-    for (int64_t c0 = 0; c0 < groups; c0 += kWave) {
-      const int64_t c = c0 + lane;
-      const uint32_t key = c < groups ? order_key(g[c]) : 0u;
-      top_push(st, list, top_k, c < groups && key >= bound, compose(key, static_cast<uint32_t>(c)));
-    }
-    top_rank(st, list, top_k);
-    const int ng = list.n;
-    const uint64_t mine = lane < ng ? st.e[lane] : 0;
-    const uint32_t floor_key = ng == top_k ? static_cast<uint32_t>(st.e[ng - 1] >> 32) : 0u;
-    wave_lds_fence();
-    const int gid = static_cast<int>(compose_index(mine));
-    // 3. Their values that reach the k-th group's maximum, four loads ahead.
-    list = TopList{0, 0};
-    constexpr int U = 4;
-    for (int b0 = 0; b0 < ng; b0 += GPW * U) {
-      float xv[U][E];
-      int64_t col[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int b = b0 + u * GPW + lane / LPG;
-        const int gi = __shfl(gid, b < ng ? b : 0, kWave);
-        col[u] = b < ng ? static_cast<int64_t>(gi) * GW + (lane % LPG) * E : v;
-        load_row_chunk<T, VEC>(row, col[u], v, xv[u]);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const uint32_t key = order_key(xv[u][e] * inv_t);
-          top_push(st, list, top_k, col[u] + e < v && key >= floor_key,
-                   compose(key, static_cast<uint32_t>(col[u] + e)));
+    if (!live) {
+      if (r < n && merges) {  // a padding row
+        for (int64_t i = lane; i < tok.m; i += kWave) out.logp[r * tok.m + i] = 0.0f;
+        if (lane == 0) {
+          if (out.lse) out.lse[r] = 0.0f;
+          if constexpr (ENT) out.ent[r] = 0.0f;
         }
+      }
     }
-    top_rank(st, list, top_k);
-    if (lane < top_k) {
-      const uint64_t c = st.e[lane];
-      out.top_logp[r * top_k + lane] = order_value(static_cast<uint32_t>(c >> 32)) - L;
-      out.top_ids[r * top_k + lane] = static_cast<int64_t>(compose_index(c));
+    if (live && merges) {
+      auto logit = [&](int64_t c) {
+        const float z = Elt<T>::load(row, c);
+        return HEAD ? z * inv_t : z;
+      };
+      float x0 = 0.0f;
+      if (t0 != tok.ignore && t0 >= 0 && t0 < v) x0 = x ? logit(t0) : pt[r];
+      float h = 0.0f;
+      const int64_t at = r * ntiles;
+      const float L = merge_lse_t<ENT, HEAD ? 10 : 1>(pm + at, ps + at, pw + at, ntiles, 1,
+                                                      stage[wave].merge, &h);
+      if (lane == 0) {
+        row_lse[slot] = L;
+        if (out.lse) out.lse[r] = L;
+        if constexpr (ENT) out.ent[r] = h;
+      }
+      for (int64_t i = lane; i < tok.m; i += kWave) {
+        if (i >= kWave) {
+          t0 = tok.at(r, i);
+          x0 = t0 != tok.ignore && t0 >= 0 && t0 < v ? logit(t0) : 0.0f;
+        }
+        out.logp[r * tok.m + i] = t0 == tok.ignore ? 0.0f : combine(x0, L, t0 >= 0 && t0 < v);
+      }
     }
+    if (live && selects) {
+      wave_lds_fence();
+      select_top<T, GW, VEC, HEAD>(stage[wave].top, row, inv_t, static_cast<uint32_t>(v), g,
+                                   groups, top_k, key, lane);
+    }
+    if (per == 2) __syncthreads();  // the row's lse
+    if (selects && r < n && lane < top_k) {
+      const uint64_t c = stage[wave].top.e[lane];
+      out.top_logp[r * top_k + lane] =
+          live ? order_value(static_cast<uint32_t>(c >> 32)) - row_lse[slot] : 0.0f;
+      out.top_ids[r * top_k + lane] = live ? static_cast<int64_t>(compose_index(c)) : -1;
+    }
+    if (per == 2) __syncthreads();  // before the stages are taken again
     wave_lds_fence();
   }
 }
 
 // ---------------------------------------------------------------------------
-// Gradient of the logits.  Thread (x, tid) owns one 16-byte chunk of every
-// row it visits, as logp_bwd_kernel does, so the launch streams the matrix in
-// address order.  The row's entries (given tokens, then alternatives) come in
-// 64 at a time, one a lane: every wave adds their gradients to G in one fixed
-// tree, and a ballot picks the entries inside the wave's own 64 chunks, whose
-// gradients go to their element in ascending entry order.  No LDS, no barrier,
-// no atomics; an entry that occurs twice is added twice.
+// Gradient of the logits.  A wave owns kBwdChunks * 64 neighbouring 16-byte
+// chunks of a row (lane l chunks l, l + 64, ...), so a launch streams the
+// matrix in address order.  The row's entries (given tokens, then
+// alternatives) come in 64 at a time, one a lane: every wave adds their
+// gradients to G in one fixed tree, and a ballot picks the entries inside the
+// wave's own columns, whose gradients go to their element in ascending entry
+// order.  No LDS, no barrier, no atomics; an entry that occurs twice is added
+// twice.
+// Bound by memory, but a wave first has to know that its row is no padding:
+// the entries' load, then the logits' (several chunks a lane, so that the wait
+// for the entries is shared), and G is summed while the logits arrive.
 // ---------------------------------------------------------------------------
+constexpr int kBwdChunks = 4;
+
 template <typename T, bool VEC, bool ENT>
 __global__ __launch_bounds__(kFinBlock) void token_bwd_kernel(
     const T* logits, int64_t ld, int64_t n, int64_t v, TokenView tok, TopView alt,
@@ -259,29 +421,55 @@ __global__ __launch_bounds__(kFinBlock) void token_bwd_kernel(
     const float* __restrict__ grad_top, const float* __restrict__ ent,
     const float* __restrict__ gent, T* dlogits, int64_t ld_out) {
   constexpr int E = Elt<T>::kPerChunk;
+  constexpr int NC = kBwdChunks;
+  constexpr int kSpan = NC * kWave * E;  // columns of a wave
   const int lane = threadIdx.x % kWave;
-  const int64_t wave0 =
-      (static_cast<int64_t>(blockIdx.x) * kFinBlock +
-       __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * kWave) * E;  // the wave's first column
+  const int64_t wave0 = (static_cast<int64_t>(blockIdx.x) * kFinWaves +
+                         __builtin_amdgcn_readfirstlane(threadIdx.x / kWave)) * kSpan;
   if (wave0 >= v) return;
-  const int64_t j0 = wave0 + lane * E;
-  const int64_t entries = tok.m + alt.k;
+  const int entries = static_cast<int>(tok.m + alt.k);
   for (int64_t rr = blockIdx.y; rr < n; rr += gridDim.y) {
     const int64_t r = n - 1 - rr;  // last to first: what the forward read last may still be cached
-    const bool active = row_active(tok, r, lane);
-    float x[E], u[E];
+    int64_t col = -1;
+    float g = 0.0f;
+    if (lane < entries) entry_at(tok, alt, grad, grad_top, r, lane, col, g);
+    const float L = lse[r];
+    const float H = ENT ? ent[r] : 0.0f, ngh = ENT ? -gent[r] : 0.0f;
+    // an ignored entry has col = -1; so may an invalid token, hence the rest
+    const bool active = __builtin_amdgcn_ballot_w64(lane < tok.m && col != -1) != 0 ||
+                        row_active(tok, r, lane);
+    const bool whole = wave0 + kSpan <= v;
+    const T* row = logits + r * ld + wave0 + lane * E;
+    T* drow = dlogits + r * ld_out + wave0 + lane * E;
+    uint4 q[NC];
+    float u[NC][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) u[e] = 0.0f;
-    float G = 0.0f;
+    for (int c = 0; c < NC; ++c) {
+      q[c] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int e = 0; e < E; ++e) u[c][e] = 0.0f;
+    }
     if (active) {
-      load_row_chunk<T, VEC>(logits + r * ld, j0, v, x);
-      for (int64_t i0 = 0; i0 < entries; i0 += kWave) {
-        const int64_t i = i0 + lane;
-        int64_t col = -1;
-        float g = 0.0f;
-        if (i < entries) entry_at(tok, alt, grad, grad_top, r, i, col, g);
+      if (whole) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) q[c] = load_whole_chunk<T, VEC>(row + c * kWave * E);
+      } else {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+          float x[E];
+          load_row_chunk<T, VEC>(row, c * kWave * E, v - wave0 - lane * E, x);
+          q[c] = round_chunk<T>(x);  // exact: the values are of type T
+        }
+      }
+      float G = 0.0f;
+      for (int i0 = 0; i0 < entries; i0 += kWave) {
+        if (i0 > 0) {
+          col = -1;
+          g = 0.0f;
+          if (i0 + lane < entries) entry_at(tok, alt, grad, grad_top, r, i0 + lane, col, g);
+        }
         G = G + wave_sum(g);
-        uint64_t hits = __builtin_amdgcn_ballot_w64(col >= wave0 && col < wave0 + kWave * E);
+        uint64_t hits = __builtin_amdgcn_ballot_w64(col >= wave0 && col < wave0 + kSpan);
         const int off = static_cast<int>(col - wave0);
         while (hits) {
           const int b = __builtin_ctzll(hits);
@@ -289,15 +477,29 @@ __global__ __launch_bounds__(kFinBlock) void token_bwd_kernel(
           const int o = __builtin_amdgcn_readlane(off, b);
           const float gb = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(g), b));
 #pragma unroll
-          for (int e = 0; e < E; ++e) u[e] = o == lane * E + e ? u[e] + gb : u[e];
+          for (int c = 0; c < NC; ++c)
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+              u[c][e] = o == (c * kWave + lane) * E + e ? u[c][e] + gb : u[c][e];
         }
       }
-      const float L = lse[r], ng = -G;
-      const float H = ENT ? ent[r] : 0.0f, ngh = ENT ? -gent[r] : 0.0f;
 #pragma unroll
-      for (int e = 0; e < E; ++e) u[e] = token_grad<ENT>(x[e] - L, u[e], ng, H, ngh);
+      for (int c = 0; c < NC; ++c) {
+        float x[E];
+        widen_chunk<T>(q[c], x);
+#pragma unroll
+        for (int e = 0; e < E; ++e) u[c][e] = token_grad<ENT>(x[e] - L, u[c][e], -G, H, ngh);
+      }
     }
-    store_row_chunk<T, VEC>(dlogits + r * ld_out, j0, v, u);
+    if (whole) {
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        store_whole_chunk<T, VEC>(drow + c * kWave * E, round_chunk<T>(u[c]));
+    } else {
+#pragma unroll
+      for (int c = 0; c < NC; ++c)
+        store_row_chunk<T, VEC>(drow, c * kWave * E, v - wave0 - lane * E, u[c]);
+    }
   }
 }
 
@@ -385,7 +587,7 @@ unsigned clamp_grid(int64_t blocks) {
 
 template <typename T, int C, bool VEC>
 void partials_typed(const void* logits, int64_t ld, int64_t n, int64_t v, const TokenView& tok,
-                    int ntiles, int segs, int tps, float* pm, float* ps, float* pw, float* gm,
+                    int ntiles, int segs, int tps, float* pm, float* ps, float* pw, uint32_t* gm,
                     hipStream_t s) {
   auto kern = gm ? (pw ? token_partials_kernel<T, C, VEC, true, true>
                        : token_partials_kernel<T, C, VEC, false, true>)
@@ -399,7 +601,7 @@ void partials_typed(const void* logits, int64_t ld, int64_t n, int64_t v, const 
 template <typename T, bool VEC>
 void partials_chunks(int chunks, const void* logits, int64_t ld, int64_t n, int64_t v,
                      const TokenView& tok, int ntiles, int segs, int tps, float* pm, float* ps,
-                     float* pw, float* gm, hipStream_t s) {
+                     float* pw, uint32_t* gm, hipStream_t s) {
   switch (chunks) {
     case 1: return partials_typed<T, 1, VEC>(logits, ld, n, v, tok, ntiles, segs, tps, pm, ps, pw, gm, s);
     case 2: return partials_typed<T, 2, VEC>(logits, ld, n, v, tok, ntiles, segs, tps, pm, ps, pw, gm, s);
@@ -409,16 +611,20 @@ void partials_chunks(int chunks, const void* logits, int64_t ld, int64_t n, int6
   }
 }
 
-template <typename T, int LPG, bool VEC>
+template <typename T, int GW, bool VEC, bool HEAD>
 void finish_typed(const void* x, int64_t ld, float inv_t, const float* pt, int64_t n, int64_t v,
                   const TokenView& tok, int ntiles, const float* pm, const float* ps,
-                  const float* pw, const float* gm, int64_t groups, int top_k, const TokenOut& out,
+                  const float* pw, const void* gm, int64_t groups, int top_k, const TokenOut& out,
                   hipStream_t s) {
-  auto kern = out.ent ? token_finish_kernel<T, LPG, VEC, true>
-                      : token_finish_kernel<T, LPG, VEC, false>;
-  hipLaunchKernelGGL(kern, dim3(clamp_grid((n + kFinWaves - 1) / kFinWaves)), dim3(kFinBlock), 0,
-                     s, static_cast<const T*>(x), ld, inv_t, pt, n, v, tok, ntiles, pm, ps,
-                     pw ? pw : ps, gm, groups, top_k, out);
+  auto kern = out.ent ? token_finish_kernel<T, GW, VEC, true, HEAD>
+                      : token_finish_kernel<T, GW, VEC, false, HEAD>;
+  // Two waves a row while the GPU has waves to spare: a latency of 14 instead of
+  // 20 us for 16 rows of the LM head, but 36 instead of 30 us for 4096 rows.
+  const int per = top_k > 0 && n <= 8 * static_cast<int64_t>(xcd_cus()) * 2 ? 2 : 1;
+  const int64_t rows = kFinWaves / per;
+  hipLaunchKernelGGL(kern, dim3(clamp_grid((n + rows - 1) / rows)), dim3(kFinBlock), 0, s,
+                     static_cast<const T*>(x), ld, inv_t, pt, n, v, tok, ntiles, pm, ps,
+                     pw ? pw : ps, static_cast<const uint32_t*>(gm), groups, top_k, per, out);
 }
 
 }  // namespace
@@ -427,7 +633,7 @@ int64_t token_groups(int chunks, int64_t ntiles) { return ntiles * chunks * 4; }
 
 void launch_token_partials(int dtype, bool vec, int chunks, const void* logits, int64_t ld,
                            int64_t n, int64_t v, const TokenView& tok, int ntiles, float* pm,
-                           float* ps, float* pw, float* gm, hipStream_t s) {
+                           float* ps, float* pw, uint32_t* gm, hipStream_t s) {
   // Segments: enough (row, segment) items for the GPU, each at least one
   // round of the workgroup's eight waves.
   const int most = (ntiles + kPartWaves - 1) / kPartWaves;
@@ -449,22 +655,22 @@ void launch_token_partials(int dtype, bool vec, int chunks, const void* logits, 
 void launch_token_finish(int dtype, bool vec, bool vocab_tiles, const void* x, int64_t ld,
                          float inv_t, const float* pt, int64_t n, int64_t v, const TokenView& tok,
                          int ntiles, const float* pm, const float* ps, const float* pw,
-                         const float* gm, int64_t groups, int top_k, const TokenOut& out,
+                         const void* gm, int64_t groups, int top_k, const TokenOut& out,
                          hipStream_t s) {
-#define ITL_FIN(T, LPG)                                                                          \
-  vec ? finish_typed<T, LPG, true>(x, ld, inv_t, pt, n, v, tok, ntiles, pm, ps, pw, gm, groups,  \
-                                   top_k, out, s)                                                \
-      : finish_typed<T, LPG, false>(x, ld, inv_t, pt, n, v, tok, ntiles, pm, ps, pw, gm, groups, \
-                                    top_k, out, s)
-  // a group is 16 lanes' chunks of a streamed row, or a 256-column vocabulary
-  // tile of the LM head (fp32: 64 lanes, bf16: 32)
+#define ITL_FIN(T, GW, HEAD)                                                                     \
+  vec ? finish_typed<T, GW, true, HEAD>(x, ld, inv_t, pt, n, v, tok, ntiles, pm, ps, pw, gm,     \
+                                        groups, top_k, out, s)                                   \
+      : finish_typed<T, GW, false, HEAD>(x, ld, inv_t, pt, n, v, tok, ntiles, pm, ps, pw, gm,    \
+                                         groups, top_k, out, s)
+  // a group is 16 lanes' chunks of a streamed row, or a vocabulary tile of the
+  // LM head
   if (vocab_tiles) {
-    if (dtype == kF32) ITL_FIN(float, 64);
-    else ITL_FIN(uint16_t, 32);
+    if (dtype == kF32) ITL_FIN(float, kLinearTile, true);
+    else ITL_FIN(uint16_t, kLinearTile, true);
   } else {
-    if (dtype == kF32) ITL_FIN(float, 16);
-    else if (dtype == kF16) ITL_FIN(_Float16, 16);
-    else ITL_FIN(uint16_t, 16);
+    if (dtype == kF32) ITL_FIN(float, 64, false);
+    else if (dtype == kF16) ITL_FIN(_Float16, 128, false);
+    else ITL_FIN(uint16_t, 128, false);
   }
 #undef ITL_FIN
 }
@@ -474,8 +680,8 @@ void launch_token_bwd(int dtype, bool vec, const void* logits, int64_t ld, int64
                       const float* grad, const float* grad_top, const float* ent,
                       const float* gent, void* dlogits, int64_t ld_out, hipStream_t s) {
   const int64_t per = dtype == kF32 ? 4 : 8;
-  const int64_t chunks = (v + per - 1) / per;
-  const dim3 grid(static_cast<unsigned>((chunks + kFinBlock - 1) / kFinBlock),
+  const int64_t chunks = (v + per - 1) / per, block = kFinBlock * kBwdChunks;
+  const dim3 grid(static_cast<unsigned>((chunks + block - 1) / block),
                   static_cast<unsigned>(n < kMaxRowsY ? n : kMaxRowsY));
 #define ITL_BWD(T)                                                                              \
   do {                                                                                          \
