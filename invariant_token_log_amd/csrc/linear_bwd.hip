@@ -523,6 +523,53 @@ __global__ __launch_bounds__(gemm::kThreads) void gemm_out_kernel(
                                               C, ldc);
 }
 
+// One product of a paired launch: gemm_out_kernel's arguments.
+struct GemmArgs {
+  const uint16_t* A;
+  int64_t lda, arows;
+  int a_kvalid;
+  const uint16_t* B;
+  int64_t ldb, brows;
+  int b_kvalid, ksteps, mblocks, nblocks;
+  int64_t m_out, n_out;
+  const float* Cin;
+  int64_t ldcin;
+  void* C;
+  int64_t ldc;
+};
+
+template <bool BF16OUT, int AF, int BF>
+__device__ __forceinline__ void gemm_pair_tile(gemm::Stages& st, const GemmArgs& g, int tile) {
+  int mb, nb;
+  gemm::tile_coords(gemm::xcd_logical(tile, g.mblocks * g.nblocks), g.mblocks, g.nblocks, mb, nb);
+  const int64_t m0 = static_cast<int64_t>(mb) * kT, n0 = static_cast<int64_t>(nb) * kT;
+  if (gemm::loader_wave())
+    gemm_out_tile<BF16OUT, true, AF, BF>(st, g.A, g.lda, g.arows, g.a_kvalid, g.B, g.ldb, g.brows,
+                                         g.b_kvalid, g.ksteps, m0, n0, g.m_out, g.n_out, g.Cin,
+                                         g.ldcin, g.C, g.ldc);
+  else
+    gemm_out_tile<BF16OUT, false, AF, BF>(st, g.A, g.lda, g.arows, g.a_kvalid, g.B, g.ldb, g.brows,
+                                          g.b_kvalid, g.ksteps, m0, n0, g.m_out, g.n_out, g.Cin,
+                                          g.ldcin, g.C, g.ldc);
+}
+
+// A chunk's two products in one launch, dh's tiles first: the same tiles, K
+// walks and bits as two launches.  dh has few, long tiles (K = the chunk's
+// columns); when they leave CUs idle, dW's many short ones run there
+// meanwhile.  At N = 2048, H = 4096 (128 dh tiles on 256 CUs) a chunk's
+// products take 990 us apart; with 256 dh tiles and more, both fill the GPU by
+// themselves and a paired launch measured the same.
+template <bool BF16DH, bool BF16DW, int DHB>
+__global__ __launch_bounds__(gemm::kThreads) void gemm_pair_kernel(GemmArgs dh, GemmArgs dw,
+                                                                   int dh_tiles) {
+  __shared__ __align__(16) gemm::Stages st;
+  const int b = blockIdx.x;
+  if (b < dh_tiles)
+    gemm_pair_tile<BF16DH, gemm::kKContig, DHB>(st, dh, b);
+  else
+    gemm_pair_tile<BF16DW, gemm::kKOuterBlocked, gemm::kKContig>(st, dw, b - dh_tiles);
+}
+
 // Zero rows x cols of C (a sum over no tokens).
 template <bool BF16OUT>
 __global__ __launch_bounds__(256) void fill_zero_kernel(void* C, int64_t ldc, int64_t rows,
@@ -683,34 +730,52 @@ void launch_linear_bwd(const uint16_t* hidden, int64_t ld_h, const uint16_t* wei
     if (tokens) launch_token_dz(*tokens, n, v, inv_t, ent, gent, c0, cols, dz, s);
     // dW[c0, c1) = dz_c^T h: K = every token, ascending (final rows); dz_c
     // read along its token axis (K-outer)
-    if (dw && c0 < v) {
-      const int64_t rows = (c1 < v ? c1 : v) - c0;
-      launch_gemm(bf16_out, gemm::kKOuterBlocked, dz, csteps, cols, l.np, gemm::kKContig, ht,
-                  npsteps * 512, h, -1, l.np, rows, h, nullptr, 0,
-                  static_cast<char*>(dw) + c0 * ld_dw * (bf16_out ? 2 : 4), ld_dw, s);
-    }
+    const int64_t rows = (c1 < v ? c1 : v) - c0;
+    char* dwc = dw ? static_cast<char*>(dw) + c0 * ld_dw * (bf16_out ? 2 : 4) : nullptr;
     // dh += dz_c W[c0, c1): K = the chunk's vocabulary, continuing the fp32
     // accumulators of the previous chunks (in dh itself for fp32 output, in
     // dh32 for bf16 output, rounded on the last chunk)
-    if (dh) {
-      const uint16_t* wtc;
-      int64_t ldwt;
-      if (prepared) {  // the prepared W^T [h, Vp]: columns [c0, c1)
-        wtc = prepared_blocked_wt(prepared, v, h) + (c0 / gemm::kK) * 512;
-        ldwt = vpsteps * 512;
-      } else {  // W[c0, c1) as it is: K-outer, its rows the lines
-        wtc = weight + c0 * ld_w;
-        ldwt = ld_w;
-      }
-      const float* cin = first ? nullptr : (dh32 ? dh32 : static_cast<const float*>(dh));
-      const int64_t ldcin = dh32 ? h : ld_dh;
-      const bool out_bf16 = bf16_out && last;
-      void* cout = bf16_out && !last ? static_cast<void*>(dh32) : dh;
-      const int64_t ldc = bf16_out && !last ? h : ld_dh;
-      launch_gemm(out_bf16, gemm::kKContig, dz, csteps * 512, l.np, -1,
-                  prepared ? gemm::kKContig : gemm::kKOuter, wtc, ldwt, h,
-                  prepared ? -1 : (c1 < v ? c1 : v) - c0, cols, n, h, cin, ldcin, cout, ldc, s);
+    const uint16_t* wtc;
+    int64_t ldwt;
+    if (prepared) {  // the prepared W^T [h, Vp]: columns [c0, c1)
+      wtc = prepared_blocked_wt(prepared, v, h) + (c0 / gemm::kK) * 512;
+      ldwt = vpsteps * 512;
+    } else {  // W[c0, c1) as it is: K-outer, its rows the lines
+      wtc = weight + c0 * ld_w;
+      ldwt = ld_w;
     }
+    const int64_t wt_kvalid = prepared ? -1 : rows;
+    const float* cin = first ? nullptr : (dh32 ? dh32 : static_cast<const float*>(dh));
+    const int64_t ldcin = dh32 ? h : ld_dh;
+    const bool dh_bf16 = bf16_out && last;
+    void* cout = bf16_out && !last ? static_cast<void*>(dh32) : dh;
+    const int64_t ldc = bf16_out && !last ? h : ld_dh;
+    const int hblocks = static_cast<int>((h + kT - 1) / kT);
+    const int dh_mblocks = static_cast<int>((n + kT - 1) / kT), dh_tiles = dh_mblocks * hblocks;
+    if (dh && dw && c0 < v && dh_tiles < 8 * xcd_cus()) {
+      const GemmArgs gh{dz, csteps * 512, l.np, -1, wtc, ldwt, h, static_cast<int>(wt_kvalid),
+                        static_cast<int>(csteps), dh_mblocks, hblocks, n, h, cin, ldcin, cout, ldc};
+      const GemmArgs gw{dz, csteps, cols, static_cast<int>(l.np), ht, npsteps * 512, h, -1,
+                        static_cast<int>(npsteps), static_cast<int>((rows + kT - 1) / kT), hblocks,
+                        rows, h, nullptr, 0, dwc, ld_dw};
+      constexpr int KC = gemm::kKContig, KO = gemm::kKOuter;
+      auto kern = prepared ? (!bf16_out ? gemm_pair_kernel<false, false, KC>
+                              : dh_bf16 ? gemm_pair_kernel<true, true, KC>
+                                        : gemm_pair_kernel<false, true, KC>)
+                           : (!bf16_out ? gemm_pair_kernel<false, false, KO>
+                              : dh_bf16 ? gemm_pair_kernel<true, true, KO>
+                                        : gemm_pair_kernel<false, true, KO>);
+      hipLaunchKernelGGL(kern, dim3(dh_tiles + gw.mblocks * hblocks), dim3(gemm::kThreads), 0, s,
+                         gh, gw, dh_tiles);
+      continue;
+    }
+    if (dw && c0 < v)
+      launch_gemm(bf16_out, gemm::kKOuterBlocked, dz, csteps, cols, l.np, gemm::kKContig, ht,
+                  npsteps * 512, h, -1, l.np, rows, h, nullptr, 0, dwc, ld_dw, s);
+    if (dh)
+      launch_gemm(dh_bf16, gemm::kKContig, dz, csteps * 512, l.np, -1,
+                  prepared ? gemm::kKContig : gemm::kKOuter, wtc, ldwt, h, wt_kvalid, cols, n, h,
+                  cin, ldcin, cout, ldc, s);
   }
   (void)hsteps;
 }

@@ -13,7 +13,7 @@ import torch
 from . import _lib
 from ._lib import check
 from .ops import (_DTYPES, _INDEX, _dtype_code, _linear_operands, _nbytes, _padded_logits,
-                  _prepared, _prepared_buffer, _ptr, _rounding, _row_vector, _rows, _stream)
+                  _prepared, _prepared_buffer, _ptr, _rounding, _row_vector, _rows)
 
 
 class TokenLogp(NamedTuple):
@@ -37,22 +37,18 @@ class QuantizedRows(NamedTuple):
     scale: torch.Tensor
 
 
-class _on:
-    """The device's current-device scope and stream, skipped when the device
-    is current already."""
-
-    __slots__ = ("scope",)
-
-    def __init__(self, device):
-        self.scope = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.scope is not None:
-            self.scope.__enter__()
-
-    def __exit__(self, *exc):
-        if self.scope is not None:
-            self.scope.__exit__(*exc)
+def _call(name, device, *args):
+    """The library function on the device's current stream (its last
+    argument), with that device current; a non-zero status raises."""
+    fn = getattr(_lib.lib(), name)
+    index = device.index
+    if torch.cuda.current_device() == index:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        check(name, st)
 
 
 def _tokens(t, n, lead, device):
@@ -137,11 +133,8 @@ def token_logp_fwd(logits, token_ids=None, top_k=0, ignore_index=-100, tile_widt
     L = _lib.lib()
     need = L.token_logp_fwd_workspace_bytes(n, v, code, int(tile_width), k)
     ws = _workspace(workspace, need, dev)
-    with _on(dev):
-        st = L.token_logp_fwd(x2.data_ptr(), code, n, v, ld, _ptr(tok), tcode, m,
-                              int(ignore_index), int(tile_width), k, *out.pointers(), _ptr(ws),
-                              _nbytes(ws), _stream(dev))
-    check("token_logp_fwd", st)
+    _call("token_logp_fwd", dev, x2.data_ptr(), code, n, v, ld, _ptr(tok), tcode, m,
+          int(ignore_index), int(tile_width), k, *out.pointers(), _ptr(ws), _nbytes(ws))
     return out.result()
 
 
@@ -171,12 +164,9 @@ def token_logp_bwd(logits, lse, token_ids=None, grad_logp=None, top_ids=None, gr
     d2, v2, ld_out = _rows(dlogits_out)
     if v2 != v or d2.shape[0] != n or dlogits_out.dtype != logits.dtype or dlogits_out.device != dev:
         raise ValueError("dlogits_out must match the logits shape, dtype and device")
-    with _on(dev):
-        st = _lib.lib().token_logp_bwd(x2.data_ptr(), code, n, v, ld, _ptr(tok), tcode, m,
-                                       int(ignore_index), _ptr(ids), k, lse.data_ptr(), _ptr(g),
-                                       _ptr(gt), _ptr(ent), _ptr(gent), d2.data_ptr(), ld_out,
-                                       _stream(dev))
-    check("token_logp_bwd", st)
+    _call("token_logp_bwd", dev, x2.data_ptr(), code, n, v, ld, _ptr(tok), tcode, m,
+          int(ignore_index), _ptr(ids), k, lse.data_ptr(), _ptr(g), _ptr(gt), _ptr(ent),
+          _ptr(gent), d2.data_ptr(), ld_out)
     return dlogits_out
 
 
@@ -283,21 +273,18 @@ def linear_token_logp_fwd(hidden, weight, token_ids=None, top_k=0, ignore_index=
     out = _Outputs(n, (n,), m, k, return_entropy, dev, outputs)
     need = L.linear_token_logp_fwd_workspace_bytes(n, h, v, m, k, flags, int(row_chunk))
     ws = _workspace(workspace, need, dev)
-    with _on(dev):
-        if q8:
-            st = L.linear_token_logp_q8_fwd(
-                hidden.data.data_ptr(), ld_h, hidden.scale.data_ptr(), weight.data.data_ptr(), ld_w,
-                weight.scale.data_ptr(), n, h, v, _ptr(tok), tcode, m, int(ignore_index),
-                float(temperature), k, *out.pointers(), int(row_chunk), _ptr(ws), _nbytes(ws),
-                _stream(dev))
-        else:
-            st = L.linear_token_logp_fwd(
-                hidden.data_ptr(), ld_h, weight.data_ptr(), ld_w, n, h, v, _ptr(tok), tcode, m,
-                int(ignore_index), float(temperature), _rounding(round_logits), k, *out.pointers(),
-                _ptr(z), _DTYPES[z.dtype] if z is not None else 0,
-                (z.stride(0) if n > 1 else v) if z is not None else 0, _ptr(pw), _nbytes(pw),
-                int(row_chunk), _ptr(ws), _nbytes(ws), _stream(dev))
-    check("linear_token_logp_q8_fwd" if q8 else "linear_token_logp_fwd", st)
+    if q8:
+        _call("linear_token_logp_q8_fwd", dev, hidden.data.data_ptr(), ld_h,
+              hidden.scale.data_ptr(), weight.data.data_ptr(), ld_w, weight.scale.data_ptr(), n, h,
+              v, _ptr(tok), tcode, m, int(ignore_index), float(temperature), k, *out.pointers(),
+              int(row_chunk), _ptr(ws), _nbytes(ws))
+    else:
+        _call("linear_token_logp_fwd", dev, hidden.data_ptr(), ld_h, weight.data_ptr(), ld_w, n, h,
+              v, _ptr(tok), tcode, m, int(ignore_index), float(temperature),
+              _rounding(round_logits), k, *out.pointers(), _ptr(z),
+              _DTYPES[z.dtype] if z is not None else 0,
+              (z.stride(0) if n > 1 else v) if z is not None else 0, _ptr(pw), _nbytes(pw),
+              int(row_chunk), _ptr(ws), _nbytes(ws))
     return out.result()
 
 
@@ -356,16 +343,14 @@ def linear_token_logp_bwd(hidden, weight, lse, token_ids=None, logp=None, grad_l
              | (_lib.LOGP_BWD_BF16_OUT if out_dtype == torch.bfloat16 else 0))
     need = L.linear_token_logp_bwd_workspace_bytes(n, h, v, flags, int(vocab_chunk))
     ws = _workspace(workspace, need, dev)
-    with _on(dev):
-        st = L.linear_token_logp_bwd(
-            hidden.data_ptr(), ld_h, weight.data_ptr(), ld_w, n, h, v, _ptr(tok), tcode, m,
-            int(ignore_index), _ptr(ids), k, float(temperature), _rounding(round_logits), _ptr(z),
-            _DTYPES[z.dtype] if z is not None else 0, max(z.stride(0), v) if z is not None else 0,
-            _ptr(pw), _nbytes(pw), lse.data_ptr(), _ptr(lp), _ptr(tl), _ptr(g), _ptr(gt), _ptr(ent),
-            _ptr(gent), _DTYPES[out_dtype], _ptr(dh), (dh.stride(0) if n > 1 else h) if dh is not None else 0,
-            _ptr(dw), (dw.stride(0) if v > 1 else h) if dw is not None else 0, int(vocab_chunk),
-            _ptr(ws), _nbytes(ws), _stream(dev))
-    check("linear_token_logp_bwd", st)
+    _call("linear_token_logp_bwd", dev, hidden.data_ptr(), ld_h, weight.data_ptr(), ld_w, n, h, v,
+          _ptr(tok), tcode, m, int(ignore_index), _ptr(ids), k, float(temperature),
+          _rounding(round_logits), _ptr(z), _DTYPES[z.dtype] if z is not None else 0,
+          max(z.stride(0), v) if z is not None else 0, _ptr(pw), _nbytes(pw), lse.data_ptr(),
+          _ptr(lp), _ptr(tl), _ptr(g), _ptr(gt), _ptr(ent), _ptr(gent), _DTYPES[out_dtype], _ptr(dh),
+          (dh.stride(0) if n > 1 else h) if dh is not None else 0, _ptr(dw),
+          (dw.stride(0) if v > 1 else h) if dw is not None else 0, int(vocab_chunk), _ptr(ws),
+          _nbytes(ws))
     return dh, dw
 
 
@@ -435,6 +420,15 @@ def _norm_rows(x, name, like=None):
     return x2.data_ptr(), x2.shape[0], h, x2.stride(0) if x2.shape[0] > 1 else h
 
 
+def _norm_out(given, name, like, h):
+    """An output like `like`: (tensor, pointer, row stride)."""
+    if given is None:
+        o = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        return o, o.data_ptr(), h
+    p, _, _, ld = _norm_rows(given, name, like)
+    return given, p, ld
+
+
 def _norm_weight(weight, x):
     if (weight.shape != x.shape[-1:] or weight.dtype != x.dtype or weight.device != x.device
             or not weight.is_contiguous()):
@@ -452,19 +446,14 @@ def rms_norm_fwd(x, weight, residual=None, eps=1e-6, return_rstd=False, y_out=No
     code = _dtype_code(x)
     pw = _norm_weight(weight, x)
     dev = x.device
-    y = torch.empty(x.shape, dtype=x.dtype, device=dev) if y_out is None else y_out
-    py, _, _, ld_y = _norm_rows(y, "y_out", x)
-    pr = ld_r = ps = ld_s = None
-    s = x
+    y, py, ld_y = _norm_out(y_out, "y_out", x, h)
+    pr, ld_r, ps, ld_s, s = None, 0, None, 0, x
     if residual is not None:
         pr, _, _, ld_r = _norm_rows(residual, "residual", x)
-        s = torch.empty(x.shape, dtype=x.dtype, device=dev) if sum_out is None else sum_out
-        ps, _, _, ld_s = _norm_rows(s, "sum_out", x)
+        s, ps, ld_s = _norm_out(sum_out, "sum_out", x, h)
     rstd = torch.empty(n, dtype=torch.float32, device=dev) if return_rstd else None
-    with _on(dev):
-        st = _lib.lib().rms_norm_fwd(px, ld_x, pr, ld_r or 0, pw, code, n, h, float(eps), py, ld_y,
-                                     ps, ld_s or 0, _ptr(rstd), _stream(dev))
-    check("rms_norm_fwd", st)
+    _call("rms_norm_fwd", dev, px, ld_x, pr, ld_r, pw, code, n, h, float(eps), py, ld_y, ps, ld_s,
+          _ptr(rstd))
     return y, s, rstd
 
 
@@ -483,15 +472,12 @@ def rms_norm_bwd(s, weight, rstd, grad_y, grad_sum=None, need_dweight=True, dx_o
     rstd = _row_vector(rstd, n, "rstd")
     _same_device(s.device, rstd=rstd)
     dev = s.device
-    dx = torch.empty(s.shape, dtype=s.dtype, device=dev) if dx_out is None else dx_out
-    px, _, _, ld_x = _norm_rows(dx, "dx_out", s)
+    dx, px, ld_x = _norm_out(dx_out, "dx_out", s, h)
     dw = torch.empty(h, dtype=s.dtype, device=dev) if need_dweight else None
     L = _lib.lib()
     ws = _workspace(workspace, L.rms_norm_bwd_workspace_bytes(n, h), dev) if need_dweight else None
-    with _on(dev):
-        st = L.rms_norm_bwd(p_s, ld_s, pw, rstd.data_ptr(), pg, ld_g, pd, ld_d, code, n, h, px, ld_x,
-                            _ptr(dw), _ptr(ws), _nbytes(ws), _stream(dev))
-    check("rms_norm_bwd", st)
+    _call("rms_norm_bwd", dev, p_s, ld_s, pw, rstd.data_ptr(), pg, ld_g, pd, ld_d, code, n, h, px,
+          ld_x, _ptr(dw), _ptr(ws), _nbytes(ws))
     return dx, dw
 
 
@@ -530,14 +516,11 @@ def _quantize(x, weight, residual, eps, sum_out):
     pr, ld_r, ps, ld_s, s = None, 0, None, 0, x
     if residual is not None:
         pr, _, _, ld_r = _norm_rows(residual, "residual", x)
-        s = torch.empty(x.shape, dtype=x.dtype, device=dev) if sum_out is None else sum_out
-        ps, _, _, ld_s = _norm_rows(s, "sum_out", x)
+        s, ps, ld_s = _norm_out(sum_out, "sum_out", x, h)
     q = torch.empty(n, h, dtype=torch.float8_e4m3fn, device=dev)
     scale = torch.empty(n, dtype=torch.float32, device=dev)
-    with _on(dev):
-        st = _lib.lib().rms_norm_q8_fwd(px, ld_x, pr, ld_r, pw, code, n, h, float(eps), q.data_ptr(),
-                                        h, scale.data_ptr(), ps, ld_s, _stream(dev))
-    check("rms_norm_q8_fwd", st)
+    _call("rms_norm_q8_fwd", dev, px, ld_x, pr, ld_r, pw, code, n, h, float(eps), q.data_ptr(), h,
+          scale.data_ptr(), ps, ld_s)
     return QuantizedRows(q, scale), s
 
 
