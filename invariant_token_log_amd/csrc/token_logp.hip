@@ -179,7 +179,10 @@ __global__ __launch_bounds__(kPartBlock) void token_partials_kernel(
 // bit mask and reads the few marked ones again instead of carrying an unrolled
 // append.
 // ---------------------------------------------------------------------------
-constexpr int kKeys = 20;  // groups a lane holds at once
+// groups a lane holds at once: 1280 of 128 columns, or 640 vocabulary tiles of
+// 256, each about 164000 columns
+template <bool HEAD>
+constexpr int kKeys = HEAD ? 10 : 20;
 
 // Order keys of the groups b0 + 64 c + lane; 0 (below every key) past the last.
 template <bool HEAD>
@@ -188,14 +191,14 @@ __device__ __forceinline__ uint32_t group_key(const uint32_t* g, int64_t i) {
 }
 template <bool HEAD>
 __device__ __forceinline__ void load_keys(const uint32_t* g, int64_t b0, int64_t groups, int lane,
-                                          uint32_t (&key)[kKeys]) {
+                                          uint32_t (&key)[kKeys<HEAD>]) {
 #pragma unroll
-  for (int c = 0; c < kKeys; ++c) {
+  for (int c = 0; c < kKeys<HEAD>; ++c) {
     const int64_t i = b0 + c * kWave + lane;
     key[c] = g[i < groups ? i : 0];
   }
 #pragma unroll
-  for (int c = 0; c < kKeys; ++c) {
+  for (int c = 0; c < kKeys<HEAD>; ++c) {
     const uint32_t k = HEAD ? order_key(__uint_as_float(key[c])) : key[c];
     key[c] = b0 + c * kWave + lane < groups ? k : 0u;
   }
@@ -206,7 +209,7 @@ __device__ __forceinline__ void load_keys(const uint32_t* g, int64_t b0, int64_t
 template <typename T, int GW, bool VEC, bool HEAD>
 __device__ __forceinline__ void select_top(TopStage& st, const T* row, float inv_t, uint32_t v,
                                            const uint32_t* g, int64_t groups, int top_k,
-                                           uint32_t (&key)[kKeys], int lane) {
+                                           uint32_t (&key)[kKeys<HEAD>], int lane) {
   constexpr int E = Elt<T>::kPerChunk;
   constexpr int LPG = GW / E;            // lanes per group
   constexpr int GPW = kWave / LPG;       // groups one wave load covers
@@ -217,12 +220,12 @@ __device__ __forceinline__ void select_top(TopStage& st, const T* row, float inv
   };
   // 1. A bound: the k-th greatest of 256 maxima, four a lane, over disjoint
   // sets of groups.  At least k groups reach it.
-  const bool one_block = groups <= kKeys * kWave;
+  const bool one_block = groups <= kKeys<HEAD> * kWave;
   uint32_t best[4] = {0, 0, 0, 0};
-  for (int64_t b0 = 0; b0 < groups; b0 += kKeys * kWave) {
+  for (int64_t b0 = 0; b0 < groups; b0 += kKeys<HEAD> * kWave) {
     if (b0 > 0) load_keys<HEAD>(g, b0, groups, lane, key);
 #pragma unroll
-    for (int c = 0; c < kKeys; ++c) best[c % 4] = max(best[c % 4], key[c]);
+    for (int c = 0; c < kKeys<HEAD>; ++c) best[c % 4] = max(best[c % 4], key[c]);
   }
   const uint32_t bound = max(wave_bound(best, top_k), 1u);
   // 2. The k greatest groups (or all, when there are fewer).  Few groups
@@ -232,11 +235,11 @@ __device__ __forceinline__ void select_top(TopStage& st, const T* row, float inv
   int reach = 0, place = 0;
   if (one_block) {
 #pragma unroll
-    for (int c = 0; c < kKeys; ++c) reach += key[c] >= bound;
+    for (int c = 0; c < kKeys<HEAD>; ++c) reach += key[c] >= bound;
   }
   if (one_block && top_reserve(st, list, reach, place)) {
 #pragma unroll
-    for (int c = 0; c < kKeys; ++c)
+    for (int c = 0; c < kKeys<HEAD>; ++c)
       if (key[c] >= bound)
         st.e[place++] = compose(key[c], static_cast<uint32_t>(c * kWave + lane));
   } else {
@@ -342,7 +345,7 @@ __global__ __launch_bounds__(kFinBlock) void token_finish_kernel(
     const int64_t r = r0 + slot;
     bool live = r < n;
     // The group keys or the given tokens are on their way first.
-    uint32_t key[kKeys];
+    uint32_t key[kKeys<HEAD>];
     const uint32_t* g = gm + r * groups;
     if (live && selects) load_keys<HEAD>(g, 0, groups, lane, key);
     int64_t t0 = live && lane < tok.m ? tok.at(r, lane) : tok.ignore;
