@@ -9,9 +9,10 @@
 
 namespace itl {
 
+constexpr int kQ8Tile = 128;  // vocabulary columns per statistic tile
 constexpr int64_t kMaxQ8Stride = int64_t{1} << 23;  // bytes between operand rows
 
-// Tile statistics [n, T] (T = ceil(v / 256), row-major), the target logits of
+// Tile statistics [n, T] (T = ceil(v / kQ8Tile), row-major), the target logits of
 // the active rows and, unless z is null, the unscaled logits [n, ld_z] fp32
 // of the 8-bit head: logits = (hidden weight^T) hs[r] ws[j]; hidden [n, ld_h]
 // and weight [v, ld_w] e4m3, 16-byte aligned rows, h a multiple of 64.  pw

@@ -3,14 +3,17 @@
 //
 //   z[r, j] = (sum_k hidden[r, k] weight[j, k]) hs[r] ws[j]
 //
-// Arithmetic: every sum is one fp32 accumulator fed by
-// v_mfma_f32_32x32x64_f8f6f4 over K in ascending steps of 64, no split;
-// z = (acc hs) ws, x = z * fl32(1 / T).  The statistic tile is 256 vocabulary
-// columns in eight groups of 32.  Maximum: exact.  Sum (and entropy moment):
-// in a group, the 16 columns 8a + b (b < 4) and the 16 columns 8a + 4 + b are
-// folded in ascending order from +0 and added; the groups follow as ((g0 + g1)
-// + (g2 + g3)) + ((g4 + g5) + (g6 + g7)).  Every kernel below evaluates exactly
-// this, so a row's outputs do not depend on n or on its place.
+// Arithmetic: e4m3 values widen exactly to bf16, every sum is one fp32
+// accumulator fed by v_mfma_f32_32x32x16_bf16, no split; z = (acc hs) ws,
+// x = z * fl32(1 / T).  (The 8-bit matrix instruction runs at twice the rate,
+// but it aligns a group's products to about 17 bits before it adds them: logits
+// off by 1.4e-5 of their spread, a hundred times what fp32 sums cost, and
+// nothing in the inputs bounds it.  4096 rows took 2.1 ms with it.)
+// The statistic tile is 128 vocabulary columns in four groups of 32.  Maximum:
+// exact.  Sum (and entropy moment): in a group, the 16 columns 8a + b (b < 4)
+// and the 16 columns 8a + 4 + b are folded in ascending order from +0 and
+// added; the groups follow as (g0 + g1) + (g2 + g3).  Every kernel below
+// evaluates exactly this, so a row's outputs do not depend on n or its place.
 //
 // The weight rows are the matrix product's first operand, so that an
 // accumulator register holds a vocabulary column and a lane a hidden row: the
@@ -18,11 +21,12 @@
 // of the wave, where the other order needs a five-level butterfly a value.
 //
 // Two kernels:
-//   q8_stats_wide (n > 128): 256 x 256 tiles, eight waves of 128 vocabulary
-//     columns x 64 hidden rows; bound by the matrix cores and their power.
-//   q8_stats_narrow<NB> (n <= 32 NB, NB = 1, 2, 4): 256 vocabulary columns x
-//     32 NB hidden rows, eight waves of 32 columns; bound by the weight's
-//     bytes, so it keeps two to three 128-byte steps of 256 rows in flight.
+//   q8_stats_wide (n > 128): 256 x 256 blocks, eight waves of 128 vocabulary
+//     columns (one tile) x 64 hidden rows; bound by the matrix cores.
+//   q8_stats_narrow<NB> (n <= 32 NB, NB = 1, 2, 4): 128 vocabulary columns x
+//     32 NB hidden rows, four waves of 32 columns, two workgroups a CU; bound
+//     by the weight's bytes.  Tiles of 128 columns leave less of the GPU idle
+//     at the end than 256 would (V = 151936: 1187 tiles instead of 594).
 #include "linear_q8.h"
 
 #include "logp_device.h"
@@ -36,9 +40,11 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-constexpr int kV = kLinearTile;    // vocabulary columns per tile
+constexpr int kV = 256;            // vocabulary columns of a wide block
+constexpr int kVT = kQ8Tile;       // vocabulary columns per statistic tile
 constexpr int kStep = 64;          // K bytes per matrix instruction
-constexpr int kQThreads = 512;     // 8 waves
+constexpr int kQThreads = 512;     // 8 waves (wide)
+constexpr int kNThreads = 256;     // 4 waves (narrow)
 
 // Eight e4m3 values (two dwords of a chunk) as bf16, exactly.
 __device__ __forceinline__ bf16x8 widen_q8(int lo, int hi) {
@@ -71,54 +77,42 @@ __device__ __forceinline__ void mfma_q8(const i32x4 (&w)[NI], const i32x4 (&h)[N
   }
 }
 
-// What the epilogue needs of the tile's hidden rows and vocabulary columns.
-template <int ROWS>
-struct Q8Reduce {
-  float red[8][ROWS];   // per vocabulary group maxima (wide: per wave pair)
-  float sum[8][ROWS];   // group sums
-  float wsum[8][ROWS];  // group entropy moments
-  float tval[ROWS];
-  float hs[ROWS];
-  float ws[kV];
-  int code[ROWS];       // -2: no statistics; -1: target elsewhere; else column
+// What the epilogue needs of a block's R hidden rows and C vocabulary columns.
+template <int R, int C>
+struct Q8Rows {
+  float hs[R];
+  float ws[C];
+  int code[R];  // -2: no statistics; -1: target elsewhere; else its column
 };
 
-template <int ROWS>
-__device__ __forceinline__ void q8_fill(Q8Reduce<ROWS>& rd, int tid, const float* hs,
-                                        const float* ws, int64_t n, int64_t v, int64_t m0,
-                                        int64_t v0, Targets targets, int64_t ignore) {
-  if (tid < ROWS) {
-    const int64_t r = m0 + tid;
+template <int R, int C, int THREADS>
+__device__ __forceinline__ void q8_fill(Q8Rows<R, C>& rd, const float* hs, const float* ws,
+                                        int64_t n, int64_t v, int64_t m0, int64_t v0,
+                                        Targets targets, int64_t ignore) {
+  for (int i = threadIdx.x; i < R; i += THREADS) {
+    const int64_t r = m0 + i;
     int code = -2;
     float s = 0.0f;
     if (r < n) {
       const int64_t t = targets[r];
-      if (t != ignore)
-        code = (t >= v0 && t < v0 + kV && t < v) ? static_cast<int>(t - v0) : -1;
+      if (t != ignore) code = (t >= v0 && t < v0 + C && t < v) ? static_cast<int>(t - v0) : -1;
       s = hs[r];
     }
-    rd.code[tid] = code;
-    rd.hs[tid] = s;
+    rd.code[i] = code;
+    rd.hs[i] = s;
   }
-  if (tid >= kQThreads - kV) {
-    const int c = tid - (kQThreads - kV);
-    rd.ws[c] = v0 + c < v ? ws[v0 + c] : 0.0f;
-  }
+  for (int i = threadIdx.x; i < C; i += THREADS) rd.ws[i] = v0 + i < v ? ws[v0 + i] : 0.0f;
 }
 
-// Statistics of a wave's NI groups (32 vocabulary columns each, from group
-// g0 on) for its NJ blocks of 32 hidden rows from row0 on:
-//   acc[i][j][q] = z[m0 + row0 + 32 j + l % 32][v0 + 32 (g0 + i) + 8 (q / 4) + 4 hf + q % 4].
-// rd's rows and columns are filled; all threads of the workgroup call.
-template <int NI, int NJ, int ROWS, bool ENT>
-__device__ __forceinline__ void q8_epilogue(f32x16 (&acc)[NI][NJ], Q8Reduce<ROWS>& rd, int g0,
-                                            int row0, int tid, int64_t m0, int64_t v0, int vb,
-                                            int vblocks, int64_t n, int64_t v, float inv_t,
-                                            float* pm, float* ps, float* pw, float* pt, float* z,
-                                            int64_t ld_z) {
-  const int lane = tid % kWave;
-  const int col = lane % 32, hf = lane / 32;
-  // z, its output, x and the masked columns of the last tile
+// From accumulators to scaled logits: acc[i][j][q] of the wave's groups (32
+// columns each, from block column c0 on) and hidden rows (32 each, from row0
+// on) is column c0 + 32 i + 8 (q / 4) + 4 hf + q % 4 of row row0 + 32 j + l %
+// 32.  Writes z when asked and leaves x, -inf past the vocabulary.
+template <int NI, int NJ, int R, int C>
+__device__ __forceinline__ void q8_logits(f32x16 (&acc)[NI][NJ], const Q8Rows<R, C>& rd, int c0,
+                                          int row0, int64_t m0, int64_t v0, int64_t n, int64_t v,
+                                          float inv_t, float* z, int64_t ld_z) {
+  const int col = threadIdx.x % 32, hf = (threadIdx.x % kWave) / 32;
 #pragma unroll
   for (int j = 0; j < NJ; ++j) {
     const int lr = row0 + 32 * j + col;
@@ -129,12 +123,12 @@ __device__ __forceinline__ void q8_epilogue(f32x16 (&acc)[NI][NJ], Q8Reduce<ROWS
     for (int i = 0; i < NI; ++i)
 #pragma unroll
       for (int a = 0; a < 4; ++a) {
-        const int c = 32 * (g0 + i) + 8 * a + 4 * hf;
+        const int c = c0 + 32 * i + 8 * a + 4 * hf;
         const float4 w = *reinterpret_cast<const float4*>(&rd.ws[c]);
         float x[4] = {acc[i][j][4 * a] * h * w.x, acc[i][j][4 * a + 1] * h * w.y,
                       acc[i][j][4 * a + 2] * h * w.z, acc[i][j][4 * a + 3] * h * w.w};
         if (zr) {
-          if (v0 + c + 4 <= v && (ld_z & 3) == 0) {
+          if (v0 + c + 4 <= v) {  // the workspace's rows are 16-byte aligned
             *reinterpret_cast<float4*>(zr + c) = make_float4(x[0], x[1], x[2], x[3]);
           } else {
 #pragma unroll
@@ -143,76 +137,56 @@ __device__ __forceinline__ void q8_epilogue(f32x16 (&acc)[NI][NJ], Q8Reduce<ROWS
           }
         }
 #pragma unroll
-        for (int b = 0; b < 4; ++b)
-          acc[i][j][4 * a + b] = v0 + c + b < v ? x[b] * inv_t : -INFINITY;
+        for (int b = 0; b < 4; ++b) acc[i][j][4 * a + b] = x[b] * inv_t;
       }
   }
-  // maxima: registers, the other half of the wave, the other waves
+  if (v0 + C > v) {
 #pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    float m = acc[0][j][0];
+    for (int j = 0; j < NJ; ++j)
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
+      for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int q = 0; q < 16; ++q) m = max_exact(m, acc[i][j][q]);
-    m = max_exact(m, __shfl_xor(m, 32, kWave));
-    if (hf == 0) rd.red[g0 / NI][row0 + 32 * j + col] = m;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) {
-    const int lr = row0 + 32 * j + col;
-    float m = rd.red[0][lr];
-#pragma unroll
-    for (int w = 1; w < 8 / NI; ++w) m = max_exact(m, rd.red[w][lr]);
-    const int code = rd.code[lr];
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int off = code - 32 * (g0 + i);  // the target's place in this group
-      if (off >= 0 && off < 32 && ((off >> 2) & 1) == hf) {
-        const int q = (off >> 3) * 4 + (off & 3);
-        float t = acc[i][j][0];
-#pragma unroll
-        for (int k = 1; k < 16; ++k) t = q == k ? acc[i][j][k] : t;
-        rd.tval[lr] = t;
-      }
-      float s = 0.0f, w = 0.0f;
-#pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        const float d = acc[i][j][q] - m;
-        const float e = __builtin_amdgcn_exp2f(d * kLog2e);
-        s = s + e;
-        if constexpr (ENT) w = ent_term(e, d, w);
-      }
-      s = s + __shfl_xor(s, 32, kWave);
-      if constexpr (ENT) w = w + __shfl_xor(w, 32, kWave);
-      if (hf == 0) {
-        rd.sum[g0 + i][lr] = s;
-        if constexpr (ENT) rd.wsum[g0 + i][lr] = w;
-      }
-    }
-  }
-  __syncthreads();
-  for (int lr = tid; lr < ROWS; lr += kQThreads) {
-    const int code = rd.code[lr];
-    if (code == -2) continue;
-    const int64_t r = m0 + lr;
-    float m = rd.red[0][lr];
-#pragma unroll
-    for (int w = 1; w < 8 / NI; ++w) m = max_exact(m, rd.red[w][lr]);
-    auto fold = [&](const float (&g)[8][ROWS]) {
-      return ((g[0][lr] + g[1][lr]) + (g[2][lr] + g[3][lr])) +
-             ((g[4][lr] + g[5][lr]) + (g[6][lr] + g[7][lr]));
-    };
-    pm[r * vblocks + vb] = m;
-    ps[r * vblocks + vb] = fold(rd.sum);
-    if constexpr (ENT) pw[r * vblocks + vb] = fold(rd.wsum);
-    if (code >= 0) pt[r] = rd.tval[lr];
+        for (int q = 0; q < 16; ++q)
+          if (v0 + c0 + 32 * i + 8 * (q / 4) + 4 * hf + q % 4 >= v) acc[i][j][q] = -INFINITY;
   }
 }
 
+// A group's sum (and entropy moment) against m: both halves of the wave get it.
+template <bool ENT>
+__device__ __forceinline__ void q8_group_sum(const f32x16& x, float m, float& s, float& w) {
+  s = 0.0f;
+  w = 0.0f;
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    const float d = x[q] - m;
+    const float e = __builtin_amdgcn_exp2f(d * kLog2e);
+    s = s + e;
+    if constexpr (ENT) w = ent_term(e, d, w);
+  }
+  s = s + __shfl_xor(s, 32, kWave);
+  if constexpr (ENT) w = w + __shfl_xor(w, 32, kWave);
+}
+
+__device__ __forceinline__ float q8_group_max(const f32x16& x) {
+  float m = x[0];
+#pragma unroll
+  for (int q = 1; q < 16; ++q) m = max_exact(m, x[q]);
+  return m;
+}
+
+// The target's logit, if column `off` of the group is one of this lane's.
+__device__ __forceinline__ bool q8_target(const f32x16& x, int off, float& t) {
+  const int hf = (threadIdx.x % kWave) / 32;
+  if (off < 0 || off >= 32 || ((off >> 2) & 1) != hf) return false;
+  const int q = (off >> 3) * 4 + (off & 3);
+  t = x[0];
+#pragma unroll
+  for (int k = 1; k < 16; ++k) t = q == k ? x[k] : t;
+  return true;
+}
+
 // ---------------------------------------------------------------------------
-// Staging, for both kernels: slots of [256 weight rows | R hidden rows] x 128
+// Staging, for both kernels: slots of [weight rows | hidden rows] x 128
 // bytes, a "pair" of K steps, whole lines of row-major operands; chunk c (16
 // bytes) of row r sits in place c ^ swzp(r), which puts the 16 rows of a read
 // on different banks.  A load fills 8 rows; rows past the data read the last
@@ -246,12 +220,15 @@ __device__ __forceinline__ int pair_back(int ksteps, int blk, int lane) {
 }
 
 // ---------------------------------------------------------------------------
-// Wide: two slots of 64 KiB; while a pair is multiplied the next one loads,
-// issued by waves 0-3 right after the barrier.
+// Wide: two slots of 64 KiB.  The one barrier of a pair sits before its last
+// chunk's products: by then every wave has read the whole slot, which the pair
+// after next takes (loads issued by waves 0-3), and the next pair, issued a
+// pair's time ago, has landed, so its first chunk is read while the last
+// products run and the matrix cores do not pause at the barrier.
 // ---------------------------------------------------------------------------
 struct SmemWide {
   uint8_t s[2][(kV + 256) * kPair];
-  Q8Reduce<256> rd;
+  Q8Rows<256, kV> rd;
   int slot;
 };
 
@@ -265,58 +242,67 @@ __device__ __forceinline__ void q8_mainloop(SmemWide& sm, const uint8_t* __restr
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int row = lane % 32, hf = lane / 32;
   const int npairs = (ksteps + 1) / 2;
-  uint32_t wp[8], hp[8];
-  int back = 0;
-  if constexpr (LOADER) {
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      wp[u] = pair_source(ld_w, v0, v, wave + 4 * u, lane);
-      hp[u] = pair_source(ld_h, m0, n, wave + 4 * u, lane);
-    }
-    back = pair_back(ksteps, wave, lane);
-  }
+  // Blocks of 8 rows: wave + 4 u of either operand, u < 8.  The offsets are
+  // taken anew for every pair (registers are short here, a pair is long).
+  const int lrow = wave * 8 + lane / 8;
+  const int lchunk = ((lane % 8) ^ swzp(lrow)) * 16;  // swzp ignores multiples of 32 rows
+  const int back = (ksteps & 1) && lchunk >= kStep ? kStep : 0;
+  const int wlast = static_cast<int>(min(v - 1 - v0, int64_t{255}));
+  const int hlast = static_cast<int>(min(n - 1 - m0, int64_t{255}));
   auto issue = [&](int p) {
     if constexpr (LOADER) {
-      const uint8_t* w0 = W + v0 * ld_w + static_cast<int64_t>(p) * kPair;
-      const uint8_t* h0 = H + m0 * ld_h + static_cast<int64_t>(p) * kPair;
-      const int b = p == npairs - 1 ? back : 0;
+      const int64_t k = static_cast<int64_t>(p) * kPair;
+      const uint8_t* w0 = W + v0 * ld_w + k;
+      const uint8_t* h0 = H + m0 * ld_h + k;
+      const uint32_t c = lchunk - (p == npairs - 1 ? back : 0);
+      const uint32_t lw = static_cast<uint32_t>(ld_w), lh = static_cast<uint32_t>(ld_h);
       uint8_t* d = sm.s[p % 2] + wave * 1024;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) load_lds16<false>(w0 + (wp[u] - b), d + u * 4096);
+      for (int u = 0; u < 8; ++u)
+        load_lds16<false>(w0 + (min(lrow + 32 * u, wlast) * lw + c), d + u * 4096);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) load_lds16<false>(h0 + (hp[u] - b), d + kV * kPair + u * 4096);
+      for (int u = 0; u < 8; ++u)
+        load_lds16<false>(h0 + (min(lrow + 32 * u, hlast) * lh + c), d + kV * kPair + u * 4096);
     }
   };
   const int sw = swzp(row);  // repeats every 16 rows
   const int wofs = ((wave / 4) * 128 + row) * kPair;
   const int hofs = (kV + (wave % 4) * 64 + row) * kPair;
+  i32x4 xw[4], xh[2], yw[4], yh[2];
+  auto read = [&](int p, int u, i32x4 (&fw)[4], i32x4 (&fh)[2]) {
+    const uint8_t* base = sm.s[p % 2] + ((2 * u + hf) ^ sw) * 16;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      fh[j] = *reinterpret_cast<const i32x4*>(base + hofs + 32 * j * kPair);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      fw[i] = *reinterpret_cast<const i32x4*>(base + wofs + 32 * i * kPair);
+  };
   issue(0);
+  if (npairs > 1) {
+    issue(1);
+    wait_vm<LOADER ? 16 : 0>();
+  } else {
+    wait_vm<0>();
+  }
+  __builtin_amdgcn_s_barrier();
+  read(0, 0, xw, xh);
   for (int p = 0; p < npairs; ++p) {
-    // pair p has landed (it is all that was in flight), and nobody reads the
-    // other slot any more
-    wait_vm_lgkm0<0>();
-    __builtin_amdgcn_s_barrier();
-    if (p + 1 < npairs) issue(p + 1);
-    const uint8_t* w_ = sm.s[p % 2] + wofs;
-    const uint8_t* h_ = sm.s[p % 2] + hofs;
-    i32x4 cw[2][4], ch[2][2];
-    auto read = [&](int u, i32x4 (&fw)[4], i32x4 (&fh)[2]) {
-      const int c = ((2 * u + hf) ^ sw) * 16;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) fh[j] = *reinterpret_cast<const i32x4*>(h_ + 32 * j * kPair + c);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) fw[i] = *reinterpret_cast<const i32x4*>(w_ + 32 * i * kPair + c);
-    };
-    read(0, cw[0], ch[0]);
-    read(1, cw[1], ch[1]);
-    mfma_q8<4, 2>(cw[0], ch[0], acc);
+    read(p, 1, yw, yh);
+    mfma_q8<4, 2>(xw, xh, acc);
     if (2 * p + 1 < ksteps) {
-      read(2, cw[0], ch[0]);
-      mfma_q8<4, 2>(cw[1], ch[1], acc);
-      read(3, cw[1], ch[1]);
-      mfma_q8<4, 2>(cw[0], ch[0], acc);
+      read(p, 2, xw, xh);
+      mfma_q8<4, 2>(yw, yh, acc);
+      read(p, 3, yw, yh);
+      mfma_q8<4, 2>(xw, xh, acc);
     }
-    mfma_q8<4, 2>(cw[1], ch[1], acc);
+    if (p + 1 < npairs) {
+      wait_vm_lgkm0<0>();  // this wave's reads of pair p, its loads of pair p + 1
+      __builtin_amdgcn_s_barrier();
+      if (p + 2 < npairs) issue(p + 2);
+      read(p + 1, 0, xw, xh);
+    }
+    mfma_q8<4, 2>(yw, yh, acc);
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
@@ -325,20 +311,19 @@ template <bool ENT>
 __global__ __launch_bounds__(kQThreads) void q8_stats_wide(
     const uint8_t* __restrict__ hidden, int64_t ld_h, const float* __restrict__ hs,
     const uint8_t* __restrict__ weight, int64_t ld_w, const float* __restrict__ ws, int64_t n,
-    int64_t v, int ksteps, int mblocks, int vblocks, const void* __restrict__ tgt, int32_t tgt32,
-    int64_t ignore, float inv_t, float* __restrict__ pm, float* __restrict__ ps,
+    int64_t v, int ksteps, int mblocks, int vblocks, int ntiles, const void* __restrict__ tgt,
+    int32_t tgt32, int64_t ignore, float inv_t, float* __restrict__ pm, float* __restrict__ ps,
     float* __restrict__ pw, float* __restrict__ pt, float* __restrict__ z, int64_t ld_z,
     int* queue, int queued) {
   const Targets targets{tgt, tgt32};
   __shared__ __align__(16) SmemWide sm;
-  const int tid = threadIdx.x;
-  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int logical = gemm::queue_tile(queue, mblocks * vblocks, queued, &sm.slot);
   if (logical < 0) return;
   int mb, vb;
   gemm::tile_coords(logical, mblocks, vblocks, mb, vb);
   const int64_t m0 = static_cast<int64_t>(mb) * 256, v0 = static_cast<int64_t>(vb) * kV;
-  q8_fill(sm.rd, tid, hs, ws, n, v, m0, v0, targets, ignore);
+  q8_fill<256, kV, kQThreads>(sm.rd, hs, ws, n, v, m0, v0, targets, ignore);
   f32x16 acc[4][2];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -350,22 +335,50 @@ __global__ __launch_bounds__(kQThreads) void q8_stats_wide(
     q8_mainloop<true>(sm, hidden, ld_h, m0, n, weight, ld_w, v0, v, ksteps, acc);
   else
     q8_mainloop<false>(sm, hidden, ld_h, m0, n, weight, ld_w, v0, v, ksteps, acc);
-  __syncthreads();
-  q8_epilogue<4, 2, 256, ENT>(acc, sm.rd, (wave / 4) * 4, (wave % 4) * 64, tid, m0, v0, vb,
-                              vblocks, n, v, inv_t, pm, ps, pw, pt, z, ld_z);
+  // A wave holds its 64 rows' whole tile: no exchange between waves.
+  const int c0 = (wave / 4) * kVT, row0 = (wave % 4) * 64;
+  q8_logits<4, 2, 256, kV>(acc, sm.rd, c0, row0, m0, v0, n, v, inv_t, z, ld_z);
+  const int tile = vb * (kV / kVT) + wave / 4;
+  if (tile >= ntiles) return;  // the second half of the last block may be empty
+  const int col = threadIdx.x % 32, hf = (threadIdx.x % kWave) / 32;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int lr = row0 + 32 * j + col;
+    const int64_t r = m0 + lr;
+    const int code = sm.rd.code[lr];
+    float m = q8_group_max(acc[0][j]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) m = max_exact(m, q8_group_max(acc[i][j]));
+    m = max_exact(m, __shfl_xor(m, 32, kWave));
+    float s[4], w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float t;
+      if (q8_target(acc[i][j], code - c0 - 32 * i, t)) pt[r] = t;
+      q8_group_sum<ENT>(acc[i][j], m, s[i], w[i]);
+    }
+    if (hf == 0 && code != -2) {
+      pm[r * ntiles + tile] = m;
+      ps[r * ntiles + tile] = (s[0] + s[1]) + (s[2] + s[3]);
+      if constexpr (ENT) pw[r * ntiles + tile] = (w[0] + w[1]) + (w[2] + w[3]);
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
-// Narrow: three or four slots with 32 NB hidden rows, every wave loading; wave
+// Narrow: two or three slots with 32 NB hidden rows, every wave loading; wave
 // w computes vocabulary group w for all hidden rows.
 // ---------------------------------------------------------------------------
 template <int NB>
-constexpr int kNarrowSlots = NB == 1 ? 4 : 3;
+constexpr int kNarrowSlots = NB == 4 ? 2 : 3;
 
 template <int NB>
 struct SmemNarrowQ8 {
-  uint8_t s[kNarrowSlots<NB>][(kV + 32 * NB) * kPair];
-  Q8Reduce<32 * NB> rd;
+  uint8_t s[kNarrowSlots<NB>][(kVT + 32 * NB) * kPair];
+  Q8Rows<32 * NB, kVT> rd;
+  float max[4][32 * NB];
+  float sum[4][32 * NB];
+  float wsum[4][32 * NB];
 };
 
 template <int NB>
@@ -379,32 +392,23 @@ __device__ __forceinline__ void q8_mainloop_narrow(SmemNarrowQ8<NB>& sm,
   const int lane = threadIdx.x % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int npairs = (ksteps + 1) / 2;
-  constexpr int kHBlocks = 4 * NB;              // hidden blocks of 8 rows
-  constexpr int NH = kHBlocks > 8 ? 2 : 1;      // loads of them a wave
-  const bool has_h = wave < kHBlocks;
+  // blocks of 8 rows: wave + 4 u of the weight's 16 and the hidden rows' 4 NB
   const uint8_t* wp[4];
-  const uint8_t* hp[NH];
+  const uint8_t* hp[NB];
 #pragma unroll
   for (int u = 0; u < 4; ++u)
-    wp[u] = weight + v0 * ld_w + pair_source(ld_w, v0, v, wave + 8 * u, lane);
+    wp[u] = weight + v0 * ld_w + pair_source(ld_w, v0, v, wave + 4 * u, lane);
 #pragma unroll
-  for (int u = 0; u < NH; ++u)
-    hp[u] = hidden + pair_source(ld_h, 0, n, wave % kHBlocks + 8 * u, lane);
-  const int back_w = pair_back(ksteps, wave, lane);
-  const int back_h = pair_back(ksteps, wave % kHBlocks, lane);
+  for (int u = 0; u < NB; ++u) hp[u] = hidden + pair_source(ld_h, 0, n, wave + 4 * u, lane);
+  const int back = pair_back(ksteps, wave, lane);
   auto issue = [&](int slot, int pair) {
     const int p = pair < npairs ? pair : npairs - 1;
-    const int64_t k = static_cast<int64_t>(p) * kPair;
-    const bool end = p == npairs - 1;
+    const int64_t k = static_cast<int64_t>(p) * kPair - (p == npairs - 1 ? back : 0);
+    uint8_t* d = sm.s[slot] + wave * 1024;
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
-      load_lds16<true>(wp[u] + k - (end ? back_w : 0), sm.s[slot] + (wave + 8 * u) * 1024);
-    if (has_h) {
+    for (int u = 0; u < 4; ++u) load_lds16<true>(wp[u] + k, d + u * 4096);
 #pragma unroll
-      for (int u = 0; u < NH; ++u)
-        load_lds16<false>(hp[u] + k - (end ? back_h : 0),
-                          sm.s[slot] + kV * kPair + (wave + 8 * u) * 1024);
-    }
+    for (int u = 0; u < NB; ++u) load_lds16<false>(hp[u] + k, d + kVT * kPair + u * 4096);
   };
   const int row = lane % 32, hf = lane / 32;
   const int sw = swzp(row);
@@ -414,14 +418,11 @@ __device__ __forceinline__ void q8_mainloop_narrow(SmemNarrowQ8<NB>& sm,
   // every wave, and nobody reads slot (p - 1) % S any more, which the pair
   // S - 1 ahead then takes.
   for (int p = 0; p < npairs; ++p) {
-    if (has_h)
-      wait_vm_lgkm0<(S - 2) * (4 + NH)>();
-    else
-      wait_vm_lgkm0<(S - 2) * 4>();
+    wait_vm_lgkm0<(S - 2) * (4 + NB)>();
     __builtin_amdgcn_s_barrier();
     issue((p + S - 1) % S, p + S - 1);
     const uint8_t* w_ = sm.s[p % S] + (wave * 32 + row) * kPair;
-    const uint8_t* h_ = sm.s[p % S] + (kV + row) * kPair;
+    const uint8_t* h_ = sm.s[p % S] + (kVT + row) * kPair;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       if (u == 2 && 2 * p + 1 >= ksteps) break;
@@ -437,19 +438,21 @@ __device__ __forceinline__ void q8_mainloop_narrow(SmemNarrowQ8<NB>& sm,
 }
 
 template <int NB, bool ENT>
-__global__ __launch_bounds__(kQThreads) void q8_stats_narrow(
+__global__ __launch_bounds__(kNThreads) void q8_stats_narrow(
     const uint8_t* __restrict__ hidden, int64_t ld_h, const float* __restrict__ hs,
     const uint8_t* __restrict__ weight, int64_t ld_w, const float* __restrict__ ws, int64_t n,
-    int64_t v, int ksteps, int vblocks, const void* __restrict__ tgt, int32_t tgt32,
+    int64_t v, int ksteps, int ntiles, const void* __restrict__ tgt, int32_t tgt32,
     int64_t ignore, float inv_t, float* __restrict__ pm, float* __restrict__ ps,
     float* __restrict__ pw, float* __restrict__ pt, float* __restrict__ z, int64_t ld_z) {
+  constexpr int R = 32 * NB;
   const Targets targets{tgt, tgt32};
   __shared__ __align__(16) SmemNarrowQ8<NB> sm;
   const int tid = threadIdx.x;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int vb = gemm::xcd_logical(blockIdx.x, vblocks);
-  const int64_t v0 = static_cast<int64_t>(vb) * kV;
-  q8_fill(sm.rd, tid, hs, ws, n, v, 0, v0, targets, ignore);
+  const int col = tid % 32, hf = (tid % kWave) / 32;
+  const int tile = gemm::xcd_logical(blockIdx.x, ntiles);
+  const int64_t v0 = static_cast<int64_t>(tile) * kVT;
+  q8_fill<R, kVT, kNThreads>(sm.rd, hs, ws, n, v, 0, v0, targets, ignore);
   f32x16 acc[1][NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j)
@@ -457,8 +460,38 @@ __global__ __launch_bounds__(kQThreads) void q8_stats_narrow(
     for (int q = 0; q < 16; ++q) acc[0][j][q] = 0.0f;
   q8_mainloop_narrow<NB>(sm, hidden, ld_h, n, weight, ld_w, v0, v, ksteps, acc);
   __syncthreads();
-  q8_epilogue<1, NB, 32 * NB, ENT>(acc, sm.rd, wave, 0, tid, 0, v0, vb, vblocks, n, v, inv_t, pm,
-                                    ps, pw, pt, z, ld_z);
+  q8_logits<1, NB, R, kVT>(acc, sm.rd, wave * 32, 0, 0, v0, n, v, inv_t, z, ld_z);
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    float m = q8_group_max(acc[0][j]);
+    m = max_exact(m, __shfl_xor(m, 32, kWave));
+    if (hf == 0) sm.max[wave][32 * j + col] = m;
+  }
+  __syncthreads();
+  auto tile_max = [&](int lr) {
+    return max_exact(max_exact(sm.max[0][lr], sm.max[1][lr]),
+                     max_exact(sm.max[2][lr], sm.max[3][lr]));
+  };
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    const int lr = 32 * j + col;
+    float t, s, w;
+    if (q8_target(acc[0][j], sm.rd.code[lr] - wave * 32, t)) pt[lr] = t;
+    q8_group_sum<ENT>(acc[0][j], tile_max(lr), s, w);
+    if (hf == 0) {
+      sm.sum[wave][lr] = s;
+      if constexpr (ENT) sm.wsum[wave][lr] = w;
+    }
+  }
+  __syncthreads();
+  for (int lr = tid; lr < R; lr += kNThreads) {
+    if (sm.rd.code[lr] == -2) continue;
+    const int64_t at = static_cast<int64_t>(lr) * ntiles + tile;
+    pm[at] = tile_max(lr);
+    ps[at] = (sm.sum[0][lr] + sm.sum[1][lr]) + (sm.sum[2][lr] + sm.sum[3][lr]);
+    if constexpr (ENT)
+      pw[at] = (sm.wsum[0][lr] + sm.wsum[1][lr]) + (sm.wsum[2][lr] + sm.wsum[3][lr]);
+  }
 }
 
 // The tile queue's counters, before the wide kernel.
@@ -476,26 +509,26 @@ void launch_q8_partials(const uint8_t* hidden, int64_t ld_h, const float* hs,
                         int64_t v, Targets targets, int64_t ignore, float* pm, float* ps,
                         float* pt, float inv_t, float* pw, float* z, int64_t ld_z, char* scratch,
                         hipStream_t s) {
-  const int vblocks = static_cast<int>((v + kV - 1) / kV);
+  const int ntiles = static_cast<int>((v + kVT - 1) / kVT);
   const int ksteps = static_cast<int>(h / kStep);
   if (n <= 128) {
     auto kern = n <= 32   ? (pw ? q8_stats_narrow<1, true> : q8_stats_narrow<1, false>)
                 : n <= 64 ? (pw ? q8_stats_narrow<2, true> : q8_stats_narrow<2, false>)
                           : (pw ? q8_stats_narrow<4, true> : q8_stats_narrow<4, false>);
-    hipLaunchKernelGGL(kern, dim3(vblocks), dim3(kQThreads), 0, s, hidden, ld_h, hs, weight, ld_w,
-                       ws, n, v, ksteps, vblocks, targets.p, targets.is32, ignore, inv_t, pm, ps,
+    hipLaunchKernelGGL(kern, dim3(ntiles), dim3(kNThreads), 0, s, hidden, ld_h, hs, weight, ld_w,
+                       ws, n, v, ksteps, ntiles, targets.p, targets.is32, ignore, inv_t, pm, ps,
                        pw, pt, z, ld_z);
     return;
   }
+  const int vblocks = static_cast<int>((v + kV - 1) / kV);
   const int mblocks = static_cast<int>((n + 255) / 256);
   int* queue = reinterpret_cast<int*>(scratch);
   hipLaunchKernelGGL(clear_queue, dim3(1), dim3(gemm::kQueueBytes / 4), 0, s, queue);
   const gemm::QueuePlan qp = gemm::queue_plan(mblocks * vblocks, xcd_cus());
   auto kern = pw ? q8_stats_wide<true> : q8_stats_wide<false>;
-  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(qp.grid)), dim3(kQThreads), 0, s,
-                     hidden, ld_h, hs, weight, ld_w, ws, n, v, ksteps,
-                     mblocks, vblocks, targets.p, targets.is32, ignore, inv_t, pm, ps, pw, pt, z,
-                     ld_z, queue, qp.queued);
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(qp.grid)), dim3(kQThreads), 0, s, hidden,
+                     ld_h, hs, weight, ld_w, ws, n, v, ksteps, mblocks, vblocks, ntiles, targets.p,
+                     targets.is32, ignore, inv_t, pm, ps, pw, pt, z, ld_z, queue, qp.queued);
 }
 
 }  // namespace itl

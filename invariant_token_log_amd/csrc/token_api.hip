@@ -66,6 +66,7 @@ StreamLayout stream_layout(int64_t n, int64_t v, int32_t dtype, int32_t w, int32
 // and the chunk's logits.
 struct HeadLayout {
   int64_t rc, ntiles, ld_z;
+  int tile;  // vocabulary columns of a statistic tile
   bool single, own_z;
   size_t pm, ps, pw, pt, act, hb, z, total;
 };
@@ -80,7 +81,8 @@ HeadLayout head_layout(int64_t n, int64_t h, int64_t v, int64_t m, int32_t top_k
   const int64_t want = row_chunk > 0 ? row_chunk : kDefaultRows;
   l.rc = l.own_z ? (want + 255) / 256 * 256 : n;
   if (l.rc > n) l.rc = n;
-  l.ntiles = (v + itl::kLinearTile - 1) / itl::kLinearTile;
+  l.tile = flags & LOGP_TOKEN_Q8 ? itl::kQ8Tile : itl::kLinearTile;
+  l.ntiles = (v + l.tile - 1) / l.tile;
   l.ld_z = (v + 7) / 8 * 8;
   const size_t rows = static_cast<size_t>(l.rc);
   const size_t table = ws_round(rows * static_cast<size_t>(l.ntiles) * 4);
@@ -179,7 +181,7 @@ void run_head(const HeadArgs& a, const HeadLayout& l, char* ws, hipStream_t s) {
                                   ld_z, a.wblk, reinterpret_cast<uint16_t*>(ws + l.hb), s);
     const bool read_z = !l.single && z;
     const int zdt = z_bf16 ? itl::kBF16 : itl::kF32;
-    itl::launch_token_finish(zdt, read_z && rows_aligned16(z, ld_z, z_bf16 ? 2 : 4), true,
+    itl::launch_token_finish(zdt, read_z && rows_aligned16(z, ld_z, z_bf16 ? 2 : 4), l.tile,
                              read_z ? z : nullptr, ld_z, a.inv_t, pt, rows, a.v, tok, ntiles, pm,
                              ps, pw, pm, ntiles, a.top_k,
                              out_rows(a.out, r0, a.tok.m, a.top_k), s);

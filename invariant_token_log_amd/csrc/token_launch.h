@@ -48,11 +48,11 @@ void launch_token_partials(int dtype, bool vec, int chunks, const void* logits, 
                            int64_t n, int64_t v, const TokenView& tok, int ntiles, float* pm,
                            float* ps, float* pw, uint32_t* gm, hipStream_t s);
 
-// Merge, alternatives and outputs.  vocab_tiles: gm is the [n, T] table of
-// the LM head's 256-column tile maxima (x then holds fp32 or bf16 logits);
-// else the streamed rows' keys.  x null: m = 1, top_k = 0, and pt
+// Merge, alternatives and outputs.  head_tile 256 or 128: gm is the [n, T]
+// table of an LM head's tile maxima (x then holds fp32 or, at 256, bf16
+// logits); 0: the streamed rows' keys.  x null: m = 1, top_k = 0, and pt
 // holds the token's logit.
-void launch_token_finish(int dtype, bool vec, bool vocab_tiles, const void* x, int64_t ld,
+void launch_token_finish(int dtype, bool vec, int head_tile, const void* x, int64_t ld,
                          float inv_t, const float* pt, int64_t n, int64_t v, const TokenView& tok,
                          int ntiles, const float* pm, const float* ps, const float* pw,
                          const void* gm, int64_t groups, int top_k, const TokenOut& out,

@@ -161,9 +161,56 @@ __global__ __launch_bounds__(kPartBlock) void token_partials_kernel(
   }
 }
 
+// The 8-bit head's merge (its own arithmetic, so without merge_lse_t's one
+// ascending chain, whose broadcast reads took 100 us for 4096 rows of 1187
+// tiles): lane l folds tiles l, l + 64, ... in ascending order, the wave adds
+// up in a butterfly.  All lanes return the lse (and H).
+template <bool ENT>
+__device__ __forceinline__ float merge_tree(const float* m, const float* s, const float* w,
+                                            int ntiles, int lane, float* ent) {
+  constexpr int U = 20;  // 1280 tiles in registers, about 164000 columns
+  float mr[U], sr[U], wr[ENT ? U : 1];
+  float mx = -INFINITY, acc = 0.0f, b = 0.0f;
+  const bool one = ntiles <= U * kWave;
+  auto load = [&](int k0, bool all) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + u * kWave + lane;
+      mr[u] = m[k < ntiles ? k : 0];
+      if (all) {
+        sr[u] = s[k < ntiles ? k : 0];
+        if constexpr (ENT) wr[u] = w[k < ntiles ? k : 0];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (k0 + u * kWave + lane >= ntiles) mr[u] = -INFINITY;
+  };
+  for (int k0 = 0; k0 < ntiles; k0 += U * kWave) {
+    load(k0, one);
+#pragma unroll
+    for (int u = 0; u < U; ++u) mx = max_exact(mx, mr[u]);
+  }
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) mx = max_exact(mx, __shfl_xor(mx, o, kWave));
+  for (int k0 = 0; k0 < ntiles; k0 += U * kWave) {
+    if (!one) load(k0, true);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (mr[u] != -INFINITY) {  // a tile of masked columns only holds nothing
+        const float e = exp_sub(mr[u], mx);
+        acc = fmaf(sr[u], e, acc);
+        if constexpr (ENT) b = fmaf(fmaf(sr[u], mr[u] - mx, wr[u]), e, b);
+      }
+  }
+  const float la = log_nat(wave_sum(acc));
+  if constexpr (ENT) *ent = la - wave_sum(b) / wave_sum(acc);
+  return mx + la;
+}
+
 // ---------------------------------------------------------------------------
 // Finish.  One wave a row merges the tile statistics (merge_lse_t: the bits of
-// logp_fwd) and writes lse, entropy and the given tokens; with alternatives it
+// logp_fwd; merge_tree for the 8-bit head) and writes lse, entropy and the given tokens; with alternatives it
 // then selects them, or, with few rows (per = 2), a second wave does so
 // meanwhile and takes the lse at the end.
 //   x          the row's logits ([n, ld], row r at x + r * ld), or null: then
@@ -179,26 +226,26 @@ __global__ __launch_bounds__(kPartBlock) void token_partials_kernel(
 // bit mask and reads the few marked ones again instead of carrying an unrolled
 // append.
 // ---------------------------------------------------------------------------
-// groups a lane holds at once: 1280 of 128 columns, or 640 vocabulary tiles of
-// 256, each about 164000 columns
-template <bool HEAD>
-constexpr int kKeys = HEAD ? 10 : 20;
+// groups a lane holds at once: 640 of 256 columns or 1280 of 128, about 164000
+// columns
+template <int GW>
+constexpr int kKeys = GW == 256 ? 10 : 20;
 
 // Order keys of the groups b0 + 64 c + lane; 0 (below every key) past the last.
 template <bool HEAD>
 __device__ __forceinline__ uint32_t group_key(const uint32_t* g, int64_t i) {
   return HEAD ? order_key(__uint_as_float(g[i])) : g[i];
 }
-template <bool HEAD>
+template <int GW, bool HEAD>
 __device__ __forceinline__ void load_keys(const uint32_t* g, int64_t b0, int64_t groups, int lane,
-                                          uint32_t (&key)[kKeys<HEAD>]) {
+                                          uint32_t (&key)[kKeys<GW>]) {
 #pragma unroll
-  for (int c = 0; c < kKeys<HEAD>; ++c) {
+  for (int c = 0; c < kKeys<GW>; ++c) {
     const int64_t i = b0 + c * kWave + lane;
     key[c] = g[i < groups ? i : 0];
   }
 #pragma unroll
-  for (int c = 0; c < kKeys<HEAD>; ++c) {
+  for (int c = 0; c < kKeys<GW>; ++c) {
     const uint32_t k = HEAD ? order_key(__uint_as_float(key[c])) : key[c];
     key[c] = b0 + c * kWave + lane < groups ? k : 0u;
   }
@@ -209,7 +256,7 @@ __device__ __forceinline__ void load_keys(const uint32_t* g, int64_t b0, int64_t
 template <typename T, int GW, bool VEC, bool HEAD>
 __device__ __forceinline__ void select_top(TopStage& st, const T* row, float inv_t, uint32_t v,
                                            const uint32_t* g, int64_t groups, int top_k,
-                                           uint32_t (&key)[kKeys<HEAD>], int lane) {
+                                           uint32_t (&key)[kKeys<GW>], int lane) {
   constexpr int E = Elt<T>::kPerChunk;
   constexpr int LPG = GW / E;            // lanes per group
   constexpr int GPW = kWave / LPG;       // groups one wave load covers
@@ -220,12 +267,12 @@ __device__ __forceinline__ void select_top(TopStage& st, const T* row, float inv
   };
   // 1. A bound: the k-th greatest of 256 maxima, four a lane, over disjoint
   // sets of groups.  At least k groups reach it.
-  const bool one_block = groups <= kKeys<HEAD> * kWave;
+  const bool one_block = groups <= kKeys<GW> * kWave;
   uint32_t best[4] = {0, 0, 0, 0};
-  for (int64_t b0 = 0; b0 < groups; b0 += kKeys<HEAD> * kWave) {
-    if (b0 > 0) load_keys<HEAD>(g, b0, groups, lane, key);
+  for (int64_t b0 = 0; b0 < groups; b0 += kKeys<GW> * kWave) {
+    if (b0 > 0) load_keys<GW, HEAD>(g, b0, groups, lane, key);
 #pragma unroll
-    for (int c = 0; c < kKeys<HEAD>; ++c) best[c % 4] = max(best[c % 4], key[c]);
+    for (int c = 0; c < kKeys<GW>; ++c) best[c % 4] = max(best[c % 4], key[c]);
   }
   const uint32_t bound = max(wave_bound(best, top_k), 1u);
   // 2. The k greatest groups (or all, when there are fewer).  Few groups
@@ -235,11 +282,11 @@ __device__ __forceinline__ void select_top(TopStage& st, const T* row, float inv
   int reach = 0, place = 0;
   if (one_block) {
 #pragma unroll
-    for (int c = 0; c < kKeys<HEAD>; ++c) reach += key[c] >= bound;
+    for (int c = 0; c < kKeys<GW>; ++c) reach += key[c] >= bound;
   }
   if (one_block && top_reserve(st, list, reach, place)) {
 #pragma unroll
-    for (int c = 0; c < kKeys<HEAD>; ++c)
+    for (int c = 0; c < kKeys<GW>; ++c)
       if (key[c] >= bound)
         st.e[place++] = compose(key[c], static_cast<uint32_t>(c * kWave + lane));
   } else {
@@ -345,9 +392,9 @@ __global__ __launch_bounds__(kFinBlock) void token_finish_kernel(
     const int64_t r = r0 + slot;
     bool live = r < n;
     // The group keys or the given tokens are on their way first.
-    uint32_t key[kKeys<HEAD>];
+    uint32_t key[kKeys<GW>];
     const uint32_t* g = gm + r * groups;
-    if (live && selects) load_keys<HEAD>(g, 0, groups, lane, key);
+    if (live && selects) load_keys<GW, HEAD>(g, 0, groups, lane, key);
     int64_t t0 = live && lane < tok.m ? tok.at(r, lane) : tok.ignore;
     if (live && tok.m > 0 && __builtin_amdgcn_ballot_w64(t0 != tok.ignore) == 0)
       live = row_active(tok, r, lane);
@@ -370,8 +417,12 @@ __global__ __launch_bounds__(kFinBlock) void token_finish_kernel(
       if (t0 != tok.ignore && t0 >= 0 && t0 < v) x0 = x ? logit(t0) : pt[r];
       float h = 0.0f;
       const int64_t at = r * ntiles;
-      const float L = merge_lse_t<ENT, HEAD ? 10 : 1>(pm + at, ps + at, pw + at, ntiles, 1,
-                                                      stage[wave].merge, &h);
+      float L;
+      if constexpr (HEAD && GW == 128)
+        L = merge_tree<ENT>(pm + at, ps + at, pw + at, ntiles, lane, &h);
+      else
+        L = merge_lse_t<ENT, HEAD ? 10 : 1>(pm + at, ps + at, pw + at, ntiles, 1,
+                                            stage[wave].merge, &h);
       if (lane == 0) {
         row_lse[slot] = L;
         if (out.lse) out.lse[r] = L;
@@ -655,7 +706,7 @@ void launch_token_partials(int dtype, bool vec, int chunks, const void* logits, 
 #undef ITL_PARTS
 }
 
-void launch_token_finish(int dtype, bool vec, bool vocab_tiles, const void* x, int64_t ld,
+void launch_token_finish(int dtype, bool vec, int head_tile, const void* x, int64_t ld,
                          float inv_t, const float* pt, int64_t n, int64_t v, const TokenView& tok,
                          int ntiles, const float* pm, const float* ps, const float* pw,
                          const void* gm, int64_t groups, int top_k, const TokenOut& out,
@@ -667,7 +718,9 @@ void launch_token_finish(int dtype, bool vec, bool vocab_tiles, const void* x, i
                                          groups, top_k, out, s)
   // a group is 16 lanes' chunks of a streamed row, or a vocabulary tile of the
   // LM head
-  if (vocab_tiles) {
+  if (head_tile == 128) {
+    ITL_FIN(float, 128, true);
+  } else if (head_tile) {
     if (dtype == kF32) ITL_FIN(float, kLinearTile, true);
     else ITL_FIN(uint16_t, kLinearTile, true);
   } else {
