@@ -220,8 +220,6 @@ def _q8_operand(q, name):
     if (q.scale.dtype != torch.float32 or q.scale.shape != q.data.shape[:1]
             or not q.scale.is_contiguous() or q.scale.device != q.data.device):
         raise TypeError(f"{name}.scale must be contiguous float32 with one entry per row")
-    if not q.data.is_cuda:
-        raise ValueError("tensors must be on a ROCm device")
     return q.data.shape
 
 
@@ -250,8 +248,10 @@ def linear_token_logp_fwd(hidden, weight, token_ids=None, top_k=0, ignore_index=
             raise ValueError("the 8-bit head takes no round_logits, prepared_weight or logits_out")
         n, h = _q8_operand(hidden, "hidden")
         v, h2 = _q8_operand(weight, "weight")
-        if h2 != h or weight.data.device != hidden.data.device:
-            raise ValueError("hidden and weight must share H and the device")
+        if h2 != h:
+            raise ValueError("hidden and weight must share H")
+        if not hidden.data.is_cuda or weight.data.device != hidden.data.device:
+            raise ValueError("hidden and weight must be on one ROCm device")
         ld_h = hidden.data.stride(0) if n > 1 else h
         ld_w = weight.data.stride(0) if v > 1 else h
         dev, pw = hidden.data.device, None
