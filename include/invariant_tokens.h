@@ -74,8 +74,9 @@ int32_t token_logp_fwd(const void* logits, int32_t dtype, int64_t n, int64_t v, 
  *                             - G[r] p [- gH[r] p (x - lse[r] + H[r])]),
  *   p = exp(x - lse[r]),  G[r] = the sum of all of r's entry gradients.
  *   tokens, m, ignore_index: the forward's.
- *   top_ids, top_k: the forward's alternatives (ids outside [0, v) are left
- *                 out); NULL and 0 when no gradient comes in for them.
+ *   top_ids, top_k: the forward's alternatives (negative ids, as padding
+ *                 rows have, are left out); NULL and 0 when no gradient comes
+ *                 in for them.
  *   lse           fp32 [n] of the forward.
  *   grad_logp     fp32 [n, m] (NULL only when m = 0).
  *   grad_top_logp fp32 [n, top_k] (NULL only when top_k = 0).

@@ -9,6 +9,7 @@ rest and its status becomes a LogpError.
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from ._lib import check
@@ -192,6 +193,7 @@ class _TokenLogp(torch.autograd.Function):
         return tuple(r)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g, _lse, g_entropy, g_top, _ids):
         logits, token_ids, lse, entropy, top_ids = ctx.saved_tensors
         if token_ids is not None and g is None:
@@ -371,6 +373,7 @@ class _LinearTokenLogp(torch.autograd.Function):
         return tuple(r)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g, _lse, g_entropy, g_top, _ids):
         hidden, weight, token_ids, z, logp, lse, entropy, top_logp, top_ids = ctx.saved_tensors
         ignore_index, temperature, round_logits, prepared = ctx.options
@@ -491,15 +494,15 @@ class _RmsNorm(torch.autograd.Function):
         return (y, s) if ctx.fused else y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, gy, gs=None):
         s, weight, rstd = ctx.saved_tensors
         need_w = ctx.needs_input_grad[1]
         if gy is None:  # only the stored sum was used
             return gs, torch.zeros_like(weight) if need_w else None, gs if ctx.fused else None, None
-        gy = gy if gy.stride(-1) == 1 else gy.contiguous()
-        if gs is not None and gs.stride(-1) != 1:
-            gs = gs.contiguous()
-        dx, dw = rms_norm_bwd(s, weight, rstd, gy, gs, need_dweight=need_w)
+        # gradients may come in broadcast (a row for all rows, one value for all)
+        gs = gs.contiguous() if gs is not None else None
+        dx, dw = rms_norm_bwd(s, weight, rstd, gy.contiguous(), gs, need_dweight=need_w)
         return dx, dw, dx if ctx.fused else None, None
 
 

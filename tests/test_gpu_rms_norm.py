@@ -146,6 +146,23 @@ def test_autograd_and_differences():
     assert a.grad.shape == (2, 2, h)
 
 
+def test_broadcast_gradients():
+    """A gradient that is one row or one value for all rows (an expanded
+    tensor), for y and for the stored sum."""
+    x, xd, r, rd, w = make(6, 80, "fp32", seed=9)
+    g = torch.randn(80, generator=torch.Generator().manual_seed(2)).to(dev())
+    wd = w.to(dev())
+
+    def grads(gy, gs):
+        a = xd.clone().requires_grad_()
+        y, s = itl.rms_norm(a, wd, residual=rd, eps=EPS)
+        torch.autograd.backward([y, s], [gy, gs])
+        return a.grad
+
+    full = grads(g.expand(6, 80).contiguous(), torch.full((6, 80), 0.5, device=dev()))
+    assert torch.equal(grads(g.expand(6, 80), torch.tensor(0.5, device=dev()).expand(6, 80)), full)
+
+
 def e4m3(d):
     return d.clamp(-448.0, 448.0).float().to(torch.float8_e4m3fn).double()
 

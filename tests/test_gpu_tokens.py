@@ -261,6 +261,23 @@ def test_parts_of_the_gradient_may_be_absent():
     assert lead.logp.shape == (2, 2, 2) and lead.top_ids.shape == (2, 2, 3)
 
 
+def test_second_derivative_is_refused():
+    _, view, tok = make(2, 50, 1, "fp32", seed=1)
+    leaf = view.clone().requires_grad_()
+    d, = torch.autograd.grad(itl.batch_invariant_token_logp(leaf, tok.to(dev())).logp.square().sum(), leaf,
+                             create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        d.sum().backward()
+
+
+def test_one_row_without_leading_dimensions():
+    x, view, tok = make(1, 700, 3, "bf16", seed=13, drop=0.0)
+    one = itl.token_logp_fwd(view[0], tok[0].to(dev()), top_k=4)
+    two = itl.token_logp_fwd(view, tok.to(dev()), top_k=4)
+    assert one.logp.shape == (3,) and one.top_ids.shape == (4,)
+    assert torch.equal(one.logp, two.logp[0]) and torch.equal(one.top_ids, two.top_ids[0])
+
+
 def test_empty_batch():
     x = torch.empty(0, 100, dtype=torch.bfloat16, device=dev())
     r = itl.token_logp_fwd(x, torch.empty(0, 3, dtype=torch.int64, device=dev()), top_k=2,
