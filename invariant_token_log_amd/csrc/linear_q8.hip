@@ -249,14 +249,14 @@ __device__ __forceinline__ void q8_mainloop(SmemWide& sm, const uint8_t* __restr
   const int back = (ksteps & 1) && lchunk >= kStep ? kStep : 0;
   const int wlast = static_cast<int>(min(v - 1 - v0, int64_t{255}));
   const int hlast = static_cast<int>(min(n - 1 - m0, int64_t{255}));
-  auto issue = [&](int p) {
+  auto issue = [&](int slot, int p) {  // into slot % 2
     if constexpr (LOADER) {
       const int64_t k = static_cast<int64_t>(p) * kPair;
       const uint8_t* w0 = W + v0 * ld_w + k;
       const uint8_t* h0 = H + m0 * ld_h + k;
       const uint32_t c = lchunk - (p == npairs - 1 ? back : 0);
       const uint32_t lw = static_cast<uint32_t>(ld_w), lh = static_cast<uint32_t>(ld_h);
-      uint8_t* d = sm.s[p % 2] + wave * 1024;
+      uint8_t* d = sm.s[slot % 2] + wave * 1024;
 #pragma unroll
       for (int u = 0; u < 8; ++u)
         load_lds16<false>(w0 + (min(lrow + 32 * u, wlast) * lw + c), d + u * 4096);
@@ -278,16 +278,43 @@ __device__ __forceinline__ void q8_mainloop(SmemWide& sm, const uint8_t* __restr
     for (int i = 0; i < 4; ++i)
       fw[i] = *reinterpret_cast<const i32x4*>(base + wofs + 32 * i * kPair);
   };
-  issue(0);
-  if (npairs > 1) {
-    issue(1);
-    wait_vm<LOADER ? 16 : 0>();
-  } else {
-    wait_vm<0>();
-  }
+  // Past the end the last pair is loaded again into the slot that is no longer
+  // read, so that every pair of the loop is alike.
+  issue(0, 0);
+  issue(1, npairs > 1 ? 1 : 0);
+  wait_vm<LOADER ? 16 : 0>();
   __builtin_amdgcn_s_barrier();
   read(0, 0, xw, xh);
-  for (int p = 0; p < npairs; ++p) {
+  // Order inside a block: the next chunk's six reads, then the conversions of
+  // one operand pair ahead of its products (left alone, the compiler reads a
+  // chunk right before its use and the matrix cores wait for LDS).
+#define ITL_Q8_ORDER                                                                            \
+  __builtin_amdgcn_sched_group_barrier(0x100, 6, 0);                                            \
+  __builtin_amdgcn_sched_group_barrier(0x002, 12, 0);                                           \
+  _Pragma("unroll") for (int o = 0; o < 7; ++o) {                                               \
+    __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);                                          \
+    __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);                                          \
+  }                                                                                             \
+  __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+  for (int p = 0; p + 1 < npairs; ++p) {
+    read(p, 1, yw, yh);
+    mfma_q8<4, 2>(xw, xh, acc);
+    ITL_Q8_ORDER
+    read(p, 2, xw, xh);
+    mfma_q8<4, 2>(yw, yh, acc);
+    ITL_Q8_ORDER
+    read(p, 3, yw, yh);
+    mfma_q8<4, 2>(xw, xh, acc);
+    ITL_Q8_ORDER
+    wait_vm_lgkm0<0>();  // this wave's reads of pair p, its loads of pair p + 1
+    __builtin_amdgcn_s_barrier();
+    issue(p, p + 2 < npairs ? p + 2 : npairs - 1);
+    read(p + 1, 0, xw, xh);
+    mfma_q8<4, 2>(yw, yh, acc);
+    ITL_Q8_ORDER
+  }
+  {
+    const int p = npairs - 1;
     read(p, 1, yw, yh);
     mfma_q8<4, 2>(xw, xh, acc);
     if (2 * p + 1 < ksteps) {
@@ -296,14 +323,9 @@ __device__ __forceinline__ void q8_mainloop(SmemWide& sm, const uint8_t* __restr
       read(p, 3, yw, yh);
       mfma_q8<4, 2>(xw, xh, acc);
     }
-    if (p + 1 < npairs) {
-      wait_vm_lgkm0<0>();  // this wave's reads of pair p, its loads of pair p + 1
-      __builtin_amdgcn_s_barrier();
-      if (p + 2 < npairs) issue(p + 2);
-      read(p + 1, 0, xw, xh);
-    }
     mfma_q8<4, 2>(yw, yh, acc);
   }
+#undef ITL_Q8_ORDER
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
