@@ -372,7 +372,7 @@ __device__ __forceinline__ void select_top(TopStage& st, const T* row, float inv
 }
 
 template <typename T, int GW, bool VEC, bool ENT, bool HEAD>
-__global__ __launch_bounds__(kFinBlock) void token_finish_kernel(
+__global__ __launch_bounds__(kFinBlock, GW == 256 ? 4 : 1) void token_finish_kernel(
     const T* __restrict__ x, int64_t ld, float inv_t, const float* __restrict__ pt, int64_t n,
     int64_t v, TokenView tok, int ntiles, const float* __restrict__ pm,
     const float* __restrict__ ps, const float* __restrict__ pw, const uint32_t* __restrict__ gm,
@@ -464,7 +464,9 @@ __global__ __launch_bounds__(kFinBlock) void token_finish_kernel(
 // twice.
 // Bound by memory, but a wave first has to know that its row is no padding:
 // the entries' load, then the logits' (several chunks a lane, so that the wait
-// for the entries is shared), and G is summed while the logits arrive.
+// for the entries is shared), and G is summed while the logits arrive.  4096 x
+// 128256 bf16 with 16 entries a row and the entropy term takes 370 us (5.7 TB/s)
+// with four chunks a lane; two 465, three 460, six 394, eight 606 (registers).
 // ---------------------------------------------------------------------------
 constexpr int kBwdChunks = 4;
 

@@ -6,10 +6,10 @@ of products exact in fp32, so the alternatives' order is exact and logp and lse
 keep the logits' bound.  Gradients: dz rounds to bf16 once, so dhidden and
 dweight are within 2^-8 of sum |dz||W| (|dz||h|), plus 1e-3 of what an entry's
 own column carries and 1e-6, as for linear_logp's backward; bf16 outputs round
-by 2^-8 more.  8-bit head: products of e4m3 values are exact in fp32; the matrix
-instruction adds 64 of them at once and H / 64 such sums follow, within (64 +
-H / 64) 2^-23 sum |h w| of the exact logit, which moves logp and lse by at most
-twice that."""
+by 2^-8 more.  8-bit head: products of e4m3 values are exact in fp32; a matrix
+instruction adds 16 of them and H / 16 such sums follow, within (16 + H / 16)
+2^-23 sum |h w| of the exact logit, which moves logp and lse by at most twice
+that."""
 
 import pytest
 import torch
@@ -163,7 +163,7 @@ def test_8bit_head(n, h, v, m, k):
     hd = a.data.cpu().double() * a.scale.cpu().double()[:, None]
     wd = b.data.cpu().double() * b.scale.cpu().double()[:, None]
     z = hd @ wd.T / 0.9
-    extra = float((2 * (64 + h / 64) * 2.0 ** -23 * (hd.abs() @ wd.abs().T)).max()) / 0.9
+    extra = float((2 * (16 + h / 16) * 2.0 ** -23 * (hd.abs() @ wd.abs().T)).max()) / 0.9
     r = itl.linear_token_logp_fwd(a, b, tok.to(dev()), top_k=k, temperature=0.9, return_entropy=True)
     ref = token_scores(z, tok, k)
     close(r.logp, ref["logp"], "logp", extra)
