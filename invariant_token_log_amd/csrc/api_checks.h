@@ -1,5 +1,4 @@
-// Host-side argument checks and workspace helpers shared by the entry points
-// of the C ABI.
+// Host-side argument checks and workspace helpers of token_api.hip.
 #pragma once
 
 #include <hip/hip_runtime.h>
