@@ -198,8 +198,9 @@ int32_t rms_norm_fwd(const void* x, int64_t ld_x, const void* residual, int64_t 
 
 /*
  * rms_norm_fwd with 8-bit rows as output:
- *   t = s * rstd * weight (fp32),  scale[r] = max|t| / 448,
- *   q = RNE_e4m3(t * (448 / max|t|))       (a row of zeros: scale 0, q 0)
+ *   t = s * rstd * weight (fp32),  a = max(max|t|, 448 * 2^-126),
+ *   scale[r] = a / 448,  q = RNE_e4m3(t * (448 / a))
+ *                                          (a row of zeros: scale 0, q 0)
  * q_out [n, ld_q] bytes, scale_out fp32 [n].  A row with an infinity or a NaN
  * gives NaN.  weight NULL: no norm, t = s (8-bit rows of a weight matrix).
  */

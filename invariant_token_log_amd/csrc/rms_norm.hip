@@ -2,8 +2,8 @@
 // gradient, on gfx950.
 //
 //   s = rne(x + residual);  rstd = 1 / sqrt(mean(s^2) + eps)
-//   y = rne(s rstd w),  or  t = s rstd w,  scale = max|t| / 448,
-//                           q = rne_e4m3(t * (448 / max|t|))
+//   y = rne(s rstd w),  or  t = s rstd w,  a = max(max|t|, 448 * 2^-126),
+//                           scale = a / 448,  q = rne_e4m3(t * (448 / a))
 //   u = s rstd;  dx = rne(ds + rstd (dy w - u mean(dy w u)));  dw = sum_r dy u
 //
 // Bound by memory: every element is read and written once, so a row stays in
@@ -28,6 +28,9 @@ namespace {
 
 constexpr int kE = 8;             // elements per chunk, every type
 constexpr float kE4m3Max = 448.0f;
+// Below this magnitude a row's scale stays at 2^-126: its own would be
+// subnormal and the factor 448 / max|t| pass fp32's range.
+constexpr float kLeastMost = 0x1.cp-118f;
 
 template <typename T>
 constexpr int kRaw = sizeof(T) == 4 ? 2 : 1;  // 16-byte pieces per chunk
@@ -200,6 +203,7 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void rms_norm_kernel(
     most = team_reduce<TEAM, true>(most, buf[1][team]);
     nan = team_reduce<TEAM, true>(nan, buf[2][team]);
     if (nan != 0.0f) most = __uint_as_float(0x7fc00000u);
+    if (most > 0.0f && most < kLeastMost) most = kLeastMost;
     if (t == 0) scale[r] = most / kE4m3Max;
     inv = most == 0.0f ? 0.0f : kE4m3Max / most;
   }

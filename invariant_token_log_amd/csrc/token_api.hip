@@ -448,8 +448,8 @@ int32_t rms_norm_fwd(const void* x, int64_t ld_x, const void* residual, int64_t 
                      int64_t ld_y, void* sum_out, int64_t ld_s, float* rstd_out,
                      void* hip_stream) {
   if (!itl::known_dtype(dtype)) return LOGP_ERR_DTYPE;
-  if (n < 0 || n > INT32_MAX || h < 1 || h > itl::kMaxNorm || ld_x < h || ld_y < h || (residual && ld_r < h) ||
-      (sum_out && ld_s < h))
+  if (n < 0 || n > INT32_MAX || h < 1 || h > itl::kMaxNorm || ld_x < h || ld_y < h ||
+      (residual && ld_r < h) || (sum_out && ld_s < h))
     return LOGP_ERR_SHAPE;
   if (!(std::isfinite(eps) && eps >= 0.0f)) return LOGP_ERR_VALUE;
   if (n == 0) return LOGP_OK;
@@ -465,8 +465,8 @@ int32_t rms_norm_q8_fwd(const void* x, int64_t ld_x, const void* residual, int64
                         void* q_out, int64_t ld_q, float* scale_out, void* sum_out, int64_t ld_s,
                         void* hip_stream) {
   if (!itl::known_dtype(dtype)) return LOGP_ERR_DTYPE;
-  if (n < 0 || n > INT32_MAX || h < 1 || h > itl::kMaxNorm || ld_x < h || ld_q < h || (residual && ld_r < h) ||
-      (sum_out && ld_s < h))
+  if (n < 0 || n > INT32_MAX || h < 1 || h > itl::kMaxNorm || ld_x < h || ld_q < h ||
+      (residual && ld_r < h) || (sum_out && ld_s < h))
     return LOGP_ERR_SHAPE;
   if (!(std::isfinite(eps) && eps >= 0.0f)) return LOGP_ERR_VALUE;
   if (n == 0) return LOGP_OK;

@@ -4,6 +4,11 @@ tokens, their gradients, 8-bit rows and the root-mean-square norm.
 Argument marshalling only (the C ABI is include/invariant_tokens.h): PyTorch
 supplies device memory and the current HIP stream; the library checks the
 rest and its status becomes a LogpError.
+
+Every function can be captured into a HIP graph.  A training step is captured
+with the *_bwd functions, or through autograd while no eager autograd graph of
+the same leaves is alive (torch ties a leaf's accumulation to the stream that
+it was first used on, and would wait there for the capturing one).
 """
 
 from typing import NamedTuple, Optional
@@ -529,8 +534,8 @@ def _quantize(x, weight, residual, eps, sum_out):
 
 def rms_norm_quantized(x, weight, residual=None, eps=1e-6, sum_out=None):
     """rms_norm_fwd with 8-bit rows as output: (QuantizedRows [N, H], s).  A
-    row's scale is its greatest magnitude / 448; the norm's fp32 result is
-    rounded once, to 8 bits."""
+    row's scale is its greatest magnitude / 448, at least 2^-126 (0 for a row
+    of zeros); the norm's fp32 result is rounded once, to 8 bits."""
     return _quantize(x, weight, residual, eps, sum_out)
 
 

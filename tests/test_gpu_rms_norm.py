@@ -206,6 +206,21 @@ def test_quantized_edges():
     assert (y[1] == 0).all()
 
 
+def test_quantized_tiny_rows():
+    """Rows whose 448 / max|t| would pass fp32's range: the scale stays at
+    2^-126.  Half a step of e4m3 is 2^-4 of the value, 2^-10 below 2^-6; the
+    fp32 factor and product move a value by less than 2^-20 of itself."""
+    x = torch.randn(5, 300, generator=torch.Generator().manual_seed(1))
+    x = x * torch.tensor([1e-30, 1e-36, 1e-37, 1e-38, 1e-41])[:, None]
+    x[:, 5] = 0.0
+    q = itl.quantize_rows(x.to(dev()))
+    scale = x.double().abs().amax(1).clamp(min=448 * 2.0 ** -126) / 448
+    assert ((q.scale.double().cpu() - scale).abs() <= 2.0 ** -23 * scale).all()
+    val = q.data.double().cpu() * q.scale.double().cpu()[:, None]
+    bound = x.double().abs() * (2.0 ** -4 + 2.0 ** -20) + scale[:, None] * 2.0 ** -10 * (1 + 2.0 ** -20)
+    assert ((val - x.double()).abs() <= bound).all()
+
+
 def test_empty_batch():
     x = torch.empty(0, 64, dtype=torch.bfloat16, device=dev())
     w = torch.ones(64, dtype=torch.bfloat16, device=dev())
