@@ -94,7 +94,14 @@ def _out(x, shape, dtype, device, name):
 class _Outputs:
     """Output buffers of a forward, checked or allocated."""
 
+    NAMES = ("logp_out", "lse_out", "entropy_out", "top_logp_out", "top_ids_out")
+
     def __init__(self, n, lead, m, k, entropy, device, given):
+        for name in given:
+            if name not in self.NAMES:
+                raise TypeError(f"unexpected argument {name}")
+        if not entropy and given.get("entropy_out") is not None:
+            raise ValueError("entropy_out needs return_entropy")
         f = torch.float32
         self.logp = _out(given.get("logp_out"), (*lead, m), f, device, "logp_out")
         self.lse = _out(given.get("lse_out"), (n,), f, device, "lse_out")

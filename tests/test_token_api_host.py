@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import invariant_token_log_amd as itl
-from invariant_token_log_amd import _lib
+from invariant_token_log_amd import _lib, token_ops
 from invariant_token_log_amd.build import LIB_PATH, build
 
 P = 0x10000  # a non-NULL, 256-byte aligned address that the checks never dereference
@@ -189,3 +189,15 @@ def test_binding_refuses_before_device_work():
     for bad in (65, -1):
         with pytest.raises(ValueError, match="top_k"):
             itl.linear_token_logp_fwd(q, q, top_k=bad)
+
+
+def test_output_names():
+    """An output buffer under a name that does not exist, or of an output that
+    was not asked for, is refused rather than left unwritten."""
+    outputs = lambda ent, **given: token_ops._Outputs(2, (2,), 1, 0, ent, torch.device("cpu"), given)
+    with pytest.raises(TypeError):
+        outputs(False, logps_out=torch.empty(2, 1))
+    with pytest.raises(ValueError):
+        outputs(False, entropy_out=torch.empty(2))
+    e = torch.empty(2)
+    assert outputs(True, entropy_out=e).entropy is e
