@@ -132,8 +132,8 @@ int32_t linear_token_logp_fwd(const void* hidden, int64_t ld_h, const void* weig
                               size_t workspace_bytes, void* hip_stream);
 
 /*
- * Workspace of linear_token_logp_bwd in bytes: linear_logp_bwd's for the same
- * flags (logp_bwd_flags) and vocab_chunk, and 8 bytes a row.
+ * Workspace of linear_token_logp_bwd in bytes for the same flags
+ * (logp_bwd_flags) and vocab_chunk.
  */
 size_t linear_token_logp_bwd_workspace_bytes(int64_t n, int64_t h, int64_t v, int32_t flags,
                                              int64_t vocab_chunk);
@@ -141,6 +141,9 @@ size_t linear_token_logp_bwd_workspace_bytes(int64_t n, int64_t h, int64_t v, in
 /*
  * Backward of linear_token_logp_fwd: linear_logp_bwd with a list of entries a
  * row.  dz is rounded to bf16 once, after the entries' gradients are added.
+ * dhidden is the sum, in ascending order, of the fp32 sums over 16384 vocabulary
+ * columns each; vocab_chunk (0 = the library's default) is rounded up to a
+ * multiple of that, and any value gives the same bits.
  *   logp, top_logp: the forward's outputs ([n, m], [n, top_k]).
  *   the rest: as linear_logp_bwd and token_logp_bwd.
  */

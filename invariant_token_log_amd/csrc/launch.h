@@ -80,13 +80,15 @@ int xcd_cus();
 // offsets, -1 for a region not used; np, vp = n, v rounded up to 256.
 constexpr int64_t kDefaultChunk = 32768;
 enum { kBwdDhidden = 1, kBwdDweight = 2, kBwdPrepared = 4, kBwdSaved = 8, kBwdBf16Out = 16 };
+constexpr int64_t kDhSegment = 16384;  // columns of a segment of the token operators' dh
 struct LinearBwdLayout {
   int64_t np, vp, vc;
-  int64_t hb, ht, dz, dh32, total;
+  int64_t hb, ht, dz, dh32, parts, total;
 };
 int64_t linear_bwd_chunk(int64_t v, int64_t vocab_chunk);
+// segments: the token operators' layout (chunks of whole segments).
 LinearBwdLayout linear_bwd_layout(int64_t n, int64_t h, int64_t v, int32_t flags,
-                                  int64_t vocab_chunk);
+                                  int64_t vocab_chunk, bool segments = false);
 
 // dh [n, h] and/or dW [v, h] (either may be null) as fp32 or bf16 (bf16_out).
 // inv_t: reciprocal temperature (1 = none); ent / gent: row entropy and its
@@ -99,8 +101,8 @@ LinearBwdLayout linear_bwd_layout(int64_t n, int64_t h, int64_t v, int32_t flags
 // bits).  vocab_chunk: columns per chunk (0 = kDefaultChunk), any value
 // gives the same bits; ws: linear_bwd_layout(...).total bytes.  tokens (or
 // null): the row's target is replaced by a list of entries; targets then hold
-// the activity of launch_token_rows, grad its sums, and every chunk's dz gets
-// the entries' columns from launch_token_dz.
+// the activity of launch_token_rows, grad its sums, every chunk's dz gets the
+// entries' columns from launch_token_dz, and dh is summed in segments.
 void launch_linear_bwd(const uint16_t* hidden, int64_t ld_h, const uint16_t* weight, int64_t ld_w,
                        int64_t n, int64_t h, int64_t v, Targets targets, int64_t ignore,
                        const void* zsaved, int32_t z_bf16, int64_t ld_z,

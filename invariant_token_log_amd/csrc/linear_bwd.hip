@@ -570,6 +570,133 @@ __global__ __launch_bounds__(gemm::kThreads) void gemm_pair_kernel(GemmArgs dh, 
     gemm_pair_tile<BF16DW, gemm::kKOuterBlocked, gemm::kKContig>(st, dw, b - dh_tiles);
 }
 
+// dh of the token operators: its K walk over the vocabulary falls into segments
+// of kDhSegment columns, each a chain from zero, added in ascending order:
+//   dh = ((seg_0 + seg_1) + seg_2) + ...
+// (one chain over V / 32 steps, as linear_logp_bwd has it, takes 1.4 ms at V =
+// 151936 however few rows there are).  With few tiles (dh_in_parts) a chunk's
+// segments are tiles of their own, which leave their sums in `parts` for
+// sum_parts_kernel; with many a tile walks the segments and keeps the running
+// sum in memory.  The same bits, and a row's do not depend on n.
+constexpr int64_t kSegSteps = kDhSegment / gemm::kK;
+
+struct Segments {
+  int count;        // of the chunk
+  int64_t b;        // elements between two segments of B
+  float* sum;       // running sum between segments, or null
+  int64_t ldsum;
+  bool bf16;        // the last segment's output
+  float* parts;     // [count, m_out, n_out], or null
+};
+
+// C = Cin + A B^T: gemm_out_tile with the addition at the end of the K walk.
+template <bool LOADER, int BF>
+__device__ __forceinline__ void gemm_add_tile(gemm::Stages& st, const GemmArgs& g,
+                                              const uint16_t* A, const uint16_t* B, int b_kvalid,
+                                              int ksteps, int64_t m0, int64_t n0, const float* cin,
+                                              int64_t ldcin, void* C, int64_t ldc, bool bf16) {
+  constexpr int MI = 8, NJ = 4, WM = 128, WN = 64;
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int wm = wave / 4, wn = wave % 4;
+  const int li = lane % 16, gr = lane / 16;
+  f32x4 acc[MI][NJ];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  if constexpr (BF != gemm::kKContig)
+    gemm::mainloop_ko<gemm::kKContig, BF, LOADER>(st, A, g.lda, m0, g.arows, g.a_kvalid, B, g.ldb,
+                                                  n0, g.brows, b_kvalid, ksteps, acc);
+  else
+    gemm::mainloop_role<true, true, LOADER>(st, A, g.lda, m0, g.arows, B, g.ldb, n0, g.brows,
+                                            ksteps, acc);
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t row = m0 + wm * WM + i * 16 + 4 * gr + q;
+      if (row >= g.m_out) continue;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const int64_t col = n0 + wn * WN + j * 16 + li;
+        if (col >= g.n_out) continue;
+        const float v = cin ? cin[row * ldcin + col] + acc[i][j][q] : acc[i][j][q];
+        if (bf16)
+          static_cast<uint16_t*>(C)[row * ldc + col] = bf16_bits(v);
+        else
+          static_cast<float*>(C)[row * ldc + col] = v;
+      }
+    }
+}
+
+template <int BF>
+__device__ __forceinline__ void gemm_seg_tile(gemm::Stages& st, const GemmArgs& g,
+                                              const Segments& sg, int tile) {
+  const int tiles = g.mblocks * g.nblocks;
+  int logical = gemm::xcd_logical(tile, sg.parts ? tiles * sg.count : tiles);
+  const int s0 = logical / tiles, s1 = sg.parts ? s0 + 1 : sg.count;
+  int mb, nb;
+  gemm::tile_coords(logical - s0 * tiles, g.mblocks, g.nblocks, mb, nb);
+  const int64_t m0 = static_cast<int64_t>(mb) * kT, n0 = static_cast<int64_t>(nb) * kT;
+  for (int s = s0; s < s1; ++s) {
+    const uint16_t* A = g.A + s * kSegSteps * 512;
+    const uint16_t* B = g.B + s * sg.b;
+    const int kvalid = g.b_kvalid < 0 ? g.b_kvalid : g.b_kvalid - static_cast<int>(s * kDhSegment);
+    const int left = g.ksteps - static_cast<int>(s * kSegSteps);
+    const int ksteps = left < kSegSteps ? left : static_cast<int>(kSegSteps);
+    const bool last = s + 1 == sg.count;
+    const float* cin = sg.parts ? nullptr : s ? sg.sum : g.Cin;
+    const int64_t ldcin = s ? sg.ldsum : g.ldcin;
+    void* C = sg.parts ? sg.parts + s * g.m_out * g.n_out : last ? g.C : sg.sum;
+    const int64_t ldc = sg.parts ? g.n_out : last ? g.ldc : sg.ldsum;
+    const bool bf16 = !sg.parts && last && sg.bf16;
+    if (s > s0) __syncthreads();  // every wave is done with the stages
+    if (gemm::loader_wave())
+      gemm_add_tile<true, BF>(st, g, A, B, kvalid, ksteps, m0, n0, cin, ldcin, C, ldc, bf16);
+    else
+      gemm_add_tile<false, BF>(st, g, A, B, kvalid, ksteps, m0, n0, cin, ldcin, C, ldc, bf16);
+  }
+}
+
+// gemm_pair_kernel with dh's tiles in segments; dW may have none.
+template <bool BF16DW, int DHB>
+__global__ __launch_bounds__(gemm::kThreads) void gemm_seg_pair_kernel(GemmArgs dh, Segments sg,
+                                                                       GemmArgs dw, int dh_tiles) {
+  __shared__ __align__(16) gemm::Stages st;
+  const int b = blockIdx.x;
+  if (b < dh_tiles)
+    gemm_seg_tile<DHB>(st, dh, sg, b);
+  else
+    gemm_pair_tile<BF16DW, gemm::kKOuterBlocked, gemm::kKContig>(st, dw, b - dh_tiles);
+}
+
+// C = ((Cin + parts[0]) + parts[1]) + ...
+template <bool BF16OUT>
+__global__ __launch_bounds__(256) void sum_parts_kernel(const float* __restrict__ parts, int count,
+                                                        int64_t n, int64_t h, const float* cin,
+                                                        int64_t ldcin, void* C, int64_t ldc) {
+  const int64_t step = n * h;
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < step;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t r = i / h, c = i - r * h;
+    float a = parts[i];
+    if (cin) a = cin[r * ldcin + c] + a;
+#pragma unroll 8
+    for (int s = 1; s < count; ++s) a = a + parts[s * step + i];
+    if (BF16OUT)
+      static_cast<uint16_t*>(C)[r * ldc + c] = bf16_bits(a);
+    else
+      static_cast<float*>(C)[r * ldc + c] = a;
+  }
+}
+
+// Whether the token operators' dh leaves its segments in parts: up to a quarter
+// of the CUs' worth of tiles.
+bool dh_in_parts(int64_t n, int64_t h) {
+  return (n + kT - 1) / kT * ((h + kT - 1) / kT) <= 64;
+}
+
 // Zero rows x cols of C (a sum over no tokens).
 template <bool BF16OUT>
 __global__ __launch_bounds__(256) void fill_zero_kernel(void* C, int64_t ldc, int64_t rows,
@@ -637,13 +764,20 @@ int64_t linear_bwd_chunk(int64_t v, int64_t vocab_chunk) {
 }
 
 LinearBwdLayout linear_bwd_layout(int64_t n, int64_t h, int64_t v, int32_t flags,
-                                  int64_t vocab_chunk) {
+                                  int64_t vocab_chunk, bool segments) {
   const bool need_dh = flags & kBwdDhidden, need_dw = flags & kBwdDweight;
   const bool saved = flags & kBwdSaved;
   LinearBwdLayout l;
   l.np = round_tile(n);
   l.vp = round_tile(v);
-  l.vc = linear_bwd_chunk(v, vocab_chunk);
+  const bool parts = segments && need_dh && dh_in_parts(n, h);
+  int64_t want = vocab_chunk;
+  if (segments) {  // whole segments, and with parts as many as 256 MB of dz hold
+    auto whole = [](int64_t c) { return (c + kDhSegment - 1) / kDhSegment * kDhSegment; };
+    if (want == 0 && parts) want = (int64_t{1} << 27) / l.np;
+    want = whole(want);
+  }
+  l.vc = linear_bwd_chunk(v, want);
   const int64_t nchunks = (l.vp + l.vc - 1) / l.vc;
   auto up = [](int64_t b) { return (b + 255) / 256 * 256; };
   int64_t off = 0;
@@ -656,8 +790,11 @@ LinearBwdLayout linear_bwd_layout(int64_t n, int64_t h, int64_t v, int32_t flags
   l.hb = take(!saved, l.np * h * 2);                      // blocked h for the recompute
   l.ht = take(need_dw, h * l.np * 2);                     // h^T for dW
   l.dz = take(need_dh || need_dw, l.np * l.vc * 2);       // dz_c for dh and dW
-  l.dh32 = take(need_dh && (flags & kBwdBf16Out) && nchunks > 1,
-                n * h * 4);                               // fp32 dh between chunks
+  const int64_t segs = (l.vc + kDhSegment - 1) / kDhSegment;
+  const bool sums = segments && !(parts && segs > 1) ? l.vp > kDhSegment : nchunks > 1;
+  l.dh32 = take(need_dh && (flags & kBwdBf16Out) && sums,
+                n * h * 4);                               // fp32 dh between chunks (segments)
+  l.parts = take(parts && segs > 1, segs * n * h * 4);    // a chunk's segments of dh
   l.total = off;
   return l;
 }
@@ -685,12 +822,13 @@ void launch_linear_bwd(const uint16_t* hidden, int64_t ld_h, const uint16_t* wei
   const int32_t flags = (dh ? kBwdDhidden : 0) | (dw ? kBwdDweight : 0) |
                         (prepared ? kBwdPrepared : 0) | (zsaved ? kBwdSaved : 0) |
                         (bf16_out ? kBwdBf16Out : 0);
-  const LinearBwdLayout l = linear_bwd_layout(n, h, v, flags, vocab_chunk);
+  const LinearBwdLayout l = linear_bwd_layout(n, h, v, flags, vocab_chunk, tokens != nullptr);
   auto at = [&](int64_t off) { return off < 0 ? nullptr : reinterpret_cast<uint16_t*>(ws + off); };
   uint16_t* hb = at(l.hb);
   uint16_t* ht = at(l.ht);
   uint16_t* dz = at(l.dz);
   float* dh32 = l.dh32 < 0 ? nullptr : reinterpret_cast<float*>(ws + l.dh32);
+  float* parts = l.parts < 0 ? nullptr : reinterpret_cast<float*>(ws + l.parts);
   const int mblocks = static_cast<int>(l.np / kT), vblocks = static_cast<int>(l.vp / kT);
   const int64_t hsteps = h / gemm::kK, npsteps = l.np / gemm::kK, vpsteps = l.vp / gemm::kK;
   const bool plain = inv_t == 1.0f && !ent && !round_bf16;
@@ -752,13 +890,33 @@ void launch_linear_bwd(const uint16_t* hidden, int64_t ld_h, const uint16_t* wei
     const int64_t ldc = bf16_out && !last ? h : ld_dh;
     const int hblocks = static_cast<int>((h + kT - 1) / kT);
     const int dh_mblocks = static_cast<int>((n + kT - 1) / kT), dh_tiles = dh_mblocks * hblocks;
+    const GemmArgs gh{dz, csteps * 512, l.np, -1, wtc, ldwt, h, static_cast<int>(wt_kvalid),
+                      static_cast<int>(csteps), dh_mblocks, hblocks, n, h, cin, ldcin, cout, ldc};
+    const GemmArgs gw{dz, csteps, cols, static_cast<int>(l.np), ht, npsteps * 512, h, -1,
+                      static_cast<int>(npsteps), static_cast<int>((rows + kT - 1) / kT), hblocks,
+                      rows, h, nullptr, 0, dwc, ld_dw};
+    constexpr int KC = gemm::kKContig, KO = gemm::kKOuter;
+    if (tokens && dh) {
+      float* run = dh32 ? dh32 : static_cast<float*>(dh);
+      const Segments sg{static_cast<int>((csteps + kSegSteps - 1) / kSegSteps),
+                        prepared ? kSegSteps * 512 : kDhSegment * ld_w, run, ldcin, dh_bf16, parts};
+      const int tiles = dh_tiles * (parts ? sg.count : 1);
+      auto kern = prepared ? (bf16_out ? gemm_seg_pair_kernel<true, KC>
+                                       : gemm_seg_pair_kernel<false, KC>)
+                           : (bf16_out ? gemm_seg_pair_kernel<true, KO>
+                                       : gemm_seg_pair_kernel<false, KO>);
+      hipLaunchKernelGGL(kern, dim3(tiles + (dw ? gw.mblocks * hblocks : 0)), dim3(gemm::kThreads),
+                         0, s, gh, sg, gw, tiles);
+      if (parts) {
+        const int64_t want = (n * h + 255) / 256;
+        const unsigned blocks = static_cast<unsigned>(want < 8192 ? want : 8192);
+        auto sum = dh_bf16 ? sum_parts_kernel<true> : sum_parts_kernel<false>;
+        hipLaunchKernelGGL(sum, dim3(blocks), dim3(256), 0, s, parts, sg.count, n, h, cin, ldcin,
+                           cout, ldc);
+      }
+      continue;
+    }
     if (dh && dw && c0 < v && dh_tiles < 8 * xcd_cus()) {
-      const GemmArgs gh{dz, csteps * 512, l.np, -1, wtc, ldwt, h, static_cast<int>(wt_kvalid),
-                        static_cast<int>(csteps), dh_mblocks, hblocks, n, h, cin, ldcin, cout, ldc};
-      const GemmArgs gw{dz, csteps, cols, static_cast<int>(l.np), ht, npsteps * 512, h, -1,
-                        static_cast<int>(npsteps), static_cast<int>((rows + kT - 1) / kT), hblocks,
-                        rows, h, nullptr, 0, dwc, ld_dw};
-      constexpr int KC = gemm::kKContig, KO = gemm::kKOuter;
       auto kern = prepared ? (!bf16_out ? gemm_pair_kernel<false, false, KC>
                               : dh_bf16 ? gemm_pair_kernel<true, true, KC>
                                         : gemm_pair_kernel<false, true, KC>)

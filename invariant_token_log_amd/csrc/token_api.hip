@@ -368,9 +368,9 @@ int32_t linear_token_logp_q8_fwd(const void* hidden, int64_t ld_h, const float* 
 
 size_t linear_token_logp_bwd_workspace_bytes(int64_t n, int64_t h, int64_t v, int32_t flags,
                                              int64_t vocab_chunk) {
-  const size_t base =
-      linear_logp_bwd_workspace_bytes(n, h, v, itl::kLinearTile, flags, vocab_chunk);
-  return base ? ws_round(base) + 2 * ws_round(static_cast<size_t>(n) * 4) : 0;
+  if (linear_logp_bwd_workspace_bytes(n, h, v, itl::kLinearTile, flags, vocab_chunk) == 0) return 0;
+  const int64_t base = itl::linear_bwd_layout(n, h, v, flags, vocab_chunk, true).total;
+  return ws_round(static_cast<size_t>(base)) + 2 * ws_round(static_cast<size_t>(n) * 4);
 }
 
 int32_t linear_token_logp_bwd(const void* hidden, int64_t ld_h, const void* weight, int64_t ld_w,

@@ -146,6 +146,46 @@ def test_gradient(n, h, v, m, k, ent, temp):
     assert torch.equal(la.grad, dh.to(torch.bfloat16)) and torch.equal(lb.grad, dw.to(torch.bfloat16))
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+def test_gradient_over_many_columns(bf16):
+    """Three segments of the vocabulary: few rows (one product a segment), the
+    same in chunks, and many rows (a tile walks them) give a row the same bits;
+    the bound is test_gradient's."""
+    h, v, few, many = 320, 16384 * 2 + 700, 5, 8300
+    gen = torch.Generator().manual_seed(4)
+    hid = torch.randn(many, h, generator=gen).to(torch.bfloat16)
+    w = (0.05 * torch.randn(v, h, generator=gen)).to(torch.bfloat16)
+    tok = torch.randint(0, v, (many, 2), generator=gen)
+    tok[1, 0], tok[2, 1], tok[3, 0] = 16384, 16383, v - 1
+    g = torch.randn(many, 2, generator=gen)
+    b = w.to(dev())
+    pw = itl.prepare_weight(b)
+
+    def grads(n, **kw):
+        a, t = hid[:n].to(dev()), tok[:n].to(dev())
+        f = itl.linear_token_logp_fwd(a, b, t)
+        return itl.linear_token_logp_bwd(a, b, f.lse, t, f.logp, g[:n].to(dev()),
+                                         out_dtype=torch.bfloat16 if bf16 else torch.float32, **kw)
+
+    dh, dw = grads(few)
+    x = hid[:few].double() @ w.double().T
+    dz, size = token_gradient(x, tok[:few], g[:few], None, None, None)
+    wd, hd = w.double(), hid[:few].double()
+    out = 2.0 ** -8 if bf16 else 0.0
+    ref_h, ref_w = dz @ wd, dz.T @ hd
+    bound_h = 2.0 ** -8 * dz.abs() @ wd.abs() + 1e-4 * size @ wd.abs() + 1e-6
+    bound_w = 2.0 ** -8 * dz.abs().T @ hd.abs() + 1e-4 * size.T @ hd.abs() + 1e-6
+    assert ((dh.double().cpu() - ref_h).abs() <= bound_h + out * (ref_h.abs() + bound_h)).all()
+    assert ((dw.double().cpu() - ref_w).abs() <= bound_w + out * (ref_w.abs() + bound_w)).all()
+    for kw in (dict(vocab_chunk=1), dict(vocab_chunk=32768), dict(prepared_weight=pw), dict(need_dweight=False),
+               dict(prepared_weight=pw, vocab_chunk=16384)):
+        dh2, dw2 = grads(few, **kw)
+        assert torch.equal(dh2, dh), kw.keys()
+        assert dw2 is None or torch.equal(dw2, dw), kw.keys()
+    for kw in (dict(), dict(need_dweight=False), dict(vocab_chunk=16384, prepared_weight=pw)):
+        assert torch.equal(grads(many, **kw)[0][:few], dh), kw.keys()
+
+
 def quant(n, h, v, seed):
     gen = torch.Generator().manual_seed(seed)
     rows = lambda r, s: itl.quantize_rows((s * torch.randn(r, h, generator=gen)).to(dev()))  # noqa: E731
