@@ -141,9 +141,10 @@ size_t linear_token_logp_bwd_workspace_bytes(int64_t n, int64_t h, int64_t v, in
 /*
  * Backward of linear_token_logp_fwd: linear_logp_bwd with a list of entries a
  * row.  dz is rounded to bf16 once, after the entries' gradients are added.
- * dhidden is the sum, in ascending order, of the fp32 sums over 16384 vocabulary
- * columns each; vocab_chunk (0 = the library's default) is rounded up to a
- * multiple of that, and any value gives the same bits.
+ * dhidden is the sum, in ascending order, of the fp32 sums over segments of the
+ * vocabulary (v / 4 columns, rounded up to a multiple of 1024, at least 4096 and
+ * at most 16384); vocab_chunk (0 = the library's default) is rounded up to whole
+ * segments, and any value gives the same bits.
  *   logp, top_logp: the forward's outputs ([n, m], [n, top_k]).
  *   the rest: as linear_logp_bwd and token_logp_bwd.
  */

@@ -80,9 +80,9 @@ int xcd_cus();
 // offsets, -1 for a region not used; np, vp = n, v rounded up to 256.
 constexpr int64_t kDefaultChunk = 32768;
 enum { kBwdDhidden = 1, kBwdDweight = 2, kBwdPrepared = 4, kBwdSaved = 8, kBwdBf16Out = 16 };
-constexpr int64_t kDhSegment = 16384;  // columns of a segment of the token operators' dh
 struct LinearBwdLayout {
   int64_t np, vp, vc;
+  int64_t seg;  // columns of a segment of the token operators' dh
   int64_t hb, ht, dz, dh32, parts, total;
 };
 int64_t linear_bwd_chunk(int64_t v, int64_t vocab_chunk);

@@ -571,17 +571,16 @@ __global__ __launch_bounds__(gemm::kThreads) void gemm_pair_kernel(GemmArgs dh, 
 }
 
 // dh of the token operators: its K walk over the vocabulary falls into segments
-// of kDhSegment columns, each a chain from zero, added in ascending order:
+// of dh_segment(V) columns, each a chain from zero, added in ascending order:
 //   dh = ((seg_0 + seg_1) + seg_2) + ...
 // (one chain over V / 32 steps, as linear_logp_bwd has it, takes 1.4 ms at V =
 // 151936 however few rows there are).  With few tiles (dh_in_parts) a chunk's
 // segments are tiles of their own, which leave their sums in `parts` for
 // sum_parts_kernel; with many a tile walks the segments and keeps the running
 // sum in memory.  The same bits, and a row's do not depend on n.
-constexpr int64_t kSegSteps = kDhSegment / gemm::kK;
-
 struct Segments {
   int count;        // of the chunk
+  int steps;        // K steps each, but the last
   int64_t b;        // elements between two segments of B
   float* sum;       // running sum between segments, or null
   int64_t ldsum;
@@ -640,11 +639,10 @@ __device__ __forceinline__ void gemm_seg_tile(gemm::Stages& st, const GemmArgs& 
   gemm::tile_coords(logical - s0 * tiles, g.mblocks, g.nblocks, mb, nb);
   const int64_t m0 = static_cast<int64_t>(mb) * kT, n0 = static_cast<int64_t>(nb) * kT;
   for (int s = s0; s < s1; ++s) {
-    const uint16_t* A = g.A + s * kSegSteps * 512;
+    const uint16_t* A = g.A + static_cast<int64_t>(s) * sg.steps * 512;
     const uint16_t* B = g.B + s * sg.b;
-    const int kvalid = g.b_kvalid < 0 ? g.b_kvalid : g.b_kvalid - static_cast<int>(s * kDhSegment);
-    const int left = g.ksteps - static_cast<int>(s * kSegSteps);
-    const int ksteps = left < kSegSteps ? left : static_cast<int>(kSegSteps);
+    const int kvalid = g.b_kvalid < 0 ? g.b_kvalid : g.b_kvalid - s * sg.steps * gemm::kK;
+    const int ksteps = min(sg.steps, g.ksteps - s * sg.steps);
     const bool last = s + 1 == sg.count;
     const float* cin = sg.parts ? nullptr : s ? sg.sum : g.Cin;
     const int64_t ldcin = s ? sg.ldsum : g.ldcin;
@@ -691,10 +689,21 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(const float* __restrict_
   }
 }
 
-// Whether the token operators' dh leaves its segments in parts: up to a quarter
-// of the CUs' worth of tiles.
+// Columns of a segment, by V alone (the sum's order): enough segments to fill
+// the GPU with few tiles, long enough that the running sum's trips to memory
+// stay small for many.  H = 4096, us by segment: 2048 rows of V = 151936 take
+// 6060 (16384) and 6280 (8192), 16 rows 1230 and 1240; H = 2048, 40 rows of
+// V = 12000: 255 in one segment, 200 in two, 137 in three.
+int64_t dh_segment(int64_t v) {
+  const int64_t quarter = (v + 4095) / 4096 * 1024;
+  return quarter < 4096 ? 4096 : quarter < 16384 ? quarter : 16384;
+}
+
+// Whether dh leaves its segments in parts: under half a tile a CU.  V = 151936,
+// H = 4096: 80 tiles (1100 rows) take 3980 us in parts and 4640 walking the
+// segments, 128 tiles (2048 rows) 6150 and 6060.
 bool dh_in_parts(int64_t n, int64_t h) {
-  return (n + kT - 1) / kT * ((h + kT - 1) / kT) <= 64;
+  return (n + kT - 1) / kT * ((h + kT - 1) / kT) < 128;
 }
 
 // Zero rows x cols of C (a sum over no tokens).
@@ -770,12 +779,12 @@ LinearBwdLayout linear_bwd_layout(int64_t n, int64_t h, int64_t v, int32_t flags
   LinearBwdLayout l;
   l.np = round_tile(n);
   l.vp = round_tile(v);
+  l.seg = dh_segment(v);
   const bool parts = segments && need_dh && dh_in_parts(n, h);
   int64_t want = vocab_chunk;
   if (segments) {  // whole segments, and with parts as many as 256 MB of dz hold
-    auto whole = [](int64_t c) { return (c + kDhSegment - 1) / kDhSegment * kDhSegment; };
-    if (want == 0 && parts) want = (int64_t{1} << 27) / l.np;
-    want = whole(want);
+    if (want == 0) want = parts ? (int64_t{1} << 27) / l.np : kDefaultChunk;
+    want = (want + l.seg - 1) / l.seg * l.seg;
   }
   l.vc = linear_bwd_chunk(v, want);
   const int64_t nchunks = (l.vp + l.vc - 1) / l.vc;
@@ -790,8 +799,8 @@ LinearBwdLayout linear_bwd_layout(int64_t n, int64_t h, int64_t v, int32_t flags
   l.hb = take(!saved, l.np * h * 2);                      // blocked h for the recompute
   l.ht = take(need_dw, h * l.np * 2);                     // h^T for dW
   l.dz = take(need_dh || need_dw, l.np * l.vc * 2);       // dz_c for dh and dW
-  const int64_t segs = (l.vc + kDhSegment - 1) / kDhSegment;
-  const bool sums = segments && !(parts && segs > 1) ? l.vp > kDhSegment : nchunks > 1;
+  const int64_t segs = (l.vc + l.seg - 1) / l.seg;
+  const bool sums = segments && !(parts && segs > 1) ? l.vp > l.seg : nchunks > 1;
   l.dh32 = take(need_dh && (flags & kBwdBf16Out) && sums,
                 n * h * 4);                               // fp32 dh between chunks (segments)
   l.parts = take(parts && segs > 1, segs * n * h * 4);    // a chunk's segments of dh
@@ -898,8 +907,10 @@ void launch_linear_bwd(const uint16_t* hidden, int64_t ld_h, const uint16_t* wei
     constexpr int KC = gemm::kKContig, KO = gemm::kKOuter;
     if (tokens && dh) {
       float* run = dh32 ? dh32 : static_cast<float*>(dh);
-      const Segments sg{static_cast<int>((csteps + kSegSteps - 1) / kSegSteps),
-                        prepared ? kSegSteps * 512 : kDhSegment * ld_w, run, ldcin, dh_bf16, parts};
+      const int64_t seg_steps = l.seg / gemm::kK;
+      const Segments sg{static_cast<int>((csteps + seg_steps - 1) / seg_steps),
+                        static_cast<int>(seg_steps), prepared ? seg_steps * 512 : l.seg * ld_w, run,
+                        ldcin, dh_bf16, parts};
       const int tiles = dh_tiles * (parts ? sg.count : 1);
       auto kern = prepared ? (bf16_out ? gemm_seg_pair_kernel<true, KC>
                                        : gemm_seg_pair_kernel<false, KC>)

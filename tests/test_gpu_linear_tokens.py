@@ -148,15 +148,15 @@ def test_gradient(n, h, v, m, k, ent, temp):
 
 @pytest.mark.parametrize("bf16", [False, True])
 def test_gradient_over_many_columns(bf16):
-    """Three segments of the vocabulary: few rows (one product a segment), the
-    same in chunks, and many rows (a tile walks them) give a row the same bits;
-    the bound is test_gradient's."""
+    """Four segments of the vocabulary (9216 columns each): few rows (one
+    product a segment), the same in chunks, and many rows (a tile walks them)
+    give a row the same bits; the bound is test_gradient's."""
     h, v, few, many = 320, 16384 * 2 + 700, 5, 8300
     gen = torch.Generator().manual_seed(4)
     hid = torch.randn(many, h, generator=gen).to(torch.bfloat16)
     w = (0.05 * torch.randn(v, h, generator=gen)).to(torch.bfloat16)
     tok = torch.randint(0, v, (many, 2), generator=gen)
-    tok[1, 0], tok[2, 1], tok[3, 0] = 16384, 16383, v - 1
+    tok[1, 0], tok[2, 1], tok[3, 0] = 9216, 9215, v - 1
     g = torch.randn(many, 2, generator=gen)
     b = w.to(dev())
     pw = itl.prepare_weight(b)
