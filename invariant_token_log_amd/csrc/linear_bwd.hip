@@ -13,7 +13,8 @@
 // dz is rounded to bf16 once (the only rounding point besides the fp32
 // accumulators) because both products run on bf16 MFMA.  Every product is a
 // single ascending K walk with no split, so dh[r] depends only on row r (batch
-// invariant) and dW is deterministic for a given token order.
+// invariant) and dW is deterministic for a given token order.  (The token
+// operators' dh is summed in segments of the vocabulary: gemm_seg_pair_kernel.)
 //
 // The vocabulary is walked in chunks of whole 256-column tiles (the
 // caller's vocab_chunk, default kDefaultChunk columns); per chunk [c0, c1):

@@ -311,7 +311,9 @@ def linear_token_logp_bwd(hidden, weight, lse, token_ids=None, logp=None, grad_l
     """Backward of linear_token_logp_fwd: (dhidden [N, H] or None, dweight
     [V, H] or None) in out_dtype, from the forward's lse, logp, top_ids,
     top_logp and entropy and the upstream gradients (top_ids and entropy only
-    where gradients come in for them).  The rest: as linear_logp_bwd."""
+    where gradients come in for them).  dhidden is summed in segments of the
+    vocabulary; vocab_chunk is rounded up to whole ones.  The rest: as
+    linear_logp_bwd."""
     n, h, v, ld_h, ld_w = _linear_operands(hidden, weight)
     dev = hidden.device
     if not hidden.is_cuda or weight.device != dev:
