@@ -237,9 +237,16 @@ template <int GW>
 constexpr int kKeys = GW == 256 ? 10 : 20;
 
 // Order keys of the groups b0 + 64 c + lane; 0 (below every key) past the last.
+// The LM head's tile maximum is NaN as soon as one of the tile's logits is, while
+// a NaN ranks as -inf beside the others: such a tile's key is kNanKey (above
+// every key) until ordered_keys has taken it from the logits.
+constexpr uint32_t kNanKey = 0xffffffffu;
+
 template <bool HEAD>
-__device__ __forceinline__ uint32_t group_key(const uint32_t* g, int64_t i) {
-  return HEAD ? order_key(__uint_as_float(g[i])) : g[i];
+__device__ __forceinline__ uint32_t group_key(uint32_t g) {
+  if constexpr (!HEAD) return g;
+  const float m = __uint_as_float(g);
+  return m != m ? kNanKey : order_key(m);
 }
 template <int GW, bool HEAD>
 __device__ __forceinline__ void load_keys(const uint32_t* g, int64_t b0, int64_t groups, int lane,
@@ -251,8 +258,41 @@ __device__ __forceinline__ void load_keys(const uint32_t* g, int64_t b0, int64_t
   }
 #pragma unroll
   for (int c = 0; c < kKeys<GW>; ++c) {
-    const uint32_t k = HEAD ? order_key(__uint_as_float(key[c])) : key[c];
+    const uint32_t k = group_key<HEAD>(key[c]);
     key[c] = b0 + c * kWave + lane < groups ? k : 0u;
+  }
+}
+
+// Replaces the kNanKey of tiles b0 + 64 c + lane by the key of the greatest of
+// the tile's logits that is no NaN (-inf when there is none), one tile after the
+// other: a row with a NaN has no probabilities, so what counts is that its
+// alternatives are right, and that rows without one only pay the test.
+template <typename T, int GW, int N>
+__device__ __forceinline__ void ordered_keys(const T* row, float inv_t, uint32_t v, int64_t b0,
+                                             int lane, uint32_t (&key)[N]) {
+  uint32_t top = key[0];
+#pragma unroll
+  for (int c = 1; c < N; ++c) top = max(top, key[c]);
+  while (const uint64_t bad = __builtin_amdgcn_ballot_w64(top == kNanKey)) {
+    const int b = __builtin_ctzll(bad);
+    int mine = 0;  // this lane's last such tile
+#pragma unroll
+    for (int c = 0; c < N; ++c) mine = key[c] == kNanKey ? c : mine;
+    const int at = __builtin_amdgcn_readlane(mine, b);
+    const uint32_t c0 = static_cast<uint32_t>(b0 + at * kWave + b) * GW;
+    float m = -INFINITY;
+#pragma unroll
+    for (int o = 0; o < GW; o += kWave) {
+      const uint32_t c = c0 + o + lane;
+      if (c < v) m = fmaxf(m, Elt<T>::load(row, c) * inv_t);  // drops a NaN
+    }
+    const uint32_t k = order_key(wave_max(m));
+    top = 0;
+#pragma unroll
+    for (int c = 0; c < N; ++c) {
+      key[c] = lane == b && c == at ? k : key[c];
+      top = max(top, key[c]);
+    }
   }
 }
 
@@ -276,6 +316,7 @@ __device__ __forceinline__ void select_top(TopStage& st, const T* row, float inv
   uint32_t best[4] = {0, 0, 0, 0};
   for (int64_t b0 = 0; b0 < groups; b0 += kKeys<GW> * kWave) {
     if (b0 > 0) load_keys<GW, HEAD>(g, b0, groups, lane, key);
+    if constexpr (HEAD) ordered_keys<T, GW>(row, inv_t, v, b0, lane, key);
 #pragma unroll
     for (int c = 0; c < kKeys<GW>; ++c) best[c % 4] = max(best[c % 4], key[c]);
   }
@@ -297,8 +338,9 @@ __device__ __forceinline__ void select_top(TopStage& st, const T* row, float inv
   } else {
     for (int64_t c0 = 0; c0 < groups; c0 += kWave) {
       const int64_t c = c0 + lane;
-      const uint32_t one = c < groups ? group_key<HEAD>(g, c) : 0u;
-      top_push(st, list, top_k, one >= bound, compose(one, static_cast<uint32_t>(c)));
+      uint32_t one[1] = {c < groups ? group_key<HEAD>(g[c]) : 0u};
+      if constexpr (HEAD) ordered_keys<T, GW>(row, inv_t, v, c0, lane, one);
+      top_push(st, list, top_k, one[0] >= bound, compose(one[0], static_cast<uint32_t>(c)));
     }
   }
   top_rank(st, list, top_k);

@@ -1,0 +1,112 @@
+"""Values, sizes and launches at the edges of the token operators: NaN and
+infinite logits, vocabularies past one register block of tiles, row chunks,
+against the plain float64 forms.
+
+Inputs of the heads are small whole numbers or lie on a grid, so that every sum
+of products is exact in fp32 and the order of the alternatives is exact too;
+logp and lse keep the bound of the logp path (gpu_helpers)."""
+
+import pytest
+import torch
+
+import invariant_token_log_amd as itl
+from gpu_helpers import ATOL, RTOL, bits, dev
+from token_reference import ranked, token_scores
+
+pytestmark = pytest.mark.gpu
+
+
+def same(a, b):
+    """Equal bits, NaN included."""
+    for x, y in zip(a, b):
+        if x is not None:
+            x, y = x.contiguous(), y.contiguous()
+            view = torch.int64 if x.dtype == torch.int64 else torch.int32
+            assert torch.equal(x.view(view), y.view(view))
+
+
+def head_operands(n, h, v, q8, seed):
+    """(hidden, weight) for the head and the exact logits z (float64): bf16
+    rows, or 8-bit rows with scales that are powers of two."""
+    gen = torch.Generator().manual_seed(seed)
+    hid = torch.randint(-4, 5, (n, h), generator=gen).float()
+    w = torch.randint(-4, 5, (v, h), generator=gen).float()
+    z = (hid @ w.T).double()  # whole numbers of at most 16 h: exact in fp32
+    if not q8:
+        return hid.to(dev(), torch.bfloat16), w.to(dev(), torch.bfloat16), z
+    s = 2.0 ** torch.randint(-2, 2, (v,), generator=gen)
+    rows = lambda x, scale: itl.QuantizedRows(x.to(dev()).to(torch.float8_e4m3fn), scale.to(dev()))  # noqa: E731
+    return rows(hid, torch.ones(n)), rows(w, s), z * s.double()
+
+
+def put_nan(weight, columns):
+    """The weight with NaN in the given rows: their logits are NaN in every row."""
+    if isinstance(weight, itl.QuantizedRows):
+        scale = weight.scale.clone()
+        scale[columns] = torch.nan
+        return itl.QuantizedRows(weight.data, scale)
+    weight = weight.clone()
+    weight[columns, 1] = torch.nan
+    return weight
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("n,h,v", [(5, 64, 3000), (140, 64, 2500), (600, 128, 1000), (3, 64, 170001)])
+def test_nan_logits_through_the_head(n, h, v, q8):
+    """A NaN logit ranks as -inf: the other columns of its tile keep their
+    places, also when it lies beside the row's greatest logits, when a tile
+    holds nothing else and when a whole row is NaN."""
+    a, b, z = head_operands(n, h, v, q8, seed=n + v)
+    beside = [c ^ 1 for c in z.argmax(1)[:3].tolist() if c ^ 1 < v]
+    last = list(range(v // 256 * 256, v))  # the last tile, whole
+    for columns in (beside, last, beside + last):
+        x = z.clone()
+        x[:, columns] = torch.nan
+        bn = put_nan(b, columns)
+        for k in (1, 20, 64):
+            r = itl.linear_token_logp_fwd(a, bn, None, top_k=k, temperature=0.5, return_entropy=True)
+            assert torch.equal(r.top_ids.cpu(), ranked(x, k)), (len(columns), k)
+            assert r.lse.isnan().all() and r.top_logp.isnan().all() and r.entropy.isnan().all()
+    if q8:
+        scale = a.scale.clone()
+        scale[1] = torch.nan
+        an = itl.QuantizedRows(a.data, scale)
+    else:
+        an = a.clone()
+        an[1, 3] = torch.nan
+    r = itl.linear_token_logp_fwd(an, b, None, top_k=9)
+    assert torch.equal(r.top_ids[1].cpu(), torch.arange(9)) and r.lse[1].isnan()
+    other = [i for i in range(n) if i != 1]
+    ref = itl.linear_token_logp_fwd(a, b, None, top_k=9)
+    same([t[other] for t in (r.lse, r.top_logp, r.top_ids)], [t[other] for t in (ref.lse, ref.top_logp, ref.top_ids)])
+
+
+def test_infinite_logits_through_the_head():
+    """+inf comes first, -inf last, and 0 * inf is a NaN."""
+    a, b, z = head_operands(40, 64, 1500, False, seed=3)
+    b[700] = 0.0
+    b[700, 0] = torch.inf
+    z[:, 700] = a[:, 0].cpu().double() * torch.inf
+    assert z[:, 700].isnan().any() and (z[:, 700] == torch.inf).any() and (z[:, 700] == -torch.inf).any()
+    for k in (1, 64):
+        r = itl.linear_token_logp_fwd(a, b, None, top_k=k)
+        assert torch.equal(r.top_ids.cpu(), ranked(z, k))
+    low = z[:, 700] == -torch.inf
+    lse = torch.logsumexp(z[low], 1)
+    assert ((r.lse.cpu().double()[low] - lse).abs() <= ATOL + RTOL * lse.abs()).all()
+    assert not torch.isfinite(r.lse.cpu()[~low]).any()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_nan_logits_streamed(dtype):
+    """The same from logits, with an infinite logit beside it."""
+    x = torch.randn(6, 5003, generator=torch.Generator().manual_seed(1)).to(dtype)
+    x[0, 100] = torch.nan
+    x[1, x[1].argmax() ^ 1] = torch.nan
+    x[2, :] = torch.nan
+    x[3, 7], x[3, 8] = torch.inf, torch.nan
+    x[4, 9], x[4, 300] = torch.inf, -torch.inf
+    for k in (1, 20, 64):
+        r = itl.token_logp_fwd(x.to(dev()), None, top_k=k)
+        assert torch.equal(r.top_ids.cpu(), ranked(x, k))
+        assert r.lse[:4].isnan().all() and torch.isfinite(r.lse[5])
