@@ -130,6 +130,8 @@ size_t logp_fwd_workspace_bytes(int64_t n, int64_t v, int32_t tile_width,
  *                 returns LOGP_ERR_TARGET if any such row was seen.
  *   logp_out      fp32 [n].
  *   lse_out       fp32 [n], may be NULL.  Saved for logp_bwd.
+ *                 A row with a NaN logit has lse = logp = NaN, one of -inf
+ *                 alone lse = -inf and logp = NaN.
  *   entropy_out   fp32 [n] or NULL: the full-vocabulary entropy
  *                 H = -sum_j p_j log p_j of each row ("Batch-Invariant LogP",
  *                 VIME CP=2 runtime provider: entropy on request, merged in

@@ -232,6 +232,23 @@ __device__ __forceinline__ float ent_term(float e, float d, float w) {
   return fmaf(e, fmaxf(d, -FLT_MAX), w);
 }
 
+// The maximum a tile reports, given the one that ignores NaN.  The merge skips
+// a tile with m = -inf as one that holds no column, so a tile of nothing but
+// NaN and -inf reports NaN: a NaN logit reaches the row's LSE wherever it is.
+// (A tile with other values carries its NaN in s.)
+template <int C, int E>
+__device__ __forceinline__ float tile_max(const float (&x)[C][E], float m) {
+  if (__builtin_expect(__builtin_amdgcn_ballot_w64(m == -INFINITY) != 0, 0)) {  // one m a wave
+    bool nan = false;
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+#pragma unroll
+      for (int e = 0; e < E; ++e) nan |= x[j][e] != x[j][e];
+    if (__builtin_amdgcn_ballot_w64(nan)) m = __uint_as_float(0x7fc00000u);
+  }
+  return m;
+}
+
 // ---------------------------------------------------------------------------
 // Tile statistic ("Batch-Invariant LogP", Tensor Parallel, step 2): one wave
 // reduces the W = C * 64 * E columns [col0, col0 + W) of one row to
@@ -269,7 +286,7 @@ __device__ __forceinline__ void tile_stats(const T* row, int64_t col0, int64_t v
     for (int e = 0; e < E; ++e) m = fmaxf(m, x[j][e]);
   // lane moves for tiles of at most 16 elements per lane, LDS crossbar above
   constexpr bool kLds = C * E > 16;
-  m = kLds ? wave_max_lds(m) : wave_max(m);
+  m = tile_max(x, kLds ? wave_max_lds(m) : wave_max(m));
   float s = 0.0f, w = 0.0f;
 #pragma unroll
   for (int j = 0; j < C; ++j)

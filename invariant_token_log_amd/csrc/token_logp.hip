@@ -118,6 +118,7 @@ __device__ __forceinline__ void token_tile_stats(const T* row, int64_t col0, int
   } else {
     m = kLds ? wave_max_lds(m) : wave_max(m);
   }
+  m = tile_max(x, m);
   float s = 0.0f, w = 0.0f;
 #pragma unroll
   for (int j = 0; j < C; ++j)

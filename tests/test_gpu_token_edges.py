@@ -110,3 +110,36 @@ def test_nan_logits_streamed(dtype):
         r = itl.token_logp_fwd(x.to(dev()), None, top_k=k)
         assert torch.equal(r.top_ids.cpu(), ranked(x, k))
         assert r.lse[:4].isnan().all() and torch.isfinite(r.lse[5])
+
+
+# a tile is tile_width columns: here 4096, the default
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_tile_of_nothing_but_nan(dtype):
+    """A tile whose only values are NaN (and -inf) is no empty tile: the row's
+    lse is NaN, as for a NaN beside other values.  Rows without one, and rows
+    and tiles of -inf alone, keep their values."""
+    v = 3 * 4096 + 5
+    x = torch.randn(8, v, generator=torch.Generator().manual_seed(2)).to(dtype)
+    x[0, -1] = torch.nan                     # beside four other values
+    x[1, -5:] = torch.nan                    # the last tile, whole
+    x[2, 4096:8192] = -torch.inf
+    x[2, 5000] = torch.nan                   # one NaN in a masked tile
+    x[3, 4096:8192] = torch.nan              # a whole tile
+    x[4] = torch.nan                         # a whole row
+    x[5, 4096:8192] = -torch.inf             # a masked tile
+    x[6] = -torch.inf                        # a masked row
+    nan = torch.tensor([True] * 5 + [False] * 3)
+    t = torch.full((8, 1), 17, dtype=torch.int64, device=dev())
+    xd = x.to(dev())
+    for k in (0, 5):
+        r = itl.token_logp_fwd(xd, t, top_k=k, return_entropy=True)
+        assert torch.equal(r.lse.isnan().cpu(), nan)
+        assert r.logp[:5].isnan().all() and r.entropy[:5].isnan().all() and r.top_logp[:5].isnan().all()
+        assert r.lse[6] == -torch.inf and r.logp[6].isnan()
+        ref = token_scores(x[[5, 7]].double(), t[[5, 7]], k)
+        assert ((r.lse[[5, 7]].cpu().double() - ref["lse"]).abs() <= ATOL + RTOL * ref["lse"].abs()).all()
+        for shards in (1, 19):  # of v = 19 * 647
+            logp, lse, ent = itl.logp_fwd(xd, t[:, 0], num_shards=shards, return_entropy=True)
+            assert torch.equal(lse.isnan().cpu(), nan) and logp[:5].isnan().all() and ent[:5].isnan().all()
+            for a, b in ((lse, r.lse), (logp, r.logp[:, 0])):
+                assert torch.equal(bits(a)[5:], bits(b)[5:])
