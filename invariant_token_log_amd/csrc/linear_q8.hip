@@ -194,7 +194,6 @@ __device__ __forceinline__ bool q8_target(const f32x16& x, int off, float& t) {
 // load stays in bounds, and what it brings is masked or not read.
 // ---------------------------------------------------------------------------
 using gemm::swzp;
-using gemm::wait_vm;
 using gemm::wait_vm_lgkm0;
 
 constexpr int kPair = 2 * kStep;  // bytes of a row per pair
@@ -282,7 +281,9 @@ __device__ __forceinline__ void q8_mainloop(SmemWide& sm, const uint8_t* __restr
   // read, so that every pair of the loop is alike.
   issue(0, 0);
   issue(1, npairs > 1 ? 1 : 0);
-  wait_vm<LOADER ? 16 : 0>();
+  // Also the LDS writes of q8_fill: with one pair this is the only barrier
+  // between them and the epilogue's reads.
+  wait_vm_lgkm0<LOADER ? 16 : 0>();
   __builtin_amdgcn_s_barrier();
   read(0, 0, xw, xh);
   // Order inside a block: the next chunk's six reads, then the conversions of

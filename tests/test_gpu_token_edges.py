@@ -143,3 +143,23 @@ def test_tile_of_nothing_but_nan(dtype):
             assert torch.equal(lse.isnan().cpu(), nan) and logp[:5].isnan().all() and ent[:5].isnan().all()
             for a, b in ((lse, r.lse), (logp, r.logp[:, 0])):
                 assert torch.equal(bits(a)[5:], bits(b)[5:])
+
+
+@pytest.mark.parametrize("h", [64, 128, 192])
+def test_8bit_head_of_one_step(h):
+    """Many rows on one pair of K steps (h = 64, 128), where a single barrier
+    stands between the scales and targets in LDS and their reads: scales and
+    targets that differ from row to row and column to column, every row."""
+    n, v = 1100, 2600
+    a, b, z = head_operands(n, h, v, True, seed=h)
+    gen = torch.Generator().manual_seed(h)
+    s = 2.0 ** torch.randint(-3, 2, (n,), generator=gen)
+    a, z = itl.QuantizedRows(a.data, s.to(dev())), z * s.double()[:, None]
+    tok = torch.randint(0, v, (n, 1), generator=gen)
+    tok[torch.rand(n, 1, generator=gen) < 0.1] = -100
+    for k in (0, 7):
+        r = itl.linear_token_logp_fwd(a, b, tok.to(dev()), top_k=k, return_entropy=True)
+        ref = token_scores(z, tok, k)
+        for got, want in ((r.logp, ref["logp"]), (r.lse, ref["lse"])):
+            assert ((got.double().cpu() - want).abs() <= ATOL + RTOL * want.abs()).all()
+        assert torch.equal(r.top_ids.cpu(), ref["top_ids"])
