@@ -350,6 +350,15 @@ Shape norm_shape(int64_t h) {
     GO(1024, 4) GO(1024, 8)                                                                     \
   }
 
+// Workgroups of a launch: a grid holds fewer than 2^32 threads, so more rows
+// take several launches.
+constexpr int64_t kMaxGroups = int64_t{1} << 20;
+
+template <typename T>
+T* row_at(T* p, int64_t r, int64_t ld) {
+  return p ? p + r * ld : nullptr;
+}
+
 bool fits16(const void* p, int64_t ld, int size) {
   return !p || (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * size) % 16 == 0);
 }
@@ -364,18 +373,27 @@ void norm_typed(const NormRows& rows, const void* weight, int64_t n, int64_t h, 
                    (q8 ? reinterpret_cast<uintptr_t>(y) % 8 == 0 && ld_y % 8 == 0
                        : fits16(y, ld_y, size));
   const float inv_h = static_cast<float>(1.0 / static_cast<double>(h));
+  const T* x = static_cast<const T*>(rows.x);
+  const T* residual = static_cast<const T*>(rows.residual);
+  T* sum = static_cast<T*>(rows.sum);
+  char* out = static_cast<char*>(y);
+  const int64_t out_size = q8 ? 1 : size;
 #define ITL_GO(TM, C)                                                                           \
   case TM * 16 + C: {                                                                           \
     auto kern = q8 ? (vec ? rms_norm_kernel<T, TM, C, true, true>                               \
                           : rms_norm_kernel<T, TM, C, false, true>)                             \
                    : (vec ? rms_norm_kernel<T, TM, C, true, false>                              \
                           : rms_norm_kernel<T, TM, C, false, false>);                           \
-    constexpr int kBlock = TM < 256 ? 256 : TM;                                                 \
-    hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>((n + kBlock / TM - 1) / (kBlock / TM))), \
-                       dim3(kBlock), 0, s, static_cast<const T*>(rows.x), rows.ld_x,            \
-                       static_cast<const T*>(rows.residual), rows.ld_r,                         \
-                       static_cast<T*>(rows.sum), rows.ld_s, static_cast<const T*>(weight), n,  \
-                       h, eps, inv_h, y, ld_y, scale, rstd);                                    \
+    constexpr int kBlock = TM < 256 ? 256 : TM, kRows = kBlock / TM;                            \
+    for (int64_t r0 = 0; r0 < n; r0 += kMaxGroups * kRows) {                                    \
+      const int64_t m = n - r0 < kMaxGroups * kRows ? n - r0 : kMaxGroups * kRows;              \
+      hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>((m + kRows - 1) / kRows)),            \
+                         dim3(kBlock), 0, s, row_at(x, r0, rows.ld_x), rows.ld_x,               \
+                         row_at(residual, r0, rows.ld_r), rows.ld_r,                            \
+                         row_at(sum, r0, rows.ld_s), rows.ld_s, static_cast<const T*>(weight),  \
+                         m, h, eps, inv_h, static_cast<void*>(out + r0 * ld_y * out_size), ld_y, \
+                         row_at(scale, r0, 1), row_at(rstd, r0, 1));                            \
+    }                                                                                           \
   } break;
   ITL_NORM_SHAPES(ITL_GO)
 #undef ITL_GO

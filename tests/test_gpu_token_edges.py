@@ -163,3 +163,24 @@ def test_8bit_head_of_one_step(h):
         for got, want in ((r.logp, ref["logp"]), (r.lse, ref["lse"])):
             assert ((got.double().cpu() - want).abs() <= ATOL + RTOL * want.abs()).all()
         assert torch.equal(r.top_ids.cpu(), ref["top_ids"])
+
+
+def test_more_rows_than_one_grid_holds():
+    """2^26 rows and a few, one column: more workgroups than one launch takes.
+    Each row as in a batch of its own, beside a launch's end and at the last."""
+    n = (1 << 26) + 7
+    x = torch.empty(n, 1, dtype=torch.bfloat16, device=dev()).normal_(generator=torch.Generator(dev()).manual_seed(1))
+    r = torch.empty_like(x).normal_(generator=torch.Generator(dev()).manual_seed(2))
+    w = torch.full((1,), 1.5, dtype=torch.bfloat16, device=dev())
+    y, s, rstd = itl.rms_norm_fwd(x, w, residual=r, return_rstd=True)
+    q, sq = itl.rms_norm_quantized(x, w, residual=r)
+    assert torch.equal(s, (x.float() + r.float()).to(torch.bfloat16)) and torch.equal(sq, s)
+    ends = [(i << 22) - 3 for i in range(1, 17)] + [0, n - 9]
+    for i in ends:
+        part = slice(i, i + 9)
+        y1, s1, rstd1 = itl.rms_norm_fwd(x[part], w, residual=r[part], return_rstd=True)
+        q1, _ = itl.rms_norm_quantized(x[part], w, residual=r[part])
+        assert torch.equal(y[part], y1) and torch.equal(rstd[part], rstd1)
+        assert torch.equal(q.data[part].view(torch.uint8), q1.data.view(torch.uint8))
+        assert torch.equal(q.scale[part], q1.scale)
+    assert torch.isfinite(y).all() and (rstd > 0).all()
