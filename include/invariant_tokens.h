@@ -101,11 +101,12 @@ enum logp_token_flags {
 /*
  * Workspace of linear_token_logp_fwd / linear_token_logp_q8_fwd in bytes.
  * The head's rows are taken row_chunk at a time (rounded up to a multiple of
- * 256; 0 = 4096); per chunk it holds the tile statistics, a re-laid copy of
- * the hidden rows and, unless logits_out is given or the call has one given
- * token a row and no alternatives, the chunk's logits (fp32, bf16 with
- * LOGP_TOKEN_ROUND_BF16), 2.5 GB for 4096 rows of 151936 columns.  Any
- * row_chunk gives the same bits.  0 for arguments the call would reject.
+ * 256); per chunk it holds the tile statistics, a re-laid copy of the hidden
+ * rows and, unless logits_out is given or the call has no alternatives and at
+ * most one given token a row, the chunk's logits (fp32, bf16 with
+ * LOGP_TOKEN_ROUND_BF16), 2.5 GB for 4096 rows of 151936 columns.  row_chunk 0
+ * takes 4096 rows where the chunk's logits are in the workspace, else 65536.
+ * Any row_chunk gives the same bits.  0 for arguments the call would reject.
  */
 size_t linear_token_logp_fwd_workspace_bytes(int64_t n, int64_t h, int64_t v, int64_t m,
                                              int32_t top_k, int32_t flags, int64_t row_chunk);

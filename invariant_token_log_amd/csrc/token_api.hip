@@ -15,7 +15,10 @@ using itl::ws_round;
 static_assert(itl::kMaxTokens == LOGP_MAX_TOKENS && itl::kMaxTop == LOGP_MAX_TOP, "limits");
 
 constexpr int kMaxTiles = 4096;
-constexpr int64_t kDefaultRows = 4096;  // rows of the head per chunk
+// Rows of the head per chunk unless the caller asks for another number: with the
+// chunk's logits in the workspace, and without (12 bytes of statistics a tile).
+constexpr int64_t kDefaultRows = 4096;
+constexpr int64_t kDefaultRowsNoLogits = 65536;
 
 int32_t check_tokens(const void* tokens, int32_t token_dtype, int64_t m) {
   if (token_dtype != LOGP_I64 && token_dtype != LOGP_I32) return LOGP_ERR_DTYPE;
@@ -78,8 +81,8 @@ HeadLayout head_layout(int64_t n, int64_t h, int64_t v, int64_t m, int32_t top_k
   const int zsize = flags & LOGP_TOKEN_ROUND_BF16 ? 2 : 4;
   l.single = m == 1 && top_k == 0 && !keeps;
   l.own_z = !l.single && !keeps && (m > 0 || top_k > 0);
-  const int64_t want = row_chunk > 0 ? row_chunk : kDefaultRows;
-  l.rc = l.own_z ? (want + 255) / 256 * 256 : n;
+  const int64_t want = row_chunk > 0 ? row_chunk : l.own_z ? kDefaultRows : kDefaultRowsNoLogits;
+  l.rc = (want + 255) / 256 * 256;
   if (l.rc > n) l.rc = n;
   l.tile = flags & LOGP_TOKEN_Q8 ? itl::kQ8Tile : itl::kLinearTile;
   l.ntiles = (v + l.tile - 1) / l.tile;

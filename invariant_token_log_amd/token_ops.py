@@ -247,8 +247,8 @@ def linear_token_logp_fwd(hidden, weight, token_ids=None, top_k=0, ignore_index=
     head of frozen weights (no round_logits, prepared_weight or logits_out).
     round_logits and prepared_weight: as linear_logp_fwd.  logits_out [N, V]
     float32 (or bfloat16 with round_logits) receives the unscaled logits for
-    linear_token_logp_bwd.  row_chunk: rows whose logits are in memory at a
-    time (0 = the library's default); any value gives the same bits."""
+    linear_token_logp_bwd.  row_chunk: rows taken at a time, which bounds the
+    workspace (0 = the library's default); any value gives the same bits."""
     q8 = isinstance(hidden, QuantizedRows)
     if q8 != isinstance(weight, QuantizedRows):
         raise TypeError("hidden and weight must both be QuantizedRows, or neither")

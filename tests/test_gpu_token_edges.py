@@ -184,3 +184,23 @@ def test_more_rows_than_one_grid_holds():
         assert torch.equal(q.data[part].view(torch.uint8), q1.data.view(torch.uint8))
         assert torch.equal(q.scale[part], q1.scale)
     assert torch.isfinite(y).all() and (rstd > 0).all()
+
+
+@pytest.mark.parametrize("m,k,kept,q8", [(1, 0, False, False), (0, 0, False, False), (2, 3, True, False),
+                                         (1, 0, False, True), (0, 0, False, True)])
+def test_row_chunks_without_logits_in_the_workspace(m, k, kept, q8):
+    """Several chunks, a part of one and one that takes the tiles for few rows:
+    the bits of the rows taken together."""
+    n, h, v = 805, 128, 1500
+    a, b, _ = head_operands(n, h, v, q8, seed=m)
+    tok = torch.randint(0, v, (n, m), generator=torch.Generator().manual_seed(5)).to(dev()) if m else None
+    if m:
+        tok[3] = -100
+    outs = []
+    for chunk in (0, 256, 300):
+        z = torch.zeros(n, v, device=dev()) if kept else None
+        extra = dict(logits_out=z) if kept else {}
+        r = itl.linear_token_logp_fwd(a, b, tok, top_k=k, return_entropy=True, row_chunk=chunk, **extra)
+        outs.append([*r, z])
+    for o in outs[1:]:
+        same(outs[0], o)
