@@ -71,9 +71,11 @@ def _tokens(t, n, lead, device):
 
 
 def _row_grad(x, n, k, name, device):
-    """A float32 [n, k] gradient or saved value, contiguous."""
-    if x.numel() != n * k or x.device != device:
-        raise ValueError(f"{name} must have one entry per row and token, on the rows' device")
+    """A gradient or saved value with k entries a row ([*lead, k], the leading
+    dimensions flattened or not), as contiguous float32."""
+    if x.dim() < 1 or x.shape[-1] != k or x.numel() != n * k or x.device != device:
+        raise ValueError(f"{name} must be [*lead, {k}], one entry per row and token, on the rows' "
+                         "device")
     return x.to(torch.float32).contiguous()
 
 

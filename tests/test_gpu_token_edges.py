@@ -204,3 +204,22 @@ def test_row_chunks_without_logits_in_the_workspace(m, k, kept, q8):
         outs.append([*r, z])
     for o in outs[1:]:
         same(outs[0], o)
+
+
+def test_backwards_refuse_gradients_in_another_layout():
+    n, v, h, m, k = 4, 300, 64, 3, 2
+    a, b, z = head_operands(n, h, v, False, seed=9)
+    x, tok = z.float().to(dev()), torch.randint(0, v, (n, m), generator=torch.Generator().manual_seed(1)).to(dev())
+    g, gt = torch.ones(n, m, device=dev()), torch.ones(n, k, device=dev())
+    f = itl.token_logp_fwd(x, tok, top_k=k)
+    e = itl.linear_token_logp_fwd(a, b, tok, top_k=k)
+    tops = dict(top_ids=f.top_ids, grad_top_logp=gt)
+    d = itl.token_logp_bwd(x, f.lse, tok, g, **tops)
+    assert torch.equal(itl.token_logp_bwd(x.view(2, 2, v), f.lse, tok.view(2, 2, m), g, **tops).view(n, v), d)
+    for bad in (g.t().contiguous(), g.view(-1)):
+        with pytest.raises(ValueError, match="grad_logp"):
+            itl.token_logp_bwd(x, f.lse, tok, bad)
+        with pytest.raises(ValueError, match="grad_logp"):
+            itl.linear_token_logp_bwd(a, b, e.lse, tok, e.logp, bad)
+    with pytest.raises(ValueError, match="grad_top_logp"):
+        itl.token_logp_bwd(x, f.lse, tok, g, top_ids=f.top_ids, grad_top_logp=gt.t())

@@ -4,8 +4,9 @@ operators, on the host (nothing here touches a device)."""
 import os
 
 import pytest
+import torch
 
-from invariant_token_log_amd import _lib
+from invariant_token_log_amd import _lib, token_ops
 from invariant_token_log_amd.build import LIB_PATH, build
 
 
@@ -27,3 +28,18 @@ def test_row_chunk_bounds_the_workspace(L, m, k, flags):
     assert need(1 << 20, 300) == need(512, 0)
     assert need(1 << 20, 0) == need(65536, 0) > need(65536, 4096)
     assert need(100, 256) == need(100, 0)
+
+
+def test_gradients_in_another_layout_are_refused():
+    """As many entries in another layout are no [*lead, M] gradient."""
+    cpu = torch.device("cpu")
+    g = torch.arange(6.0).view(2, 3)
+    for good in (g, g.double(), g.view(2, 1, 3), g.repeat(1, 2)[:, :3]):
+        assert torch.equal(token_ops._row_grad(good, 2, 3, "grad_logp", cpu).view(2, 3), g)
+    for bad in (g.t(), g.reshape(-1), g.view(3, 2), g.view(1, 6), torch.zeros(4, 3), torch.zeros(())):
+        with pytest.raises(ValueError, match="grad_logp"):
+            token_ops._row_grad(bad, 2, 3, "grad_logp", cpu)
+    ids = torch.zeros(2, 3, dtype=torch.int64)
+    with pytest.raises(ValueError, match="grad_top_logp"):
+        token_ops._alternatives(ids, g.t(), 2, cpu)
+    assert token_ops._alternatives(ids, g, 2, cpu)[1] == 3
