@@ -79,6 +79,16 @@ def _row_grad(x, n, k, name, device):
     return x.to(torch.float32).contiguous()
 
 
+def _token_grad(grad_logp, n, m, device):
+    """The given tokens' gradient, None without tokens (where one that has
+    entries would be lost)."""
+    if m:
+        return _row_grad(grad_logp, n, m, "grad_logp", device)
+    if grad_logp is not None and grad_logp.numel():
+        raise ValueError("grad_logp needs the token_ids that it belongs to")
+    return None
+
+
 def _same_device(device, **tensors):
     for name, t in tensors.items():
         if t is not None and t.device != device:
@@ -169,7 +179,7 @@ def token_logp_bwd(logits, lse, token_ids=None, grad_logp=None, top_ids=None, gr
         raise ValueError("entropy and grad_entropy go together")
     if m and grad_logp is None:
         raise ValueError("grad_logp is needed for the given tokens")
-    g = _row_grad(grad_logp, n, m, "grad_logp", dev) if m else None
+    g = _token_grad(grad_logp, n, m, dev)
     ids, k, gt = _alternatives(top_ids, grad_top_logp, n, dev)
     lse = _row_vector(lse, n, "lse")
     ent, gent = _row_vector(entropy, n, "entropy"), _row_vector(grad_entropy, n, "grad_entropy")
@@ -332,7 +342,7 @@ def linear_token_logp_bwd(hidden, weight, lse, token_ids=None, logp=None, grad_l
     if (entropy is None) != (grad_entropy is None):
         raise ValueError("entropy and grad_entropy go together")
     lp = _row_grad(logp, n, m, "logp", dev) if m else None
-    g = _row_grad(grad_logp, n, m, "grad_logp", dev) if m else None
+    g = _token_grad(grad_logp, n, m, dev)
     ids, k, gt = _alternatives(top_ids, grad_top_logp, n, dev)
     tl = _row_grad(top_logp, n, k, "top_logp", dev) if ids is not None else None
     lse = _row_vector(lse, n, "lse")

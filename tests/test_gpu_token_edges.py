@@ -223,3 +223,19 @@ def test_backwards_refuse_gradients_in_another_layout():
             itl.linear_token_logp_bwd(a, b, e.lse, tok, e.logp, bad)
     with pytest.raises(ValueError, match="grad_top_logp"):
         itl.token_logp_bwd(x, f.lse, tok, g, top_ids=f.top_ids, grad_top_logp=gt.t())
+
+
+def test_backwards_refuse_a_gradient_without_its_tokens():
+    n, v, h, m, k = 4, 300, 64, 3, 2
+    a, b, z = head_operands(n, h, v, False, seed=9)
+    x, g, gt = z.float().to(dev()), torch.ones(n, m, device=dev()), torch.ones(n, k, device=dev())
+    f, e = itl.token_logp_fwd(x, None, top_k=k), itl.linear_token_logp_fwd(a, b, None, top_k=k)
+    with pytest.raises(ValueError, match="token_ids"):
+        itl.token_logp_bwd(x, f.lse, None, g, top_ids=f.top_ids, grad_top_logp=gt)
+    with pytest.raises(ValueError, match="token_ids"):
+        itl.linear_token_logp_bwd(a, b, e.lse, None, g, g, top_ids=e.top_ids, top_logp=e.top_logp, grad_top_logp=gt)
+    # no tokens, and a gradient of none of them
+    leaf = x.clone().requires_grad_()
+    r = itl.batch_invariant_token_logp(leaf, None, top_k=k)
+    (r.logp.sum() + r.top_logp.sum()).backward()
+    assert torch.isfinite(leaf.grad).all()

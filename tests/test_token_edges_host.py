@@ -43,3 +43,15 @@ def test_gradients_in_another_layout_are_refused():
     with pytest.raises(ValueError, match="grad_top_logp"):
         token_ops._alternatives(ids, g.t(), 2, cpu)
     assert token_ops._alternatives(ids, g, 2, cpu)[1] == 3
+
+
+def test_gradient_without_tokens_is_refused():
+    """A gradient of log-probabilities without the tokens that it belongs to
+    would be lost."""
+    cpu = torch.device("cpu")
+    g = torch.arange(6.0).view(2, 3)
+    with pytest.raises(ValueError, match="token_ids"):
+        token_ops._token_grad(g, 2, 0, cpu)
+    assert token_ops._token_grad(torch.empty(2, 0), 2, 0, cpu) is None
+    assert token_ops._token_grad(None, 2, 0, cpu) is None
+    assert torch.equal(token_ops._token_grad(g, 2, 3, cpu), g)
