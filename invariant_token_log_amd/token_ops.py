@@ -469,8 +469,8 @@ def rms_norm_fwd(x, weight, residual=None, eps=1e-6, return_rstd=False, y_out=No
     """Root-mean-square norm of s = x + residual (rounded to x's dtype, then
     normed; s = x without a residual): (y, s, rstd), y = s / sqrt(mean(s^2) +
     eps) * weight, rstd [N] float32 (None unless asked for).  x [*lead, H]
-    float32, bfloat16 or float16, weight [H].  sum_out may be x or residual
-    (in place)."""
+    float32, bfloat16 or float16, weight [H].  sum_out receives s (a copy of x
+    without a residual) and may be x or residual (in place)."""
     px, n, h, ld_x = _norm_rows(x, "x")
     code = _dtype_code(x)
     pw = _norm_weight(weight, x)
@@ -479,6 +479,7 @@ def rms_norm_fwd(x, weight, residual=None, eps=1e-6, return_rstd=False, y_out=No
     pr, ld_r, ps, ld_s, s = None, 0, None, 0, x
     if residual is not None:
         pr, _, _, ld_r = _norm_rows(residual, "residual", x)
+    if residual is not None or sum_out is not None:
         s, ps, ld_s = _norm_out(sum_out, "sum_out", x, h)
     rstd = torch.empty(n, dtype=torch.float32, device=dev) if return_rstd else None
     _call("rms_norm_fwd", dev, px, ld_x, pr, ld_r, pw, code, n, h, float(eps), py, ld_y, ps, ld_s,
@@ -545,6 +546,7 @@ def _quantize(x, weight, residual, eps, sum_out):
     pr, ld_r, ps, ld_s, s = None, 0, None, 0, x
     if residual is not None:
         pr, _, _, ld_r = _norm_rows(residual, "residual", x)
+    if residual is not None or sum_out is not None:
         s, ps, ld_s = _norm_out(sum_out, "sum_out", x, h)
     q = torch.empty(n, h, dtype=torch.float8_e4m3fn, device=dev)
     scale = torch.empty(n, dtype=torch.float32, device=dev)

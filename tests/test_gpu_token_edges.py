@@ -239,3 +239,21 @@ def test_backwards_refuse_a_gradient_without_its_tokens():
     r = itl.batch_invariant_token_logp(leaf, None, top_k=k)
     (r.logp.sum() + r.top_logp.sum()).backward()
     assert torch.isfinite(leaf.grad).all()
+
+
+@pytest.mark.parametrize("h", [100, 2048])
+def test_norm_writes_a_given_sum_without_a_residual(h):
+    gen = torch.Generator().manual_seed(h)
+    x = torch.randn(5, h, generator=gen).to(dev(), torch.bfloat16)
+    w = torch.ones(h, dtype=torch.bfloat16, device=dev())
+    y, _, _ = itl.rms_norm_fwd(x, w)
+    for norm in (lambda t, s: itl.rms_norm_fwd(t, w, sum_out=s)[:2], lambda t, s: itl.rms_norm_quantized(t, w, sum_out=s)):
+        buf = torch.full_like(x, 7.0)
+        _, s = norm(x, buf)
+        assert s is buf and torch.equal(buf, x)
+        own = x.clone()  # in place
+        _, s = norm(own, own)
+        assert s is own and torch.equal(own, x)
+    own, buf = x.clone(), torch.empty_like(x)  # y over x, x kept beside it
+    y2, s, _ = itl.rms_norm_fwd(own, w, y_out=own, sum_out=buf)
+    assert torch.equal(own, y) and torch.equal(buf, x)
