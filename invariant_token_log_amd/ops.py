@@ -241,6 +241,12 @@ def linear_logp_bwd_workspace_bytes(n, h, v, need_dhidden=True, need_dweight=Tru
     return _lib.lib().linear_logp_bwd_workspace_bytes(n, h, v, tile_width, flags, vocab_chunk)
 
 
+def _saved_stride(z, n, v):
+    """Row stride of the saved logits: their own, so that the library refuses
+    rows that overlap (an expanded tensor); a single row's need not be v."""
+    return z.stride(0) if n > 1 else max(z.stride(0), v)
+
+
 def linear_logp_bwd(hidden, weight, targets, lse, grad_logp, ignore_index=-100,
                     tile_width=LINEAR_TILE, need_dhidden=True, need_dweight=True,
                     out_dtype=torch.float32, dhidden_out=None, dweight_out=None,
@@ -296,7 +302,7 @@ def linear_logp_bwd(hidden, weight, targets, lse, grad_logp, ignore_index=-100,
                                t1.data_ptr(), _INDEX[t1.dtype], int(ignore_index), int(tile_width),
                                float(temperature), _rounding(round_logits), _ptr(z),
                                _DTYPES[z.dtype] if z is not None else 0,
-                               max(z.stride(0), v) if z is not None else 0, _ptr(pw),
+                               _saved_stride(z, n, v) if z is not None else 0, _ptr(pw),
                                _nbytes(pw), lse.data_ptr(),
                                g.data_ptr(), _ptr(ent),
                                _ptr(gent), _DTYPES[out_dtype], _ptr(dh),

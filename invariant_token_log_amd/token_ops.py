@@ -19,7 +19,7 @@ from torch.autograd.function import once_differentiable
 from . import _lib
 from ._lib import check
 from .ops import (_DTYPES, _INDEX, _dtype_code, _linear_operands, _nbytes, _padded_logits,
-                  _prepared, _prepared_buffer, _ptr, _rounding, _row_vector, _rows)
+                  _prepared, _prepared_buffer, _ptr, _rounding, _row_vector, _rows, _saved_stride)
 
 
 class TokenLogp(NamedTuple):
@@ -374,7 +374,7 @@ def linear_token_logp_bwd(hidden, weight, lse, token_ids=None, logp=None, grad_l
     _call("linear_token_logp_bwd", dev, hidden.data_ptr(), ld_h, weight.data_ptr(), ld_w, n, h, v,
           _ptr(tok), tcode, m, int(ignore_index), _ptr(ids), k, float(temperature),
           _rounding(round_logits), _ptr(z), _DTYPES[z.dtype] if z is not None else 0,
-          max(z.stride(0), v) if z is not None else 0, _ptr(pw), _nbytes(pw), lse.data_ptr(),
+          _saved_stride(z, n, v) if z is not None else 0, _ptr(pw), _nbytes(pw), lse.data_ptr(),
           _ptr(lp), _ptr(tl), _ptr(g), _ptr(gt), _ptr(ent), _ptr(gent), _DTYPES[out_dtype], _ptr(dh),
           (dh.stride(0) if n > 1 else h) if dh is not None else 0, _ptr(dw),
           (dw.stride(0) if v > 1 else h) if dw is not None else 0, int(vocab_chunk), _ptr(ws),

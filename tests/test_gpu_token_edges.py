@@ -257,3 +257,23 @@ def test_norm_writes_a_given_sum_without_a_residual(h):
     own, buf = x.clone(), torch.empty_like(x)  # y over x, x kept beside it
     y2, s, _ = itl.rms_norm_fwd(own, w, y_out=own, sum_out=buf)
     assert torch.equal(own, y) and torch.equal(buf, x)
+
+
+def test_saved_logits_that_overlap_are_refused():
+    n, v, h = 4, 304, 64
+    a, b, z = head_operands(n, h, v, False, seed=11)
+    tok = torch.randint(0, v, (n, 1), generator=torch.Generator().manual_seed(1)).to(dev())
+    f = itl.linear_token_logp_fwd(a, b, tok)
+    g = torch.ones(n, 1, device=dev())
+    one = z[:1].float().to(dev())
+    for bad in (one.expand(n, v), torch.zeros(4 * v, device=dev()).as_strided((n, v), (v - 4, 1))):
+        with pytest.raises(itl.LogpError) as e:
+            itl.linear_token_logp_bwd(a, b, f.lse, tok, f.logp, g, saved_logits=bad)
+        assert e.value.status == itl._lib.LOGP_ERR_SHAPE
+        with pytest.raises(itl.LogpError) as e:
+            itl.linear_logp_bwd(a, b, tok[:, 0], f.lse, g[:, 0], saved_logits=bad)
+        assert e.value.status == itl._lib.LOGP_ERR_SHAPE
+    dh, _ = itl.linear_token_logp_bwd(a, b, f.lse, tok, f.logp, g)
+    assert torch.equal(itl.linear_token_logp_bwd(a, b, f.lse, tok, f.logp, g, saved_logits=z.float().to(dev()))[0], dh)
+    d1, _ = itl.linear_token_logp_bwd(a[:1], b, f.lse[:1], tok[:1], f.logp[:1], g[:1], saved_logits=one)
+    assert torch.equal(d1, dh[:1])

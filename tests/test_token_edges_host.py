@@ -55,3 +55,16 @@ def test_gradient_without_tokens_is_refused():
     assert token_ops._token_grad(torch.empty(2, 0), 2, 0, cpu) is None
     assert token_ops._token_grad(None, 2, 0, cpu) is None
     assert torch.equal(token_ops._token_grad(g, 2, 3, cpu), g)
+
+
+def test_saved_logits_keep_their_row_stride():
+    """Rows that overlap keep their stride for the library to refuse: taken as
+    v columns apart, rows past the first would be read behind the data."""
+    from invariant_token_log_amd.ops import _saved_stride
+
+    row = torch.zeros(1, 8)
+    assert _saved_stride(row.expand(5, 8), 5, 8) == 0
+    assert _saved_stride(torch.zeros(40).as_strided((5, 8), (4, 1)), 5, 8) == 4
+    assert _saved_stride(torch.zeros(5, 12)[:, :8], 5, 8) == 12
+    assert _saved_stride(row, 1, 8) == 8
+    assert _saved_stride(torch.zeros(1, 12)[:, :8], 1, 8) == 12
