@@ -11,7 +11,8 @@ import torch
 
 import invariant_token_log_amd as itl
 from gpu_helpers import ATOL, RTOL, bits, dev
-from token_reference import ranked, token_scores
+from invariant_token_log_amd import _lib
+from token_reference import ranked, token_gradient, token_scores
 
 pytestmark = pytest.mark.gpu
 
@@ -277,3 +278,146 @@ def test_saved_logits_that_overlap_are_refused():
     assert torch.equal(itl.linear_token_logp_bwd(a, b, f.lse, tok, f.logp, g, saved_logits=z.float().to(dev()))[0], dh)
     d1, _ = itl.linear_token_logp_bwd(a[:1], b, f.lse[:1], tok[:1], f.logp[:1], g[:1], saved_logits=one)
     assert torch.equal(d1, dh[:1])
+
+
+@pytest.mark.parametrize("q8", [False, True])
+@pytest.mark.parametrize("n,v", [(2, 163840), (5, 163841), (140, 164100), (600, 201088), (3, 262144)])
+def test_head_past_one_block_of_tiles(n, v, q8):
+    """Vocabularies around 163840 columns, where the tables of a row no longer
+    fit one block of registers in the merge and in the selection; rows on both
+    sides of every tile and of two waves a row, a row alone, a row of equal
+    logits.  The merge's chain over T tiles is off by at most T 2^-24 in the sum
+    and the moment, which moves the entropy by twice that of the mean distance
+    to the maximum."""
+    h, k = 64, 20
+    a, b, _ = head_operands(n, h, v, q8, seed=v)
+    if q8:
+        a.data.view(torch.uint8)[1] = 0
+        hd, wd = a.data.cpu().double(), b.data.cpu().double() * b.scale.cpu().double()[:, None]
+    else:
+        a[1] = 0.0
+        hd, wd = a.cpu().double(), b.cpu().double()
+    rows = sorted({0, 1, n // 2, n - 1})
+    tok = torch.randint(0, v, (n, 2), generator=torch.Generator().manual_seed(3))
+    tok[0] = torch.tensor([v - 1, 0])
+    r = itl.linear_token_logp_fwd(a, b, tok.to(dev()), top_k=k, temperature=16.0, return_entropy=True)
+    x = hd[rows] @ wd.T / 16.0  # exact
+    ref = token_scores(x, tok[rows], k)
+    at = lambda t: t[rows].double().cpu()  # noqa: E731
+    assert torch.equal(r.top_ids[rows].cpu(), ref["top_ids"])
+    for got, want in ((r.logp, ref["logp"]), (r.lse, ref["lse"]), (r.top_logp, ref["top_logp"])):
+        assert ((at(got) - want).abs() <= ATOL + RTOL * want.abs()).all()
+    chain = 2 * (v + 127) // 128 * 2.0 ** -24 * (x.amax(1) - ref["lse"] + ref["entropy"])
+    assert ((at(r.entropy) - ref["entropy"]).abs() <= ATOL + RTOL * ref["entropy"] + chain).all()
+    for i in rows:
+        one = itl.QuantizedRows(a.data[i:i + 1], a.scale[i:i + 1]) if q8 else a[i:i + 1]
+        s = itl.linear_token_logp_fwd(one, b, tok[i:i + 1].to(dev()), top_k=k, temperature=16.0, return_entropy=True)
+        same([t[i:i + 1] for t in r], s)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_gradient_through_segments_of_the_vocabulary(bf16):
+    """Three segments of 4096 columns, with several tokens (one twice, one
+    invalid, some at a segment's edge), alternatives, entropy and temperature:
+    few rows (every segment a product of its own, then their sum) against
+    float64 within test_gpu_linear_tokens' bounds; many rows (a tile walks the
+    segments) give a row the bits of the few; dweight of the many against
+    float64.  The workspace tells which of the two runs."""
+    h, v, few, many, m, k, temp = 320, 9000, 6, 16640, 3, 4, 0.7
+    gen = torch.Generator().manual_seed(8)
+    hid = (torch.randn(many, h, generator=gen) * 16).round().clamp(-127, 127) / 16
+    w = (torch.randn(v, h, generator=gen) * 51).round().clamp(-127, 127) / 1024
+    tok = torch.randint(0, v, (many, m), generator=gen)
+    tok[0, 1] = tok[0, 0]
+    tok[1] = -100
+    tok[2, 0] = v + 5
+    tok[3] = torch.tensor([4095, 4096, 8192])
+    tok[4, 0] = v - 1
+    g, gt, ge = torch.randn(many, m, generator=gen), torch.randn(many, k, generator=gen), torch.randn(many, generator=gen)
+    out = torch.bfloat16 if bf16 else torch.float32
+    b = w.to(dev(), torch.bfloat16)
+    pw = itl.prepare_weight(b)
+    ops = [t.to(dev()) for t in (hid.to(torch.bfloat16), tok, g, gt, ge)]
+
+    def grads(part, **kw):
+        a, t, gp, gtp, gep = (o[part] for o in ops)
+        f = itl.linear_token_logp_fwd(a, b, t, top_k=k, temperature=temp, return_entropy=True)
+        return itl.linear_token_logp_bwd(a, b, f.lse, t, f.logp, gp, f.top_ids, f.top_logp, gtp, temperature=temp,
+                                         entropy=f.entropy, grad_entropy=gep, out_dtype=out, **kw), f
+
+    def need(n, chunk=0):
+        flags = _lib.LOGP_BWD_DHIDDEN | _lib.LOGP_BWD_DWEIGHT
+        np_, vc = (n + 255) // 256 * 256, min(chunk or 32768, 9216)
+        rest = 2 * np_ * h * 2 + np_ * vc * 2  # the hidden rows twice, dz
+        return _lib.lib().linear_token_logp_bwd_workspace_bytes(n, h, v, flags, chunk) - rest
+
+    assert need(few) >= 3 * few * h * 4                # every segment's part
+    assert need(many) < 4 * many * h and need(many, 8192) < 4 * many * h  # none: the tiles walk
+
+    (dh, dw), f = grads(slice(0, few))
+    inv = 1.0 / temp
+    wd, hd = w.double(), hid[:few].double()
+    dx, size = token_gradient(hd @ wd.T * inv, tok[:few], g[:few], f.top_ids.cpu(), gt[:few], ge[:few])
+    dz, size = dx * inv, size * inv
+    half = 2.0 ** -8 if bf16 else 0.0
+
+    def inside(got, want, bound):
+        assert ((got.double() - want).abs() <= bound + half * (want.abs() + bound)).all()
+
+    inside(dh.cpu(), dz @ wd, 2.0 ** -8 * dz.abs() @ wd.abs() + 1e-4 * size @ wd.abs() + 1e-6)
+    inside(dw.cpu(), dz.T @ hd, 2.0 ** -8 * dz.abs().T @ hd.abs() + 1e-4 * size.T @ hd.abs() + 1e-6)
+    for kw in (dict(vocab_chunk=4096), dict(vocab_chunk=8192), dict(prepared_weight=pw), dict(prepared_weight=pw, vocab_chunk=8192)):
+        (d2, w2), _ = grads(slice(0, few), **kw)
+        assert torch.equal(d2, dh) and torch.equal(w2, dw), kw.keys()
+    (dhm, dwm), fm = grads(slice(0, many))
+    assert torch.equal(dhm[:few], dh) and not dhm[1].any()
+    tail = slice(many - few, many)
+    assert torch.equal(dhm[tail], grads(tail)[0][0])
+    for kw in (dict(vocab_chunk=4096), dict(vocab_chunk=8192), dict(prepared_weight=pw), dict(prepared_weight=pw, vocab_chunk=8192),
+               dict(need_dweight=False), dict(need_dweight=False, vocab_chunk=8192)):
+        (d2, w2), _ = grads(slice(0, many), **kw)
+        assert torch.equal(d2, dhm) and (w2 is None or torch.equal(w2, dwm)), kw.keys()
+    # dweight of all rows, the formula in 64 bits on the device
+    hd, wd = ops[0].double(), b.double()
+    x = torch.mm(hd, wd.t().contiguous()) * inv
+    lse = torch.logsumexp(x, 1, keepdim=True)
+    p = torch.exp(x - lse)
+    given = ops[1] != -100
+    act = given.any(1, keepdim=True).double()
+    gd, gtd = ops[2].double() * given, ops[3].double() * act
+    logp = x - lse
+    ent = -(p * logp).sum(1, keepdim=True)
+    total = (gd.sum(1) + gtd.sum(1))[:, None]
+    gent = ops[4].double()[:, None]
+    d = (-p * total - gent * p * (logp + ent)) * act
+    size = (p * (gd.abs().sum(1) + gtd.abs().sum(1))[:, None] + gent.abs() * p * (logp.abs() + ent)) * act
+    inside_v = (ops[1] >= 0) & (ops[1] < v)
+    d.scatter_add_(1, ops[1].clamp(0, v - 1), gd * inside_v)
+    size.scatter_add_(1, ops[1].clamp(0, v - 1), gd.abs() * inside_v)
+    d.scatter_add_(1, fm.top_ids.clamp(min=0), gtd)
+    size.scatter_add_(1, fm.top_ids.clamp(min=0), gtd.abs())
+    d, size = (d * inv).t().contiguous(), (size * inv).t().contiguous()
+    inside(dwm, torch.mm(d, hd), 2.0 ** -8 * torch.mm(d.abs(), hd.abs()) + 1e-4 * torch.mm(size, hd.abs()) + 1e-6)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("n,v", [(3, 163841), (600, 164100), (2, 262144)])
+def test_logits_past_one_block_of_groups(n, v, dtype):
+    """The same from logits: more groups of 128 columns (64 of fp32) than the
+    selection's registers hold at once; a row of equal logits, a row alone."""
+    gen = torch.Generator().manual_seed(v)
+    rows = sorted({0, 1, n - 1})
+    x = torch.zeros(n, v, dtype=dtype, device=dev())
+    some = (3 * torch.randn(len(rows), v, generator=gen)).to(dtype)
+    some[1] = 0.5
+    x[rows] = some.to(dev())
+    tok = torch.randint(0, v, (n, 2), generator=gen)
+    for k in (1, 20, 64):
+        r = itl.token_logp_fwd(x, tok.to(dev()), top_k=k, return_entropy=True)
+        ref = token_scores(some.double(), tok[rows], k)
+        assert torch.equal(r.top_ids[rows].cpu(), ref["top_ids"])
+        for got, want in ((r.logp, ref["logp"]), (r.lse, ref["lse"]), (r.top_logp, ref["top_logp"])):
+            assert ((got[rows].double().cpu() - want).abs() <= ATOL + RTOL * want.abs()).all()
+        for i in rows:
+            same([t[i:i + 1] for t in r], itl.token_logp_fwd(x[i:i + 1], tok[i:i + 1].to(dev()), top_k=k,
+                                                             return_entropy=True))
