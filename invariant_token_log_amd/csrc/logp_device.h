@@ -371,7 +371,8 @@ __device__ __forceinline__ float merge_lse_t(P m, P s, P w, int ntiles, int64_t 
         const bool live = mr[c] != -INFINITY;
         const float ek = live ? exp_sub(mr[c], big_m) : 0.0f;
         st.se[lane] = make_float2(live ? sr[c] : 0.0f, ek);
-        if constexpr (ENT) st.y[lane] = live ? fmaf(sr[c], mr[c] - big_m, wr[c]) : 0.0f;
+        // e_k = 0 adds nothing (a tile of the type's lowest value has y_k = -inf)
+        if constexpr (ENT) st.y[lane] = ek > 0.0f ? fmaf(sr[c], mr[c] - big_m, wr[c]) : 0.0f;
         __builtin_amdgcn_wave_barrier();
         const int cnt = ntiles - c0 < kWave ? ntiles - c0 : kWave;
         for (int j0 = 0; j0 < cnt; j0 += 8) {

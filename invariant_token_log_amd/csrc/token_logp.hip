@@ -206,7 +206,8 @@ __device__ __forceinline__ float merge_tree(const float* m, const float* s, cons
       if (mr[u] != -INFINITY) {  // a tile of masked columns only holds nothing
         const float e = exp_sub(mr[u], mx);
         acc = fmaf(sr[u], e, acc);
-        if constexpr (ENT) b = fmaf(fmaf(sr[u], mr[u] - mx, wr[u]), e, b);
+        if constexpr (ENT)  // e = 0: as in merge_lse_t
+          b = fmaf(e > 0.0f ? fmaf(sr[u], mr[u] - mx, wr[u]) : 0.0f, e, b);
       }
   }
   const float la = log_nat(wave_sum(acc));

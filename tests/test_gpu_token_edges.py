@@ -421,3 +421,53 @@ def test_logits_past_one_block_of_groups(n, v, dtype):
         for i in rows:
             same([t[i:i + 1] for t in r], itl.token_logp_fwd(x[i:i + 1], tok[i:i + 1].to(dev()), top_k=k,
                                                              return_entropy=True))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_entropy_beside_tiles_of_the_lowest_value(dtype):
+    """Whole tiles masked with the type's lowest value (and with -inf, or far
+    below the rest) add nothing to the entropy."""
+    v, low = 3 * 4096 + 5, torch.finfo(dtype).min
+    x = (3 * torch.randn(5, v, generator=torch.Generator().manual_seed(6))).to(dtype)
+    x[0, 4096:8192] = low
+    x[1, 5:] = low
+    x[2, 4096:] = -torch.inf
+    x[2, 8192:] = low
+    x[3, :4096] = low / 4
+    ref = token_scores(x.double(), None, 0)
+    near = torch.where(x.double() < -1e4, 0.0, x.double())  # masked columns carry no weight
+    bound = ATOL + RTOL * ref["entropy"] + 1e-6 * (near.amax(1) - near.amin(1))
+    xd, t = x.to(dev()), torch.zeros(5, dtype=torch.int64, device=dev())
+    r = itl.token_logp_fwd(xd, None, top_k=3, return_entropy=True)
+    for got in (r.entropy, itl.logp_fwd(xd, t, return_entropy=True)[2]):
+        assert ((got.double().cpu() - ref["entropy"]).abs() <= bound).all()
+    d = itl.token_logp_bwd(xd, r.lse, entropy=r.entropy, grad_entropy=torch.ones(5, device=dev()))
+    assert torch.isfinite(d).all() and (d[0, 4096:8192] == 0).all() and (d[1, 5:] == 0).all()
+
+
+@pytest.mark.parametrize("q8", [False, True])
+def test_entropy_of_the_head_beside_far_tiles(q8):
+    """A whole tile whose logits are near the lowest fp32 value."""
+    h, v = 64, 1000
+    gen = torch.Generator().manual_seed(7)
+    hid, w = torch.ones(3, h), torch.randint(-4, 5, (v, h), generator=gen).float() / 64
+    w[256:512] = 0.0
+    big = 2.0 ** 127  # times -1.75 = -2.98e38
+    if q8:
+        w[256:512, 0] = -1.75
+        scale = torch.ones(v)
+        scale[256:512] = big
+        a = itl.QuantizedRows(hid.to(dev()).to(torch.float8_e4m3fn), torch.ones(3, device=dev()))
+        b = itl.QuantizedRows(w.to(dev()).to(torch.float8_e4m3fn), scale.to(dev()))
+    else:
+        w[256:512, 0] = -1.75 * big
+        a, b = hid.to(dev(), torch.bfloat16), w.to(dev(), torch.bfloat16)
+    x = hid.double() @ w.double().T
+    x[:, 256:512] = -1.75 * big
+    ref = token_scores(x, None, 0)
+    r = itl.linear_token_logp_fwd(a, b, None, return_entropy=True)
+    for got, want in ((r.lse, ref["lse"]), (r.entropy, ref["entropy"])):
+        assert ((got.double().cpu() - want).abs() <= 2 * ATOL + RTOL * want.abs()).all()
+    if not q8:
+        got = itl.linear_logp_fwd(a, b, torch.zeros(3, dtype=torch.int64, device=dev()), return_entropy=True)[2]
+        assert ((got.double().cpu() - ref["entropy"]).abs() <= 2 * ATOL + RTOL * ref["entropy"]).all()
