@@ -97,15 +97,20 @@ __device__ __forceinline__ void store_transposed(const uint16_t (*tile)[kTS], ui
 }
 
 // dst = the K32-blocked [cols, K = rows_p] operand with element (c, r) =
-// r < rows ? src[r * ld + c] : 0 (cols a multiple of 16, rows_p of 32).
+// r < rows ? src[r * ld + c] : 0 (cols a multiple of 16, rows_p of 32).  With
+// targets, an ignored row is 0 as well: its dz is 0, and what a padding row
+// holds (infinities, NaN) must not reach the sum over the tokens.
 // Tiles of 32 source rows x 256 source columns: every thread loads 16-byte
 // chunks of whole 512-byte row segments, the tile leaves as 1 KiB pieces.
 // Grid: x = column tiles, y = row tiles (grid-stride beyond gridDim.y).
 __global__ __launch_bounds__(256) void transpose_blocked(const uint16_t* __restrict__ src,
                                                          int64_t ld, int64_t rows,
                                                          int64_t rows_p, int64_t cols,
-                                                         uint16_t* __restrict__ dst) {
+                                                         uint16_t* __restrict__ dst,
+                                                         const void* __restrict__ tgt,
+                                                         int32_t tgt32, int64_t ignore) {
   __shared__ __align__(16) uint16_t tile[kTR][kTS];
+  const Targets targets{tgt, tgt32};
   const int tid = threadIdx.x;
   const int64_t c0 = static_cast<int64_t>(blockIdx.x) * kTC;
   const int cols_here = static_cast<int>(cols - c0 < kTC ? cols - c0 : kTC);
@@ -116,7 +121,8 @@ __global__ __launch_bounds__(256) void transpose_blocked(const uint16_t* __restr
     for (int u = 0; u < 4; ++u) {
       const int r = (tid >> 5) + 8 * u, ch = (tid & 31) * 8;
       uint4 x = make_uint4(0u, 0u, 0u, 0u);
-      if (r0 + r < rows && ch < cols_here) x = load_stream(src + (r0 + r) * ld + c0 + ch);
+      if (r0 + r < rows && ch < cols_here && (!tgt || targets[r0 + r] != ignore))
+        x = load_stream(src + (r0 + r) * ld + c0 + ch);
       *reinterpret_cast<uint4*>(&tile[r][ch]) = x;
     }
     __syncthreads();
@@ -732,11 +738,12 @@ dim3 tile_grid(int64_t rows_p, int64_t cols) {
 }
 
 // dst = the K32-blocked [cols, K = rows_p] transpose of src [rows, ld]
-// (rows past `rows` zero).
+// (rows past `rows`, and with targets the ignored ones, zero).
 void launch_transpose(const uint16_t* src, int64_t ld, int64_t rows, int64_t rows_p,
-                      int64_t cols, uint16_t* dst, hipStream_t s) {
+                      int64_t cols, uint16_t* dst, hipStream_t s,
+                      Targets targets = Targets{nullptr, 0}, int64_t ignore = 0) {
   hipLaunchKernelGGL(transpose_blocked, tile_grid(rows_p, cols), dim3(256), 0, s, src, ld, rows,
-                     rows_p, cols, dst);
+                     rows_p, cols, dst, targets.p, targets.is32, ignore);
 }
 
 // C = A B^T (+ Cin), A [arows, k] and B [brows, k] in the forms af / bf
@@ -845,7 +852,7 @@ void launch_linear_bwd(const uint16_t* hidden, int64_t ld_h, const uint16_t* wei
   const uint16_t* wop = prepared ? prepared_blocked_w(prepared) : weight;
   const int64_t ldw = prepared ? int64_t{0} : ld_w;
   if (!zsaved) launch_block_rows(hidden, ld_h, n, l.np, h, hb, s);
-  if (dw) launch_transpose(hidden, ld_h, n, l.np, h, ht, s);
+  if (dw) launch_transpose(hidden, ld_h, n, l.np, h, ht, s, targets, ignore);
   for (int64_t c0 = 0; c0 < l.vp; c0 += l.vc) {
     const int64_t c1 = c0 + l.vc < l.vp ? c0 + l.vc : l.vp;
     const int64_t cols = c1 - c0, csteps = cols / gemm::kK;

@@ -471,3 +471,46 @@ def test_entropy_of_the_head_beside_far_tiles(q8):
     if not q8:
         got = itl.linear_logp_fwd(a, b, torch.zeros(3, dtype=torch.int64, device=dev()), return_entropy=True)[2]
         assert ((got.double().cpu() - ref["entropy"]).abs() <= 2 * ATOL + RTOL * ref["entropy"]).all()
+
+
+@pytest.mark.parametrize("value", [torch.nan, torch.inf])
+@pytest.mark.parametrize("n", [6, 40, 300])
+def test_what_a_padding_row_holds_stays_there(n, value):
+    """Hidden rows, gradients and kept logits of padding rows may be anything:
+    no output and no gradient of the batch shows it, dweight included."""
+    h, v = 128, 1000
+    gen = torch.Generator().manual_seed(n)
+    a = torch.randn(n, h, generator=gen).to(dev(), torch.bfloat16)
+    b = (0.05 * torch.randn(v, h, generator=gen)).to(dev(), torch.bfloat16)
+    tok = torch.randint(0, v, (n, 2), generator=gen).to(dev())
+    pads = [2, n - 1]
+    tok[pads] = -100
+    g, ge = torch.randn(n, 2, generator=gen).to(dev()), torch.randn(n, generator=gen).to(dev())
+    pw = itl.prepare_weight(b)
+
+    def tokens(fill, saved, out, prepared):
+        x, gx, gex = a.clone(), g.clone(), ge.clone()
+        z = torch.zeros(n, v, device=dev()) if saved else None
+        for t in (x, gx, gex):
+            t[pads] = fill
+        f = itl.linear_token_logp_fwd(x, b, tok, top_k=3, return_entropy=True, logits_out=z)
+        if saved:
+            z[pads] = fill
+        gt = torch.full((n, 3), 0.5, device=dev())
+        gt[pads] = fill
+        return (*f, *itl.linear_token_logp_bwd(x, b, f.lse, tok, f.logp, gx, f.top_ids, f.top_logp, gt, entropy=f.entropy,
+                                               grad_entropy=gex, saved_logits=z, out_dtype=out, prepared_weight=prepared))
+
+    def single(fill, t):
+        x, gx = a.clone(), g[:, 0].clone()
+        x[pads] = fill
+        gx[pads] = fill
+        logp, lse = itl.linear_logp_fwd(x, b, t)
+        return logp, lse, *itl.linear_logp_bwd(x, b, t, lse, gx)
+
+    for saved, out, prepared in ((False, torch.float32, None), (True, torch.bfloat16, None), (False, torch.bfloat16, pw)):
+        for one, two in zip(tokens(0.0, saved, out, prepared), tokens(value, saved, out, prepared)):
+            assert torch.isfinite(two).all() and torch.equal(one, two)
+    for t in (tok[:, 0].contiguous(), tok[:, 0].int()):
+        for one, two in zip(single(0.0, t), single(value, t)):
+            assert torch.isfinite(two).all() and torch.equal(one, two)
