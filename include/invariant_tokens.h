@@ -24,6 +24,12 @@
  * first, the lowest index first among equals; a NaN logit ranks as -inf (the
  * row's lse, and with it every log-probability, is then NaN).
  *
+ * A log-probability is the difference of a logit and the row's fp32 lse, as in
+ * logp_fwd, and has the resolution of that lse: 2^-24 of its magnitude.  Where a
+ * row's greatest logit is itself a mask (the type's lowest value in every
+ * column), log v is lost beside it, in logp and in the gradient; its entropy
+ * is exact.
+ *
  * Batch invariance: a row's outputs depend only on that row (and the weight),
  * not on n, its position, the launch geometry or top_k; lse and entropy have
  * the bits of logp_fwd at the same tile_width, or of linear_logp_fwd.
@@ -187,7 +193,8 @@ int32_t linear_token_logp_q8_fwd(const void* hidden, int64_t ld_h, const float* 
  *   y = RNE_dtype(s * rstd * weight),  rstd = 1 / sqrt(mean(s^2) + eps)
  * The stored s is what is normed, so the fused call has the bits of an
  * addition followed by the norm of its stored result.  Sums in fp32 through a
- * tree fixed by h alone.
+ * tree fixed by h alone; squares past fp32's range (values of about 1e19) give
+ * rstd 0, and squares below it count as 0.
  *   x [n, ld_x], residual [n, ld_r] (NULL: none), weight [h], y [n, ld_y],
  *   sum_out [n, ld_s] (NULL only without a residual): dtype LOGP_F32, LOGP_BF16
  *   or LOGP_F16; any alignment, whole 16-byte accesses where the rows are

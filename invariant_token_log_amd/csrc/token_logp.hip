@@ -740,7 +740,7 @@ void launch_token_partials(int dtype, bool vec, int chunks, const void* logits, 
                            int64_t n, int64_t v, const TokenView& tok, int ntiles, float* pm,
                            float* ps, float* pw, uint32_t* gm, hipStream_t s) {
   // Segments: enough (row, segment) items for the GPU, each at least one
-  // round of the workgroup's eight waves.
+  // round of the workgroup's four waves.
   const int most = (ntiles + kPartWaves - 1) / kPartWaves;
   const int64_t want = (4 * 8 * static_cast<int64_t>(xcd_cus()) + n - 1) / n;
   const int segs0 = static_cast<int>(want < most ? want : most);

@@ -576,7 +576,9 @@ def norm_linear_token_logp(x, norm_weight, weight, token_ids=None, residual=None
     TokenLogp.  x [N, H] bfloat16.  With a bfloat16 weight [V, H] it is
     differentiable in x, residual, norm_weight and weight (rms_norm, then
     linear_token_logp); with a QuantizedRows weight the normed rows are
-    quantised in the norm and the 8-bit head scores them (no gradient)."""
+    quantised in the norm and the 8-bit head scores them (no gradient).  The
+    gradient of norm_weight sums over all rows, padding rows (whose part is 0)
+    included: they must be finite for it."""
     if isinstance(weight, QuantizedRows):
         if round_logits or save_logits or prepared_weight is not None:
             raise ValueError("the 8-bit head takes no round_logits, save_logits or prepared_weight")
