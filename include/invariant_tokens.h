@@ -27,8 +27,8 @@
  * A log-probability is the difference of a logit and the row's fp32 lse, as in
  * logp_fwd, and has the resolution of that lse: 2^-24 of its magnitude.  Where a
  * row's greatest logit is itself a mask (the type's lowest value in every
- * column), log v is lost beside it, in logp and in the gradient; its entropy
- * is exact.
+ * column), log v is lost beside it, in logp and in the gradient (not in the
+ * entropy).
  *
  * Batch invariance: a row's outputs depend only on that row (and the weight),
  * not on n, its position, the launch geometry or top_k; lse and entropy have

@@ -17,9 +17,9 @@
 // 8192 x 4096 49 (42), 8192 x 8192 124 (83), 4096 x 8200 126 (42), 4096 x 16384
 // 184 (83), 1024 x 65536 1322 (83); forward 8192 x 4096 41 (42), 4096 x 16384 100
 // (83), 1024 x 65536 137 (83); 8 bits 4096 x 16384 103 (73), 1024 x 65536 348 (73).
-//  Each thread adds its squares in ascending order, the lanes
-// of a wave follow in a butterfly and the waves in order, so the sum's tree
-// depends on h alone: not on n, the row's place or its alignment.
+// Each thread adds its squares in ascending order, the lanes of a wave follow in
+// a butterfly and the waves in order, so the sum's tree depends on h alone: not
+// on n, the row's place or its alignment.
 // s is rounded to its type before it is normed, since the stored s is what
 // the next layer and the backward read: the fused call then has the bits of
 // an addition followed by a norm.
