@@ -514,3 +514,91 @@ def test_what_a_padding_row_holds_stays_there(n, value):
     for t in (tok[:, 0].contiguous(), tok[:, 0].int()):
         for one, two in zip(single(0.0, t), single(value, t)):
             assert torch.isfinite(two).all() and torch.equal(one, two)
+
+
+def test_heads_on_two_streams_at_once():
+    """Both heads on two streams, many rows (the tile queue is in the call's own
+    workspace) and few, forward and backward: the bits of one call after the other."""
+    cases = []
+    for n, seed in ((700, 1), (40, 2)):
+        a, b, _ = head_operands(n, 128, 6000, False, seed)
+        qa, qb, _ = head_operands(n, 128, 6000, True, seed)
+        tok = torch.randint(0, 6000, (n, 2), generator=torch.Generator().manual_seed(seed)).to(dev())
+        cases.append((a, b, qa, qb, tok, torch.ones(n, 2, device=dev())))
+
+    def run(a, b, qa, qb, tok, g):
+        f = itl.linear_token_logp_fwd(a, b, tok, top_k=5, return_entropy=True)
+        dh, dw = itl.linear_token_logp_bwd(a, b, f.lse, tok, f.logp, g)
+        return [*f, dh, dw, *itl.linear_token_logp_fwd(qa, qb, tok, top_k=5, return_entropy=True)]
+
+    want = [run(*c) for c in cases]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for c in cases:
+            s = torch.cuda.Stream()
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                got.append(run(*c))
+        torch.cuda.synchronize()
+        for x, y in zip(want, got):
+            same(x, y)
+
+
+@pytest.mark.parametrize("n", [30, 16400])
+def test_graph_replays_of_the_segmented_backward(n):
+    """The backward through several vocabulary segments, in parts (30 rows) and
+    walked (16400), captured and replayed with new inputs and eager work between."""
+    h, v, m, k = 320, 9000, 2, 3
+    a = torch.zeros(n, h, dtype=torch.bfloat16, device=dev())
+    tok = torch.zeros(n, m, dtype=torch.int64, device=dev())
+    g, gt = torch.zeros(n, m, device=dev()), torch.zeros(n, k, device=dev())
+    w = (0.05 * torch.randn(v, h, generator=torch.Generator().manual_seed(1))).to(dev(), torch.bfloat16)
+
+    def step():
+        f = itl.linear_token_logp_fwd(a, w, tok, top_k=k, return_entropy=True)
+        return [*f, *itl.linear_token_logp_bwd(a, w, f.lse, tok, f.logp, g, f.top_ids, f.top_logp, gt, entropy=f.entropy,
+                                               grad_entropy=g[:, 0].contiguous(), out_dtype=torch.bfloat16)]
+
+    def fill(seed):
+        gen = torch.Generator(dev()).manual_seed(seed)
+        a.normal_(generator=gen)
+        tok.copy_(torch.randint(0, v, (n, m), generator=gen, device=dev()))
+        tok[seed] = -100
+        g.normal_(generator=gen)
+        gt.normal_(generator=gen)
+
+    fill(0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for seed in (1, 2, 3):
+        fill(seed)
+        graph.replay()
+        torch.cuda.synchronize()
+        for i, (x, y) in enumerate(zip(out, step())):
+            assert torch.equal(x, y), (seed, i)
+        torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("n", [5, 16640])
+def test_strided_outputs_of_the_segmented_backward(n):
+    """dhidden and dweight in views with longer, unaligned rows, in parts and
+    walked: the same bits, and nothing written beside them."""
+    h, v = 320, 9000
+    a, b, _ = head_operands(n, h, v, False, seed=n)
+    tok = torch.randint(0, v, (n, 2), generator=torch.Generator().manual_seed(n)).to(dev())
+    g = torch.randn(n, 2, generator=torch.Generator().manual_seed(n)).to(dev())
+    f = itl.linear_token_logp_fwd(a, b, tok, temperature=50.0)
+    for dtype in (torch.float32, torch.bfloat16):
+        want = itl.linear_token_logp_bwd(a, b, f.lse, tok, f.logp, g, temperature=50.0, out_dtype=dtype)
+        bufs = [torch.full((rows, h + 5), 9.0, dtype=dtype, device=dev()) for rows in (n, v)]
+        got = itl.linear_token_logp_bwd(a, b, f.lse, tok, f.logp, g, temperature=50.0, out_dtype=dtype,
+                                        dhidden_out=bufs[0][:, 3:h + 3], dweight_out=bufs[1][:, 3:h + 3])
+        for x, y, buf in zip(want, got, bufs):
+            assert torch.equal(x, y) and (buf[:, :3] == 9).all() and (buf[:, h + 3:] == 9).all()
