@@ -268,7 +268,9 @@ __device__ __forceinline__ void load_keys(const uint32_t* g, int64_t b0, int64_t
 // Replaces the kNanKey of tiles b0 + 64 c + lane by the key of the greatest of
 // the tile's logits that is no NaN (-inf when there is none), one tile after the
 // other: a row with a NaN has no probabilities, so what counts is that its
-// alternatives are right, and that rows without one only pay the test.
+// alternatives are right, and that rows without one only pay the test (no time
+// in 249 us for 16 rows).  16 rows of nothing but NaN take 1.2 ms at V = 151936,
+// 4096 such rows 2.5 ms more than others.
 template <typename T, int GW, int N>
 __device__ __forceinline__ void ordered_keys(const T* row, float inv_t, uint32_t v, int64_t b0,
                                              int lane, uint32_t (&key)[N]) {
