@@ -19,7 +19,20 @@ from .ops import (  # noqa: F401
     logp_fwd,
     prepare_weight,
 )
+from .layer_ops import (  # noqa: F401
+    dropout,
+    dropout_bwd,
+    dropout_fwd,
+    embedding,
+    embedding_bwd,
+    embedding_fwd,
+    layer_norm,
+    layer_norm_bwd,
+    layer_norm_fwd,
+    quantize_rows_fp4,
+)
 from .token_ops import (  # noqa: F401
+    Fp4Rows,
     QuantizedRows,
     TokenLogp,
     batch_invariant_token_logp,

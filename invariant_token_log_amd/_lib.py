@@ -45,7 +45,7 @@ LOGP_TOKEN_ROUND_BF16 = 2
 LOGP_TOKEN_Q8 = 4
 
 _i32, _i64, _sz, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
-_f32 = ctypes.c_float
+_f32, _f64 = ctypes.c_float, ctypes.c_double
 
 _SIGNATURES = {
     "logp_fwd_workspace_bytes": (_sz, [_i64, _i64, _i32, _i32, _i32]),
@@ -90,6 +90,22 @@ _SIGNATURES = {
     "rms_norm_bwd_workspace_bytes": (_sz, [_i64, _i64]),
     "rms_norm_bwd": (_i32, [_vp, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _i32, _i64, _i64, _vp,
                             _i64, _vp, _vp, _sz, _vp]),
+    "embedding_fwd": (_i32, [_vp, _i64, _i64, _i64, _i32, _vp, _i32, _i64, _i64, _f32, _vp, _i64,
+                             _vp]),
+    "embedding_fp4_fwd": (_i32, [_vp, _i64, _vp, _i64, _i64, _i64, _vp, _i32, _i64, _i64, _f32,
+                                 _i32, _vp, _i64, _vp]),
+    "embedding_bwd_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "embedding_bwd": (_i32, [_vp, _i64, _i32, _vp, _i32, _i64, _i64, _i64, _i64, _f32, _i32, _i32,
+                             _vp, _i64, _vp, _sz, _vp]),
+    "dropout_fwd": (_i32, [_vp, _i64, _vp, _i64, _i32, _i64, _i64, _f64, _i64, _vp, _i64, _i64,
+                           _vp, _i64, _vp]),
+    "layer_norm_fwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _vp, _i32, _i64, _i64, _f32, _f64, _i64,
+                              _vp, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp]),
+    "layer_norm_bwd_workspace_bytes": (_sz, [_i64, _i64]),
+    "layer_norm_bwd": (_i32, [_vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _i32, _i64, _i64,
+                              _f64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                              _sz, _vp]),
+    "fp4_quantize": (_i32, [_vp, _i64, _i32, _i64, _i64, _vp, _i64, _vp, _i64, _vp]),
     "logp_status_str": (ctypes.c_char_p, [_i32]),
     "logp_contract_id": (ctypes.c_char_p, []),
 }

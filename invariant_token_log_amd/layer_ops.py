@@ -1,0 +1,308 @@
+"""The other end of the tied table and the residual stream: embedding with its
+gradient by sorted tokens, dropout from a counter-based generator, layer norm,
+4-bit rows.
+
+Argument marshalling only (the C ABI is include/invariant_layers.h), as in
+token_ops.py; what is said there of HIP graphs holds here too.
+
+Dropout's mask is never stored: it is a function of (seed, draw, row number,
+column), and the backward pass computes it again.  seed is an integer, or a
+one-element int64 tensor on the device that is read when the kernel runs, so
+that a captured graph draws anew whenever the tensor changes; between a forward
+and its backward it must stay as it is.  draw tells the calls of one seed apart
+(a layer's number), first_row numbers a part of a batch as the whole would.
+"""
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _lib
+from .ops import _DTYPES, _INDEX, _dtype_code, _nbytes, _ptr, _row_vector
+from .token_ops import (Fp4Rows, _call, _fp4_operand, _norm_out, _norm_rows, _norm_weight,
+                        _same_device, _stride, _workspace)
+
+
+def _ids(t, device):
+    if t.dtype not in _INDEX:
+        raise TypeError("token_ids must be int64 or int32")
+    if t.device != device:
+        raise ValueError("token_ids must be on the table's device")
+    return t.contiguous(), t.numel(), _INDEX[t.dtype]
+
+
+def _table(t, name):
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1) or not t.is_cuda:
+        raise ValueError(f"{name} must be [V, H] with contiguous rows on a ROCm device")
+    return t.shape[0], t.shape[1], _stride(t)
+
+
+def embedding_fwd(token_ids, weight, scale=1.0, ignore_index=-100, out=None, out_dtype=None):
+    """Rows of weight [V, H] (float32, bfloat16, float16, or Fp4Rows) by token,
+    times scale: [*token_ids.shape, H] in the weight's dtype (out_dtype, bfloat16
+    unless given, from Fp4Rows).  token_ids int64 or int32; one equal to
+    ignore_index gives a row of zeros, any other outside [0, V) a row of NaN."""
+    fp4 = isinstance(weight, Fp4Rows)
+    if fp4:
+        v, h = _fp4_operand(weight, "weight")
+        dev, dtype = weight.data.device, out_dtype or torch.bfloat16
+    else:
+        v, h, ld = _table(weight, "weight")
+        dev, dtype = weight.device, weight.dtype
+        if out_dtype not in (None, dtype):
+            raise ValueError("out_dtype is for Fp4Rows; other tables give rows of their own dtype")
+    if dtype not in _DTYPES:
+        raise TypeError("rows must be float32, bfloat16 or float16")
+    tok, n, tcode = _ids(token_ids, dev)
+    shape = (*token_ids.shape, h)
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=dev)
+    elif tuple(out.shape) != shape or out.dtype != dtype or out.device != dev:
+        raise ValueError(f"out must be a {dtype} tensor of shape {shape}")
+    po, _, _, ld_o = _norm_rows(out, "out")
+    if fp4:
+        _call("embedding_fp4_fwd", dev, weight.data.data_ptr(), _stride(weight.data),
+              weight.scale.data_ptr(), _stride(weight.scale), v, h, tok.data_ptr(), tcode, n,
+              int(ignore_index), float(scale), _DTYPES[dtype], po, ld_o)
+    else:
+        _call("embedding_fwd", dev, weight.data_ptr(), ld, v, h, _DTYPES[dtype], tok.data_ptr(),
+              tcode, n, int(ignore_index), float(scale), po, ld_o)
+    return out
+
+
+def embedding_bwd(token_ids, grad, num_rows, scale=1.0, ignore_index=-100, out_dtype=None,
+                  dweight_out=None, accumulate=False, workspace=None):
+    """Gradient [num_rows, H] of embedding_fwd's weight from grad
+    [*token_ids.shape, H], in grad's dtype (out_dtype: that or float32): for every
+    token the sum over its occurrences in ascending order, in float32, rounded
+    once.  accumulate adds it to dweight_out, e.g. the dweight of a tied LM head
+    (linear_token_logp_bwd), and leaves the rows of absent tokens as they are."""
+    pg, n, h, ld_g = _norm_rows(grad, "grad")
+    dev = grad.device
+    tok, nt, tcode = _ids(token_ids, dev)
+    if tuple(grad.shape[:-1]) != tuple(token_ids.shape):
+        raise ValueError("grad must be [*token_ids.shape, H]")
+    code = _dtype_code(grad)
+    v = int(num_rows)
+    if dweight_out is None:
+        if accumulate:
+            raise ValueError("accumulate needs the dweight_out that it adds to")
+        dweight_out = torch.empty(v, h, dtype=out_dtype or grad.dtype, device=dev)
+    if out_dtype not in (None, dweight_out.dtype):
+        raise ValueError("dweight_out must be of out_dtype")
+    if dweight_out.dtype not in (grad.dtype, torch.float32):
+        raise TypeError("dweight must be float32 or of grad's dtype")
+    v2, h2, ld = _table(dweight_out, "dweight_out")
+    if (v2, h2) != (v, h) or dweight_out.device != dev:
+        raise ValueError("dweight_out must be [num_rows, H] on grad's device")
+    ws = _workspace(workspace, _lib.lib().embedding_bwd_workspace_bytes(nt, v, h), dev)
+    _call("embedding_bwd", dev, pg, ld_g, code, tok.data_ptr(), tcode, nt, v, h, int(ignore_index),
+          float(scale), _DTYPES[dweight_out.dtype], int(bool(accumulate)), dweight_out.data_ptr(),
+          ld, _ptr(ws), _nbytes(ws))
+    return dweight_out
+
+
+class _Embedding(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, token_ids, weight, scale, ignore_index):
+        ctx.save_for_backward(token_ids)
+        ctx.options = (weight.shape[0], scale, ignore_index)
+        return embedding_fwd(token_ids, weight, scale, ignore_index)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g):
+        (token_ids,) = ctx.saved_tensors
+        return None, embedding_bwd(token_ids, g.contiguous(), *ctx.options), None, None
+
+
+def embedding(token_ids, weight, scale=1.0, ignore_index=-100):
+    """Differentiable embedding_fwd of a weight [V, H] (not Fp4Rows): its gradient
+    is whole, in the weight's dtype."""
+    return _Embedding.apply(token_ids, weight, float(scale), int(ignore_index))
+
+
+def _seed(seed, device):
+    """(value, pointer or None) of a seed."""
+    if isinstance(seed, torch.Tensor):
+        if seed.dtype != torch.int64 or seed.numel() != 1 or seed.device != device:
+            raise ValueError("a seed tensor must be one int64 on the rows' device")
+        return 0, seed.data_ptr()
+    value = int(seed) & (2 ** 64 - 1)
+    return value - 2 ** 64 if value >= 2 ** 63 else value, None
+
+
+def dropout_fwd(x, p, seed, residual=None, draw=0, first_row=0, out=None):
+    """residual + dropped(x) (dropped(x) without a residual), rounded once to x's
+    dtype: an element of x [*lead, H] (float32, bfloat16, float16) is dropped with
+    probability p (to 2^-16), the others are scaled by the reciprocal of what is
+    kept.  out may be x or residual."""
+    px, n, h, ld_x = _norm_rows(x, "x")
+    code = _dtype_code(x)
+    pr, ld_r = None, 0
+    if residual is not None:
+        pr, _, _, ld_r = _norm_rows(residual, "residual", x)
+    out, po, ld_o = _norm_out(out, "out", x, h)
+    value, at = _seed(seed, x.device)
+    _call("dropout_fwd", x.device, px, ld_x, pr, ld_r, code, n, h, float(p), value, at, int(draw),
+          int(first_row), po, ld_o)
+    return out
+
+
+def dropout_bwd(grad, p, seed, draw=0, first_row=0, dx_out=None):
+    """Gradient of dropout_fwd's x from that of its output (which is the
+    residual's gradient itself).  dx_out may be grad."""
+    return dropout_fwd(grad, p, seed, None, draw, first_row, dx_out)
+
+
+class _Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, p, seed, residual, draw, first_row):
+        held = isinstance(seed, torch.Tensor)
+        ctx.save_for_backward(seed if held else None)
+        ctx.options = (p, seed if not held else None, draw, first_row)
+        return dropout_fwd(x, p, seed, residual, draw, first_row)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g):
+        p, seed, draw, first_row = ctx.options
+        if seed is None:
+            (seed,) = ctx.saved_tensors
+        g = g.contiguous()
+        dx = dropout_bwd(g, p, seed, draw, first_row) if ctx.needs_input_grad[0] else None
+        return dx, None, None, g if ctx.needs_input_grad[3] else None, None, None
+
+
+def dropout(x, p, seed, residual=None, draw=0, first_row=0):
+    """Differentiable dropout_fwd; the mask is computed again in the backward."""
+    return _Dropout.apply(x, float(p), seed, residual, int(draw), int(first_row))
+
+
+def _norm_bias(bias, x):
+    return _norm_weight(bias, x, "bias") if bias is not None else None
+
+
+def _drop_args(p, seed, draw, first_row, device):
+    """The library's (p, seed, its address, draw, first row)."""
+    if not p:
+        return 0.0, 0, None, 0, 0
+    if seed is None:
+        raise ValueError("dropout needs a seed")
+    return (float(p), *_seed(seed, device), int(draw), int(first_row))
+
+
+def layer_norm_fwd(x, weight, bias=None, residual=None, eps=1e-5, dropout=0.0, seed=None, draw=0,
+                   first_row=0, return_stats=False, y_out=None, sum_out=None):
+    """Layer norm of s = residual + dropped(x) (dropout_fwd's arguments; s = x
+    without either), rounded to x's dtype before it is normed: (y, s, mean, rstd),
+    y = (s - mean(s)) / sqrt(var(s) + eps) * weight + bias, mean and rstd [N]
+    float32 (None unless asked for).  x [*lead, H] float32, bfloat16 or float16,
+    weight and bias [H].  sum_out receives s and may be x or residual."""
+    px, n, h, ld_x = _norm_rows(x, "x")
+    code = _dtype_code(x)
+    pw, pb = _norm_weight(weight, x), _norm_bias(bias, x)
+    dev = x.device
+    drop = _drop_args(dropout, seed, draw, first_row, dev)
+    y, py, ld_y = _norm_out(y_out, "y_out", x, h)
+    pr, ld_r, ps, ld_s, s = None, 0, None, 0, x
+    if residual is not None:
+        pr, _, _, ld_r = _norm_rows(residual, "residual", x)
+    if residual is not None or drop[0] or sum_out is not None:
+        s, ps, ld_s = _norm_out(sum_out, "sum_out", x, h)
+    mean, rstd = None, None
+    if return_stats:
+        mean, rstd = torch.empty(2, n, dtype=torch.float32, device=dev)
+    _call("layer_norm_fwd", dev, px, ld_x, pr, ld_r, pw, pb, code, n, h, float(eps), *drop, py,
+          ld_y, ps, ld_s, _ptr(mean), _ptr(rstd))
+    return y, s, mean, rstd
+
+
+def layer_norm_bwd(s, weight, mean, rstd, grad_y, grad_sum=None, dropout=0.0, seed=None, draw=0,
+                   first_row=0, need_dresidual=True, need_dweight=True, need_dbias=True,
+                   dx_out=None, dresidual_out=None, workspace=None):
+    """(dx, dresidual, dweight, dbias) of layer_norm_fwd from its stored sum s,
+    mean, rstd and the gradients of y and (where given) of s.  Without dropout
+    dresidual is dx itself.  dx_out and dresidual_out may be grad_y or grad_sum,
+    not one another; what is not needed is None."""
+    p_s, n, h, ld_s = _norm_rows(s, "s")
+    code = _dtype_code(s)
+    pw = _norm_weight(weight, s)
+    dev = s.device
+    drop = _drop_args(dropout, seed, draw, first_row, dev)
+    pg, _, _, ld_g = _norm_rows(grad_y, "grad_y", s)
+    pd, ld_d = None, 0
+    if grad_sum is not None:
+        pd, _, _, ld_d = _norm_rows(grad_sum, "grad_sum", s)
+    mean, rstd = _row_vector(mean, n, "mean"), _row_vector(rstd, n, "rstd")
+    _same_device(dev, mean=mean, rstd=rstd)
+    dx, px, ld_x = _norm_out(dx_out, "dx_out", s, h)
+    dres, pr, ld_r = dx, None, 0
+    if not need_dresidual:
+        dres = None
+    elif drop[0]:
+        dres, pr, ld_r = _norm_out(dresidual_out, "dresidual_out", s, h)
+    if dresidual_out is not None and pr is None:
+        raise ValueError("dresidual_out is for a gradient through dropout that is asked for")
+    dw = torch.empty(h, dtype=s.dtype, device=dev) if need_dweight else None
+    db = torch.empty(h, dtype=s.dtype, device=dev) if need_dbias else None
+    need = _lib.lib().layer_norm_bwd_workspace_bytes(n, h) if need_dweight or need_dbias else 0
+    ws = _workspace(workspace, need, dev)
+    _call("layer_norm_bwd", dev, p_s, ld_s, pw, mean.data_ptr(), rstd.data_ptr(), pg, ld_g, pd,
+          ld_d, code, n, h, *drop, px, ld_x, pr, ld_r, _ptr(dw), _ptr(db), _ptr(ws), _nbytes(ws))
+    return dx, dres, dw, db
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, eps, p, seed, draw, first_row):
+        y, s, mean, rstd = layer_norm_fwd(x, weight, bias, residual, eps, p, seed, draw, first_row,
+                                          return_stats=True)
+        held = isinstance(seed, torch.Tensor)
+        ctx.save_for_backward(s, weight, mean, rstd, seed if held else None)
+        ctx.options = (p, None if held else seed, draw, first_row)
+        ctx.fused = residual is not None
+        ctx.set_materialize_grads(False)
+        return (y, s) if ctx.fused else y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, gy, gs=None):
+        s, weight, mean, rstd, held = ctx.saved_tensors
+        p, seed, draw, first_row = ctx.options
+        seed = held if seed is None else seed
+        need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
+        if gy is None:  # only the stored sum was used, or nothing
+            gs = gs.contiguous() if gs is not None else None
+            dx = gs
+            if p and need_x and gs is not None:
+                dx = dropout_bwd(gs, p, seed, draw, first_row)
+            zero = torch.zeros_like(weight) if need_w or need_b else None
+            return dx, zero if need_w else None, zero if need_b else None, gs, *[None] * 5
+        # gradients may come in broadcast (a row for all rows, one value for all)
+        gs = gs.contiguous() if gs is not None else None
+        dx, dres, dw, db = layer_norm_bwd(s, weight, mean, rstd, gy.contiguous(), gs, p, seed, draw,
+                                          first_row, need_r, need_w, need_b)
+        return dx, dw, db, dres, *[None] * 5
+
+
+def layer_norm(x, weight, bias=None, residual=None, eps=1e-5, dropout=0.0, seed=None, draw=0,
+               first_row=0):
+    """Differentiable layer_norm_fwd: y, or (y, s) with a residual."""
+    return _LayerNorm.apply(x, weight, bias, residual, float(eps), float(dropout), seed, int(draw),
+                            int(first_row))
+
+
+def quantize_rows_fp4(x):
+    """x [N, H] (float32, bfloat16, float16; H a multiple of 32) as Fp4Rows, e.g. a
+    frozen table that embedding_fwd and linear_token_logp_fwd share, made once per
+    weight version.  A group's scale is the smallest power of two that brings it
+    within 6, the greatest e2m1 value."""
+    if x.dim() != 2:
+        raise ValueError("x must be [N, H]")
+    px, n, h, ld = _norm_rows(x, "x")
+    code = _dtype_code(x)
+    data = torch.empty(n, h // 2, dtype=torch.uint8, device=x.device)
+    scale = torch.empty(n, h // 32, dtype=torch.uint8, device=x.device)
+    _call("fp4_quantize", x.device, px, ld, code, n, h, data.data_ptr(), h // 2, scale.data_ptr(),
+          h // 32)
+    return Fp4Rows(data, scale)

@@ -43,6 +43,15 @@ class QuantizedRows(NamedTuple):
     scale: torch.Tensor
 
 
+class Fp4Rows(NamedTuple):
+    """4-bit rows: data [N, H / 2] uint8, two e2m1 values a byte (the even
+    column in the low half), and scale [N, H / 32] uint8, one byte b for every 32
+    columns, which stands for 2^(b - 127); both with contiguous rows."""
+
+    data: torch.Tensor
+    scale: torch.Tensor
+
+
 def _call(name, device, *args):
     """The library function on the device's current stream (its last
     argument), with that device current; a non-zero status raises."""
@@ -247,6 +256,24 @@ def _q8_operand(q, name):
             or not q.scale.is_contiguous() or q.scale.device != q.data.device):
         raise TypeError(f"{name}.scale must be contiguous float32 with one entry per row")
     return q.data.shape
+
+
+def _fp4_operand(q, name):
+    """[rows, H] of 4-bit rows."""
+    for part in q:
+        if part.dtype != torch.uint8 or part.dim() != 2 or (part.stride(1) != 1 and part.shape[1] > 1):
+            raise TypeError(f"{name}: Fp4Rows hold [rows, H / 2] and [rows, H / 32] uint8 with "
+                            "contiguous rows")
+    rows, h = q.data.shape[0], 2 * q.data.shape[1]
+    if h % 32 or tuple(q.scale.shape) != (rows, h // 32):
+        raise ValueError(f"{name}: Fp4Rows take H a multiple of 32 and one scale for 32 columns")
+    if not q.data.is_cuda or q.scale.device != q.data.device:
+        raise ValueError(f"{name} must be on one ROCm device")
+    return rows, h
+
+
+def _stride(t):
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
 def linear_token_logp_fwd(hidden, weight, token_ids=None, top_k=0, ignore_index=-100,
@@ -458,10 +485,10 @@ def _norm_out(given, name, like, h):
     return given, p, ld
 
 
-def _norm_weight(weight, x):
+def _norm_weight(weight, x, name="weight"):
     if (weight.shape != x.shape[-1:] or weight.dtype != x.dtype or weight.device != x.device
             or not weight.is_contiguous()):
-        raise ValueError("weight must be a contiguous [H] of x's dtype and device")
+        raise ValueError(f"{name} must be a contiguous [H] of x's dtype and device")
     return weight.data_ptr()
 
 
