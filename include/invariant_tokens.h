@@ -101,17 +101,21 @@ int32_t token_logp_bwd(const void* logits, int32_t dtype, int64_t n, int64_t v, 
 enum logp_token_flags {
   LOGP_TOKEN_KEEPS_LOGITS = 1, /* logits_out is given */
   LOGP_TOKEN_ROUND_BF16 = 2,   /* logits_rounding is LOGP_ROUND_BF16 */
-  LOGP_TOKEN_Q8 = 4            /* linear_token_logp_q8_fwd */
+  LOGP_TOKEN_Q8 = 4,           /* linear_token_logp_q8_fwd */
+  LOGP_TOKEN_FP4 = 8           /* linear_token_logp_fp4_fwd (may be joined by ROUND_BF16) */
 };
 
 /*
- * Workspace of linear_token_logp_fwd / linear_token_logp_q8_fwd in bytes.
+ * Workspace of linear_token_logp_fwd / linear_token_logp_q8_fwd /
+ * linear_token_logp_fp4_fwd in bytes.
  * The head's rows are taken row_chunk at a time (rounded up to a multiple of
  * 256); per chunk it holds the tile statistics, a re-laid copy of the hidden
  * rows and, unless logits_out is given or the call has no alternatives and at
  * most one given token a row, the chunk's logits (fp32, bf16 with
  * LOGP_TOKEN_ROUND_BF16), 2.5 GB for 4096 rows of 151936 columns.  row_chunk 0
  * takes 4096 rows where the chunk's logits are in the workspace, else 65536.
+ * With LOGP_TOKEN_FP4 and more than 256 rows it also holds a bf16 copy of the
+ * weight (v rounded up to a multiple of 256, times 2 h bytes).
  * Any row_chunk gives the same bits.  0 for arguments the call would reject.
  */
 size_t linear_token_logp_fwd_workspace_bytes(int64_t n, int64_t h, int64_t v, int64_t m,
@@ -186,6 +190,26 @@ int32_t linear_token_logp_q8_fwd(const void* hidden, int64_t ld_h, const float* 
                                  float* lse_out, float* entropy_out, float* top_logp_out,
                                  int64_t* top_ids_out, int64_t row_chunk, void* workspace,
                                  size_t workspace_bytes, void* hip_stream);
+
+/*
+ * The forward through a 4-bit LM head (frozen weights: decoding, scoring):
+ * linear_token_logp_fwd, with the same bits, on the weight that the 4-bit rows
+ * data [v, ld_d] and scales [v, ld_s] stand for (fp4_quantize of
+ * invariant_layers.h), whose values are exact in bf16 (scale bytes 253 and 254
+ * give infinities where a value passes its range, 255 gives NaN).
+ *   hidden  bf16, as linear_token_logp_fwd.  16-byte aligned data rows
+ *           (LOGP_ERR_ALIGN); scales of any alignment.
+ *   The rest: as linear_token_logp_fwd (workspace flag LOGP_TOKEN_FP4, with
+ *   LOGP_TOKEN_ROUND_BF16 where logits_rounding asks for it); no logits output.
+ */
+int32_t linear_token_logp_fp4_fwd(const void* hidden, int64_t ld_h, const void* data, int64_t ld_d,
+                                  const void* scales, int64_t ld_s, int64_t n, int64_t h,
+                                  int64_t v, const void* tokens, int32_t token_dtype, int64_t m,
+                                  int64_t ignore_index, float temperature, int32_t logits_rounding,
+                                  int32_t top_k, float* logp_out, float* lse_out,
+                                  float* entropy_out, float* top_logp_out, int64_t* top_ids_out,
+                                  int64_t row_chunk, void* workspace, size_t workspace_bytes,
+                                  void* hip_stream);
 
 /*
  * Root-mean-square norm with the residual's addition:

@@ -43,6 +43,7 @@ LOGP_MAX_TOP = 64
 LOGP_TOKEN_KEEPS_LOGITS = 1
 LOGP_TOKEN_ROUND_BF16 = 2
 LOGP_TOKEN_Q8 = 4
+LOGP_TOKEN_FP4 = 8
 
 _i32, _i64, _sz, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
 _f32, _f64 = ctypes.c_float, ctypes.c_double
@@ -83,6 +84,9 @@ _SIGNATURES = {
     "linear_token_logp_q8_fwd": (_i32, [_vp, _i64, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _vp,
                                         _i32, _i64, _i64, _f32, _i32, _vp, _vp, _vp, _vp, _vp,
                                         _i64, _vp, _sz, _vp]),
+    "linear_token_logp_fp4_fwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _vp,
+                                         _i32, _i64, _i64, _f32, _i32, _i32, _vp, _vp, _vp, _vp,
+                                         _vp, _i64, _vp, _sz, _vp]),
     "rms_norm_fwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _i32, _i64, _i64, _f32, _vp, _i64, _vp,
                             _i64, _vp, _vp]),
     "rms_norm_q8_fwd": (_i32, [_vp, _i64, _vp, _i64, _vp, _i32, _i64, _i64, _f32, _vp, _i64, _vp,

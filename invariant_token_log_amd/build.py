@@ -22,7 +22,8 @@ LIB_NAME = "libinvariant_logp.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = ["api.hip", "logp_kernels.hip", "linear_logp.hip", "linear_bwd.hip",
            "token_api.hip", "token_logp.hip", "linear_q8.hip", "rms_norm.hip",
-           "layer_api.hip", "embedding.hip", "dropout.hip", "layer_norm.hip", "fp4.hip"]
+           "layer_api.hip", "embedding.hip", "dropout.hip", "layer_norm.hip", "fp4.hip",
+           "linear_fp4.hip"]
 # bandwidth probes that bench.py times next to the kernels (not part of the
 # library's C ABI)
 PROBE_PATH = os.path.join(HERE, "libitl_ceiling.so")

@@ -3,6 +3,8 @@
 #include "invariant_tokens.h"
 
 #include "api_checks.h"
+#include "fp4.h"
+#include "linear_fp4.h"
 #include "linear_q8.h"
 #include "rms_norm.h"
 
@@ -65,13 +67,15 @@ StreamLayout stream_layout(int64_t n, int64_t v, int32_t dtype, int32_t w, int32
 }
 
 // The head's forward, rc rows at a time: tile statistics [rc, T] (m, s, w),
-// the one given token's logits, the rows' activity, the re-laid hidden rows
-// and the chunk's logits.
+// the one given token's logits, the rows' activity, the re-laid hidden rows,
+// the chunk's logits and, once for all chunks, the decoded copy of a 4-bit
+// weight.
 struct HeadLayout {
   int64_t rc, ntiles, ld_z;
   int tile;  // vocabulary columns of a statistic tile
   bool single, own_z;
-  size_t pm, ps, pw, pt, act, hb, z, total;
+  bool direct;  // 4-bit weight, read as it is
+  size_t pm, ps, pw, pt, act, hb, z, wd, total;
 };
 
 HeadLayout head_layout(int64_t n, int64_t h, int64_t v, int64_t m, int32_t top_k, int32_t flags,
@@ -95,10 +99,15 @@ HeadLayout head_layout(int64_t n, int64_t h, int64_t v, int64_t m, int32_t top_k
   l.pt = 3 * table;
   l.act = l.pt + ws_round(rows * 4);
   l.hb = l.act + ws_round(rows * 4);
+  l.direct = (flags & LOGP_TOKEN_FP4) && n <= itl::kFp4Direct;
   const int64_t hb = flags & LOGP_TOKEN_Q8 ? itl::q8_fwd_scratch_bytes(l.rc, h)
+                     : l.direct            ? 0
                                            : itl::linear_fwd_blocked_bytes(l.rc, h);
   l.z = l.hb + ws_round(static_cast<size_t>(hb));
-  l.total = l.z + (l.own_z ? ws_round(rows * static_cast<size_t>(l.ld_z) * zsize) : 0);
+  l.wd = l.z + (l.own_z ? ws_round(rows * static_cast<size_t>(l.ld_z) * zsize) : 0);
+  l.total = l.wd + ((flags & LOGP_TOKEN_FP4) && !l.direct
+                        ? ws_round(static_cast<size_t>(itl::fp4_decoded_bytes(v, h)))
+                        : 0);
   return l;
 }
 
@@ -131,6 +140,7 @@ struct HeadArgs {
   int64_t ld_z;
   const uint16_t* wblk;
   bool q8;
+  const itl::Fp4Weight* fp4;  // or null
 };
 
 // Rows r0 .. of every row operand.
@@ -153,6 +163,12 @@ void run_head(const HeadArgs& a, const HeadLayout& l, char* ws, hipStream_t s) {
   int32_t* act = reinterpret_cast<int32_t*>(ws + l.act);
   const int ntiles = static_cast<int>(l.ntiles);
   const int esize = a.q8 ? 1 : 2;
+  const uint16_t* wblk = a.wblk;
+  if (a.fp4 && !l.direct) {
+    uint16_t* decoded = reinterpret_cast<uint16_t*>(ws + l.wd);
+    itl::launch_fp4_decode(*a.fp4, a.v, a.h, decoded, s);
+    wblk = decoded;
+  }
   for (int64_t r0 = 0; r0 < a.n; r0 += l.rc) {
     const int64_t rows = l.rc < a.n - r0 ? l.rc : a.n - r0;
     const itl::TokenView tok = token_rows(a.tok, r0);
@@ -177,11 +193,15 @@ void run_head(const HeadArgs& a, const HeadLayout& l, char* ws, hipStream_t s) {
                               a.hidden_scale + r0, static_cast<const uint8_t*>(a.weight), a.ld_w,
                               a.weight_scale, rows, a.h, a.v, tg, ignore, pm, ps, pt, a.inv_t, pw,
                               static_cast<float*>(z), ld_z, ws + l.hb, s);
+    else if (l.direct)
+      itl::launch_fp4_partials(reinterpret_cast<const uint16_t*>(hidden), a.ld_h, *a.fp4, rows, a.h,
+                               a.v, tg, ignore, pm, ps, pt, a.inv_t, a.round_bf16, pw, z, z_bf16,
+                               ld_z, s);
     else
       itl::launch_linear_partials(reinterpret_cast<const uint16_t*>(hidden), a.ld_h,
                                   static_cast<const uint16_t*>(a.weight), a.ld_w, rows, a.h, a.v,
                                   tg, ignore, pm, ps, pt, a.inv_t, a.round_bf16, pw, z, z_bf16,
-                                  ld_z, a.wblk, reinterpret_cast<uint16_t*>(ws + l.hb), s);
+                                  ld_z, wblk, reinterpret_cast<uint16_t*>(ws + l.hb), s);
     const bool read_z = !l.single && z;
     const int zdt = z_bf16 ? itl::kBF16 : itl::kF32;
     itl::launch_token_finish(zdt, read_z && rows_aligned16(z, ld_z, z_bf16 ? 2 : 4), l.tile,
@@ -270,7 +290,9 @@ int32_t token_logp_bwd(const void* logits, int32_t dtype, int64_t n, int64_t v, 
 
 size_t linear_token_logp_fwd_workspace_bytes(int64_t n, int64_t h, int64_t v, int64_t m,
                                              int32_t top_k, int32_t flags, int64_t row_chunk) {
-  if (check_head_sizes(n, h, v, m, top_k, row_chunk) != LOGP_OK || flags < 0 || flags > 7) return 0;
+  if (check_head_sizes(n, h, v, m, top_k, row_chunk) != LOGP_OK || flags < 0 || flags > 15 ||
+      ((flags & LOGP_TOKEN_FP4) && (flags & (LOGP_TOKEN_Q8 | LOGP_TOKEN_KEEPS_LOGITS))))
+    return 0;
   return head_layout(n, h, v, m, top_k, flags, row_chunk).total;
 }
 
@@ -364,6 +386,49 @@ int32_t linear_token_logp_q8_fwd(const void* hidden, int64_t ld_h, const float* 
   a.top_k = top_k;
   a.out = itl::TokenOut{logp_out, lse_out, entropy_out, top_logp_out, top_ids_out};
   a.q8 = true;
+  (void)hipGetLastError();
+  run_head(a, l, static_cast<char*>(workspace), static_cast<hipStream_t>(hip_stream));
+  return itl::launch_status();
+}
+
+int32_t linear_token_logp_fp4_fwd(const void* hidden, int64_t ld_h, const void* data, int64_t ld_d,
+                                  const void* scales, int64_t ld_s, int64_t n, int64_t h,
+                                  int64_t v, const void* tokens, int32_t token_dtype, int64_t m,
+                                  int64_t ignore_index, float temperature, int32_t logits_rounding,
+                                  int32_t top_k, float* logp_out, float* lse_out,
+                                  float* entropy_out, float* top_logp_out, int64_t* top_ids_out,
+                                  int64_t row_chunk, void* workspace, size_t workspace_bytes,
+                                  void* hip_stream) {
+  int32_t st = check_head_sizes(n, h, v, m, top_k, row_chunk);
+  if (st != LOGP_OK) return st;
+  if (ld_h < h || ld_d < h / 2 || ld_s < h / itl::kFp4Group) return LOGP_ERR_SHAPE;
+  if (!itl::usable_temperature(temperature) ||
+      (logits_rounding != LOGP_ROUND_NONE && logits_rounding != LOGP_ROUND_BF16))
+    return LOGP_ERR_VALUE;
+  if (n == 0) return LOGP_OK;
+  if ((st = check_tokens(tokens, token_dtype, m)) != LOGP_OK) return st;
+  if (!hidden || !data || !scales) return LOGP_ERR_NULL;
+  if ((st = check_outputs(m, top_k, logp_out, top_logp_out, top_ids_out)) != LOGP_OK) return st;
+  if (!rows_aligned16(hidden, ld_h, 2) || !rows_aligned16(data, ld_d, 1)) return LOGP_ERR_ALIGN;
+  const bool rounded = logits_rounding == LOGP_ROUND_BF16;
+  const HeadLayout l = head_layout(n, h, v, m, top_k,
+                                   LOGP_TOKEN_FP4 | (rounded ? LOGP_TOKEN_ROUND_BF16 : 0),
+                                   row_chunk);
+  if (!itl::ws_ok(workspace, workspace_bytes, l.total)) return LOGP_ERR_WORKSPACE;
+  const itl::Fp4Weight w{static_cast<const uint8_t*>(data), ld_d,
+                         static_cast<const uint8_t*>(scales), ld_s};
+  HeadArgs a{};
+  a.hidden = hidden;
+  a.ld_h = ld_h;
+  a.n = n;
+  a.h = h;
+  a.v = v;
+  a.tok = view_of(tokens, token_dtype, m, ignore_index);
+  a.inv_t = itl::reciprocal_temperature(temperature);
+  a.round_bf16 = rounded ? 1 : 0;
+  a.top_k = top_k;
+  a.out = itl::TokenOut{logp_out, lse_out, entropy_out, top_logp_out, top_ids_out};
+  a.fp4 = &w;
   (void)hipGetLastError();
   run_head(a, l, static_cast<char*>(workspace), static_cast<hipStream_t>(hip_stream));
   return itl::launch_status();

@@ -284,11 +284,14 @@ def linear_token_logp_fwd(hidden, weight, token_ids=None, top_k=0, ignore_index=
     [N, H] and weight [V, H] bfloat16, logits = hidden weight^T / temperature;
     token_ids [N, M].  hidden and weight may both be QuantizedRows: the 8-bit
     head of frozen weights (no round_logits, prepared_weight or logits_out).
+    weight may be Fp4Rows: the 4-bit head of frozen weights, with the bits of the
+    bfloat16 weight they stand for (no prepared_weight or logits_out; more than
+    256 rows take a bfloat16 copy of the weight in the workspace).
     round_logits and prepared_weight: as linear_logp_fwd.  logits_out [N, V]
     float32 (or bfloat16 with round_logits) receives the unscaled logits for
     linear_token_logp_bwd.  row_chunk: rows taken at a time, which bounds the
     workspace (0 = the library's default); any value gives the same bits."""
-    q8 = isinstance(hidden, QuantizedRows)
+    q8, fp4 = isinstance(hidden, QuantizedRows), isinstance(weight, Fp4Rows)
     if q8 != isinstance(weight, QuantizedRows):
         raise TypeError("hidden and weight must both be QuantizedRows, or neither")
     L = _lib.lib()
@@ -309,6 +312,19 @@ def linear_token_logp_fwd(hidden, weight, token_ids=None, top_k=0, ignore_index=
         ld_w = weight.data.stride(0) if v > 1 else h
         dev, pw = hidden.data.device, None
         flags = _lib.LOGP_TOKEN_Q8
+    elif fp4:
+        if prepared_weight is not None or z is not None:
+            raise ValueError("the 4-bit head takes no prepared_weight or logits_out")
+        if hidden.dtype != torch.bfloat16 or hidden.dim() != 2 or hidden.stride(1) != 1:
+            raise TypeError("hidden must be [N, H] bfloat16 with contiguous rows")
+        v, h = _fp4_operand(weight, "weight")
+        n, dev, pw = hidden.shape[0], hidden.device, None
+        if hidden.shape[1] != h:
+            raise ValueError("hidden and weight must share H")
+        if weight.data.device != dev:
+            raise ValueError("hidden and weight must be on one ROCm device")
+        ld_h = hidden.stride(0) if n > 1 else h
+        flags = _lib.LOGP_TOKEN_FP4 | (_lib.LOGP_TOKEN_ROUND_BF16 if round_logits else 0)
     else:
         n, h, v, ld_h, ld_w = _linear_operands(hidden, weight)
         dev = hidden.device
@@ -331,6 +347,11 @@ def linear_token_logp_fwd(hidden, weight, token_ids=None, top_k=0, ignore_index=
               hidden.scale.data_ptr(), weight.data.data_ptr(), ld_w, weight.scale.data_ptr(), n, h,
               v, _ptr(tok), tcode, m, int(ignore_index), float(temperature), k, *out.pointers(),
               int(row_chunk), _ptr(ws), _nbytes(ws))
+    elif fp4:
+        _call("linear_token_logp_fp4_fwd", dev, hidden.data_ptr(), ld_h, weight.data.data_ptr(),
+              _stride(weight.data), weight.scale.data_ptr(), _stride(weight.scale), n, h, v,
+              _ptr(tok), tcode, m, int(ignore_index), float(temperature), _rounding(round_logits), k,
+              *out.pointers(), int(row_chunk), _ptr(ws), _nbytes(ws))
     else:
         _call("linear_token_logp_fwd", dev, hidden.data_ptr(), ld_h, weight.data_ptr(), ld_w, n, h,
               v, _ptr(tok), tcode, m, int(ignore_index), float(temperature),
@@ -603,15 +624,23 @@ def norm_linear_token_logp(x, norm_weight, weight, token_ids=None, residual=None
     TokenLogp.  x [N, H] bfloat16.  With a bfloat16 weight [V, H] it is
     differentiable in x, residual, norm_weight and weight (rms_norm, then
     linear_token_logp); with a QuantizedRows weight the normed rows are
-    quantised in the norm and the 8-bit head scores them (no gradient).  The
-    gradient of norm_weight sums over all rows, padding rows (whose part is 0)
+    quantised in the norm and the 8-bit head scores them, with Fp4Rows the 4-bit
+    head scores them as they are (no gradient through either).  The gradient of norm_weight sums over all rows, padding rows (whose part is 0)
     included: they must be finite for it."""
-    if isinstance(weight, QuantizedRows):
-        if round_logits or save_logits or prepared_weight is not None:
+    if isinstance(weight, (QuantizedRows, Fp4Rows)):
+        fp4 = isinstance(weight, Fp4Rows)
+        bits = 4 if fp4 else 8
+        if fp4 and (save_logits or prepared_weight is not None):
+            raise ValueError("the 4-bit head takes no save_logits or prepared_weight")
+        if not fp4 and (round_logits or save_logits or prepared_weight is not None):
             raise ValueError("the 8-bit head takes no round_logits, save_logits or prepared_weight")
         if torch.is_grad_enabled() and any(t is not None and t.requires_grad
                                            for t in (x, norm_weight, residual)):
-            raise ValueError("the 8-bit head has no gradient: call it under torch.no_grad()")
+            raise ValueError(f"the {bits}-bit head has no gradient: call it under torch.no_grad()")
+        if fp4:
+            y, _, _ = rms_norm_fwd(x, norm_weight, residual, eps)
+            return linear_token_logp_fwd(y, weight, token_ids, top_k, ignore_index, temperature,
+                                         return_entropy, round_logits)
         hidden, _ = rms_norm_quantized(x, norm_weight, residual, eps)
         return linear_token_logp_fwd(hidden, weight, token_ids, top_k, ignore_index, temperature,
                                      return_entropy)

@@ -160,3 +160,40 @@ def test_seeds():
     with pytest.raises(ValueError, match="seed"):
         layer_ops._drop_args(0.1, None, 0, 0, dev)
     assert layer_ops._drop_args(0.0, None, 3, 4, dev) == (0.0, 0, None, 0, 0)
+
+
+def test_head(L):
+    flags = _lib.LOGP_TOKEN_FP4
+    need = L.linear_token_logp_fwd_workspace_bytes(8, 128, 3000, 2, 3, flags, 0)
+    assert need == L.linear_token_logp_fwd_workspace_bytes(8, 128, 3000, 2, 3, 0, 0)
+    many = L.linear_token_logp_fwd_workspace_bytes(257, 128, 3000, 2, 3, flags, 0)
+    # twelve blocks of 256 decoded rows
+    assert many == L.linear_token_logp_fwd_workspace_bytes(257, 128, 3000, 2, 3, 0, 0) + 12 * 256 * 128 * 2
+    for bad in (flags | 1, flags | 4, 16):
+        assert L.linear_token_logp_fwd_workspace_bytes(8, 128, 3000, 2, 3, bad, 0) == 0
+    base = dict(h_ptr=P, ld_h=128, d=P, ld_d=64, s=P, ld_s=4, n=8, h=128, v=3000, tokens=P, tdt=0, m=2, ignore=-100, temp=1.0,
+                rnd=0, k=3, logp=P, lse=P, ent=None, top=P, ids=P, rows=0, ws=P, ws_bytes=need, stream=None)
+    expect(L.linear_token_logp_fp4_fwd, base, [
+        (_lib.LOGP_ERR_SHAPE, dict(n=-1)), (_lib.LOGP_ERR_SHAPE, dict(h=96)), (_lib.LOGP_ERR_SHAPE, dict(v=0)),
+        (_lib.LOGP_ERR_SHAPE, dict(m=257)), (_lib.LOGP_ERR_SHAPE, dict(ld_h=127)), (_lib.LOGP_ERR_SHAPE, dict(ld_d=63)),
+        (_lib.LOGP_ERR_SHAPE, dict(ld_s=3)), (_lib.LOGP_ERR_SHAPE, dict(rows=-1)), (_lib.LOGP_ERR_VALUE, dict(k=65)),
+        (_lib.LOGP_ERR_VALUE, dict(temp=0.0)), (_lib.LOGP_ERR_VALUE, dict(rnd=2)), (_lib.LOGP_ERR_DTYPE, dict(tdt=3)),
+        (_lib.LOGP_ERR_NULL, dict(h_ptr=None)), (_lib.LOGP_ERR_NULL, dict(d=None)), (_lib.LOGP_ERR_NULL, dict(s=None)),
+        (_lib.LOGP_ERR_NULL, dict(tokens=None)), (_lib.LOGP_ERR_NULL, dict(logp=None)), (_lib.LOGP_ERR_NULL, dict(ids=None)),
+        (_lib.LOGP_ERR_ALIGN, dict(h_ptr=P + 8)), (_lib.LOGP_ERR_ALIGN, dict(ld_h=132)), (_lib.LOGP_ERR_ALIGN, dict(d=P + 8)),
+        (_lib.LOGP_ERR_ALIGN, dict(ld_d=72)), (_lib.LOGP_ERR_WORKSPACE, dict(ws=None)),
+        (_lib.LOGP_ERR_WORKSPACE, dict(ws_bytes=need - 1)), (OK, dict(n=0, h_ptr=None, d=None, s=None, ws=None)),
+    ])
+
+
+def test_head_binding():
+    q = itl.Fp4Rows(torch.zeros(9, 32, dtype=torch.uint8), torch.zeros(9, 2, dtype=torch.uint8))
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="4-bit head takes no"):
+        itl.linear_token_logp_fwd(x, q, logits_out=torch.zeros(4, 9))
+    with pytest.raises(TypeError, match="bfloat16"):
+        itl.linear_token_logp_fwd(x.float(), q)
+    with pytest.raises(TypeError, match="QuantizedRows"):
+        itl.linear_token_logp_fwd(itl.QuantizedRows(x.to(torch.float8_e4m3fn), torch.ones(4)), q)
+    with pytest.raises(ValueError, match="ROCm device"):
+        itl.linear_token_logp_fwd(x, q)
