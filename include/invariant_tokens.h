@@ -197,8 +197,9 @@ int32_t linear_token_logp_q8_fwd(const void* hidden, int64_t ld_h, const float* 
  * data [v, ld_d] and scales [v, ld_s] stand for (fp4_quantize of
  * invariant_layers.h), whose values are exact in bf16 (scale bytes 253 and 254
  * give infinities where a value passes its range, 255 gives NaN).
- *   hidden  bf16, as linear_token_logp_fwd.  16-byte aligned data rows
- *           (LOGP_ERR_ALIGN); scales of any alignment.
+ *   hidden  bf16, as linear_token_logp_fwd, rows at most 2^25 elements apart;
+ *           data and scale rows at most 2^23 bytes apart (LOGP_ERR_SHAPE), data
+ *           rows 16-byte aligned (LOGP_ERR_ALIGN), scales of any alignment.
  *   The rest: as linear_token_logp_fwd (workspace flag LOGP_TOKEN_FP4, with
  *   LOGP_TOKEN_ROUND_BF16 where logits_rounding asks for it); no logits output.
  */

@@ -18,6 +18,10 @@ struct Fp4Weight {
   int64_t ld_s;
 };
 
+// Bytes between the weight's rows, elements between the hidden rows, at most.
+constexpr int64_t kMaxFp4Stride = int64_t{1} << 23;
+constexpr int64_t kMaxHiddenStride = int64_t{1} << 25;
+
 // Up to this many rows the products read the 4-bit rows themselves; more rows
 // take the bf16 kernels on a decoded copy.
 constexpr int64_t kFp4Direct = 256;

@@ -10,10 +10,13 @@
 // row has the bits of the bf16 head on the decoded weight.
 //
 // Few rows: bound by the weight's bytes, 17 / 32 of a byte a value.  A workgroup
-// takes 256 columns and ROWS hidden rows, eight waves of 64 columns x ROWS / 2
-// rows.  Slots of 256 K values hold whole 128-byte lines of the weight's rows,
-// brought by direct loads, their scales, which pass through registers (their
-// rows have any alignment), and the hidden rows' pieces.
+// takes tiles of 256 columns x ROWS hidden rows, eight waves of 32 columns x
+// ROWS rows, so that every weight is decoded once.  Slots of 256 K values hold
+// whole 128-byte lines of the weight's rows and the hidden rows' pieces, panels
+// of two slots the scales (16 bytes a row: taken slot by slot their requests
+// were as many as the weight's, 16 us of 92), all brought by direct loads.  The
+// slots of a workgroup's tiles follow one another, so that the next tile's first
+// ones are on their way during a tile's epilogue.
 #include "linear_fp4.h"
 
 #include "fp4.h"
@@ -36,19 +39,26 @@ constexpr int kSlotK = kSlotSteps * BK;         // 256
 constexpr int kSlotBytes = kSlotK / 2;          // of a weight row: one line
 
 template <int ROWS>
-constexpr int kSlots = ROWS == 32 ? 3 : 2;
+constexpr int kSlots = ROWS == 64 ? 2 : 3;
+constexpr int kPanels = 3;  // those of slots p .. p + 2, each of which may begin one
+// Rows of the epilogue, whose waves take 64 columns x half of them.
+template <int ROWS>
+constexpr int kEpiRows = ROWS < 32 ? 32 : ROWS;
+template <int ROWS>
+constexpr int kMostRows = ROWS == 64 ? static_cast<int>(kFp4Direct) : ROWS;
 
 template <int ROWS>
-struct Fp4Stages {
-  uint8_t w[kSlots<ROWS>][BN * kSlotBytes];
-  uint16_t h[kSlots<ROWS>][ROWS * kSlotK];
-  uint16_t scale[kSlots<ROWS>][BN * kSlotSteps / 2];
+struct Fp4Slot {
+  uint8_t w[BN * kSlotBytes];
+  uint16_t h[ROWS * kSlotK];
 };
 
 template <int ROWS>
 struct SmemFp4 {
-  Fp4Stages<ROWS> st;
-  Reduce<ROWS> rd;
+  Fp4Slot<ROWS> slot[kSlots<ROWS>];
+  uint8_t scale[kPanels][BN * 2 * kSlotSteps];
+  Reduce<kEpiRows<ROWS>> rd;
+  int64_t target[kMostRows<ROWS>];
 };
 
 // Two scale bytes at any address.
@@ -56,8 +66,8 @@ struct __attribute__((packed)) ScalePair {
   uint16_t w;
 };
 
-// Eight weights (a dword of codes) under the scale 2^(b - 127) given as the fp32
-// with exponent b.
+// Eight weights (a dword of codes) under the scale 2^(b - 127) given as an fp32
+// with exponent bits b, whatever its other bits.
 __device__ __forceinline__ bf16x8 decode8(uint32_t q, float scale) {
   typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
   const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 0);
@@ -73,169 +83,356 @@ __device__ __forceinline__ bf16x8 decode8(uint32_t q, float scale) {
 __device__ __forceinline__ int weight_swz(int r) { return (r >> 1) & 7; }
 __device__ __forceinline__ int hidden_swz(int r) { return r & 15; }
 
-template <int ROWS>
-__device__ __forceinline__ void mainloop_fp4(Fp4Stages<ROWS>& sm,
-                                             const uint16_t* __restrict__ hidden, int64_t ld_h,
-                                             int64_t m0, int64_t n,
-                                             const uint8_t* __restrict__ data, int64_t ld_d,
-                                             const uint8_t* __restrict__ scales, int64_t ld_s,
-                                             int64_t v0, int64_t v, int ksteps,
-                                             f32x4 (&acc)[ROWS / 32][4]) {
-  constexpr int S = kSlots<ROWS>, MI = ROWS / 32;
-  constexpr int NH = ROWS / 16;      // hidden loads a wave and slot (1 KiB each: two rows)
-  constexpr int kLoads = 4 + NH;  // a slot's direct loads, beside those of its scales
-  const int tid = threadIdx.x, lane = tid % kWave;
-  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int wm = wave / 4, wn = wave % 4, li = lane % 16, g = lane / 16;
-  const int nslots = (ksteps + kSlotSteps - 1) / kSlotSteps;
-  const int last = ksteps - (nslots - 1) * kSlotSteps;  // steps of the last slot
+// Where a workgroup's loads are: the next slot to issue, in its tiles.  An
+// address is a scalar base and a lane's 32-bit offset from it, which changes
+// with the tile alone (strides: kMaxFp4Stride and kMaxHiddenStride).
+template <int ROWS, bool ALIGNED>
+struct Fp4Loader {
+  static constexpr int NH = ROWS / 16;  // hidden loads a wave and slot (1 KiB each: two rows)
+  // A wave's direct loads of a slot, and those of a slot that begins a panel.
+  static constexpr int kOdd = 4 + NH, kEven = kOdd + (ALIGNED ? 2 : 0);
+  int64_t ld_h, n, ld_d, ld_s, v;
+  int ksteps, nslots, last;  // last: steps of a tile's last slot
+  int mblocks, tile, step, end;
+  int p, ring, panel;  // the next slot: of its tile, its place, its panel's
+  int64_t w0, h0, s0;  // where the tile's rows begin
+  uint32_t wofs[4], hofs[NH], sofs[2];
 
-  // Rows past the data read the last one, pieces past K the last one of the
-  // row: every load stays in bounds, and what it brings is masked or not read.
-  const uint8_t* wp[4];
-  int wc[4];
+  // Rows past the data read the last one: every load stays in bounds, and what
+  // it brings is masked or not read.
+  __device__ __forceinline__ void rows(int tid, int wave, int lane) {
+    const int64_t m0 = static_cast<int64_t>(tile % mblocks) * ROWS;
+    const int64_t v0 = static_cast<int64_t>(tile / mblocks) * BN;
+    const int vmax = static_cast<int>(min(v - 1 - v0, int64_t{BN - 1}));
+    const int hmax = static_cast<int>(min(n - 1 - m0, int64_t{ROWS - 1}));
+    w0 = v0 * ld_d;
+    h0 = m0 * ld_h;
+    s0 = v0 * ld_s;
+    const uint32_t lw = static_cast<uint32_t>(ld_d), lh = static_cast<uint32_t>(ld_h) * 2;
+    const uint32_t ls = static_cast<uint32_t>(ld_s);
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int r = (wave + 8 * u) * 8 + lane / 8;
-    wp[u] = data + min(v0 + r, v - 1) * ld_d;
-    wc[u] = (lane % 8) ^ weight_swz(r);
+    for (int u = 0; u < 4; ++u) {
+      const int r = (wave + 8 * u) * 8 + lane / 8;
+      wofs[u] = min(r, vmax) * lw + ((lane % 8) ^ weight_swz(r)) * 16;
+    }
+#pragma unroll
+    for (int u = 0; u < NH; ++u) {
+      const int r = (wave + 8 * u) * 2 + lane / 32;
+      hofs[u] = min(r, hmax) * lh + ((lane % 32) ^ hidden_swz(r)) * 16;
+    }
+    if constexpr (ALIGNED) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        sofs[u] = min((wave + 8 * u) * 16 + lane / 4, vmax) * ls + 4 * (lane % 4);
+    } else {
+      sofs[0] = min(tid / 2, vmax) * ls;
+    }
   }
-  const uint16_t* hp[NH];
-  int hc[NH];
-#pragma unroll
-  for (int u = 0; u < NH; ++u) {
-    const int r = (wave + 8 * u) * 2 + lane / 32;
-    hp[u] = hidden + min(m0 + r, n - 1) * ld_h;
-    hc[u] = (lane % 32) ^ hidden_swz(r);
-  }
-  // Scales: thread t takes four of column t / 2, two at a time (K is a multiple
-  // of 64), past the end the last two.
-  const uint8_t* sp = scales + min(v0 + tid / 2, v - 1) * ld_s;
-  auto load_scales = [&](int p, uint16_t (&x)[2]) {
-    const int at = p * kSlotSteps + 4 * (tid % 2);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      x[i] = reinterpret_cast<const ScalePair*>(sp + min(at + 2 * i, ksteps - 2))->w;
-  };
-  auto issue = [&](int slot, int q, uint16_t (&sc)[2]) {
-    const int p = q < nslots ? q : nslots - 1;
-    const int most = p == nslots - 1 ? last : kSlotSteps;
-    load_scales(p, sc);
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      __builtin_amdgcn_global_load_lds(
-          wp[u] + static_cast<int64_t>(p) * kSlotBytes + min(wc[u], most - 1) * 16,
-          sm.w[slot] + (wave + 8 * u) * 1024, 16, 0, 0);
-#pragma unroll
-    for (int u = 0; u < NH; ++u)
-      __builtin_amdgcn_global_load_lds(
-          hp[u] + static_cast<int64_t>(p) * kSlotK + min(hc[u], 4 * most - 1) * 8,
-          sm.h[slot] + (wave + 8 * u) * 512, 16, 0, 0);
-  };
 
+  // Issues the next slot's loads; past the last tile the last slot's again, so
+  // that every slot has its loads in flight behind it.  Pieces past K are the
+  // row's last.  sc: scale bytes that pass through registers, four of column
+  // tid / 2, two and two.
+  __device__ __forceinline__ void issue(SmemFp4<ROWS>& sm, const uint16_t* hidden,
+                                        const uint8_t* data, const uint8_t* scales, int tid,
+                                        int wave, int lane, uint16_t (&sc)[2]) {
+    if (p % 2 == 0) panel = panel == kPanels - 1 ? 0 : panel + 1;
+    const uint8_t* sb = scales + s0 + p * kSlotSteps;
+    if constexpr (ALIGNED) {
+      if (p % 2 == 0) {
+        const int past = max(p * kSlotSteps + 4 * (lane % 4) - (ksteps - 4), 0);
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          __builtin_amdgcn_global_load_lds(sb + (sofs[u] - past),
+                                           sm.scale[panel] + (wave + 8 * u) * 256, 4, 0, 0);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        sc[i] = reinterpret_cast<const ScalePair*>(
+                    scales + (s0 + sofs[0] +
+                              min(p * kSlotSteps + 4 * (tid % 2) + 2 * i, ksteps - 2)))
+                    ->w;
+    }
+    Fp4Slot<ROWS>& to = sm.slot[ring];
+    const uint8_t* wb = data + w0 + static_cast<int64_t>(p) * kSlotBytes;
+    const uint8_t* hb =
+        reinterpret_cast<const uint8_t*>(hidden + h0 + static_cast<int64_t>(p) * kSlotK);
+    const bool whole = p < nslots - 1 || last == kSlotSteps;
+    if (whole) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        __builtin_amdgcn_global_load_lds(wb + wofs[u], to.w + (wave + 8 * u) * 1024, 16, 0, 0);
+#pragma unroll
+      for (int u = 0; u < NH; ++u)
+        __builtin_amdgcn_global_load_lds(hb + hofs[u], to.h + (wave + 8 * u) * 512, 16, 0, 0);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int c = (lane % 8) ^ weight_swz((wave + 8 * u) * 8 + lane / 8);
+        __builtin_amdgcn_global_load_lds(wb + (wofs[u] - max(c - last + 1, 0) * 16),
+                                         to.w + (wave + 8 * u) * 1024, 16, 0, 0);
+      }
+#pragma unroll
+      for (int u = 0; u < NH; ++u) {
+        const int c = (lane % 32) ^ hidden_swz((wave + 8 * u) * 2 + lane / 32);
+        __builtin_amdgcn_global_load_lds(hb + (hofs[u] - max(c - 4 * last + 1, 0) * 16),
+                                         to.h + (wave + 8 * u) * 512, 16, 0, 0);
+      }
+    }
+    ring = ring == kSlots<ROWS> - 1 ? 0 : ring + 1;
+    if (p < nslots - 1) {
+      ++p;
+    } else if (tile + step < end) {
+      tile += step;
+      p = 0;
+      rows(tid, wave, lane);
+    }
+  }
+};
+
+// The first `count` of a slot's eight steps: acc += hidden rows x the wave's 32
+// columns.  Steps are read from LDS NR at a time, one such part ahead of the
+// decoding and the products.
+template <int ROWS, bool WHOLE>
+__device__ __forceinline__ void slot_steps(const Fp4Slot<ROWS>& slot, const uint8_t* scale,
+                                           int count, int wave, int li, int g,
+                                           f32x4 (&acc)[ROWS / 16][2]) {
+  constexpr int MI = ROWS / 16, NR = MI == 4 ? 1 : 2, NP = kSlotSteps / NR;
+  const int col = wave * 32 + li;
   const int sw = weight_swz(li);  // the same for rows 16 apart
-  auto steps = [&](int slot, int count) {
-    uint2 sc[4];
+  uint2 sc[2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      sc[j] = *reinterpret_cast<const uint2*>(&sm.scale[slot][(wn * 64 + 16 * j + li) * 4]);
+  for (int j = 0; j < 2; ++j)
+    sc[j] = *reinterpret_cast<const uint2*>(scale + (col + 16 * j) * 2 * kSlotSteps);
+  uint32_t q[2][NR][2];
+  bf16x8 a[2][NR][MI];
+  auto read = [&](int part) {
 #pragma unroll
-    for (int s = 0; s < kSlotSteps; ++s) {
-      if (s % 2 == 0 && s >= count) break;  // uniform; K is a multiple of 64
-      bf16x8 a[MI], b[4];
+    for (int r = 0; r < NR; ++r) {
+      const int s = part * NR + r;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        q[part % 2][r][j] = *reinterpret_cast<const uint32_t*>(
+            slot.w + (col + 16 * j) * kSlotBytes + (s ^ sw) * 16 + g * 4);
 #pragma unroll
       for (int i = 0; i < MI; ++i)
-        a[i] = *reinterpret_cast<const bf16x8*>(
-            sm.h[slot] + (wm * (ROWS / 2) + 16 * i + li) * kSlotK + ((4 * s + g) ^ li) * 8);
+        a[part % 2][r][i] = *reinterpret_cast<const bf16x8*>(
+            slot.h + (16 * i + li) * kSlotK + ((4 * s + g) ^ li) * 8);
+    }
+  };
+  read(0);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t q = *reinterpret_cast<const uint32_t*>(
-            sm.w[slot] + (wn * 64 + 16 * j + li) * kSlotBytes + (s ^ sw) * 16 + g * 4);
-        const uint32_t e = s < 4 ? sc[j].x >> (8 * s) : sc[j].y >> (8 * (s - 4));
-        b[j] = decode8(q, __uint_as_float((e & 255u) << 23));
+  for (int part = 0; part < NP; ++part) {
+    if (part + 1 < NP) read(part + 1);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const int s = part * NR + r;
+      if (!WHOLE && s % 2 == 0 && s >= count) return;  // uniform; K is a multiple of 64
+      bf16x8 b[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        // the scale byte to the exponent's place: the conversion takes no other bit
+        const uint32_t x = s < 4 ? sc[j].x : sc[j].y;
+        const uint32_t e = s % 4 == 3 ? x >> 1 : x << (23 - 8 * (s % 4));
+        b[j] = decode8(q[part % 2][r][j], __uint_as_float(e));
       }
 #pragma unroll
       for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], b[j], acc[i][j], 0, 0, 0);
+        for (int j = 0; j < 2; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[part % 2][r][i], b[j], acc[i][j],
+                                                              0, 0, 0);
     }
-  };
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
 
-  uint16_t sc[S - 1][2];
+// From 32 columns x ROWS rows a wave to the epilogue's 64 x EPI / 2 through z, a
+// slot's place; columns are turned by 16 every 4 rows, which puts a wave's
+// stores on different banks.
+template <int ROWS, int MI>
+__device__ __forceinline__ void regroup(const f32x4 (&part)[ROWS / 16][2], float* z, int wave,
+                                        int row0, int col0, int li, int g, f32x4 (&acc)[MI][4]) {
+  static_assert(ROWS * BN * 4 <= sizeof(Fp4Slot<ROWS>), "z in a slot");
+  auto at = [&](int row, int col) { return row * BN + (col ^ ((row >> 2 & 3) << 4)); };
+  block_sync_lds();
 #pragma unroll
-  for (int p = 0; p < S - 1; ++p) issue(p, p, sc[p]);
-  // Slot p's loads have landed once only those of the S - 2 slots issued after
-  // it are in flight; after the barrier that holds for every wave, the scales
-  // are in LDS, and nobody reads slot p - 1 any more, whose place the loads for
-  // slot p + S - 1 take.
-  for (int p0 = 0; p0 < nslots; p0 += S - 1) {
+  for (int i = 0; i < ROWS / 16; ++i)
 #pragma unroll
-    for (int u = 0; u < S - 1; ++u) {
-      const int p = p0 + u;  // past the end: nothing is added
-      wait_vm_lgkm0<(S - 2) * kLoads>();
-      sm.scale[p % S][2 * tid] = sc[u][0];
-      sm.scale[p % S][2 * tid + 1] = sc[u][1];
-      wait_vm_lgkm0<(S - 2) * kLoads>();
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        z[at(16 * i + 4 * g + q, wave * 32 + 16 * j + li)] = part[i][j][q];
+  block_sync_lds();
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        acc[i][j][q] = row0 + 16 * i < ROWS  // the others are past n
+                           ? z[at(row0 + 16 * i + 4 * g + q, col0 + 16 * j + li)]
+                           : 0.0f;
+  block_sync_lds();
+}
+
+// A workgroup's tiles.  (A function of its own for its __restrict__ operands:
+// inlined, they tell the compiler that the direct loads read nothing that LDS
+// holds; otherwise it waits for all of them before every read of LDS.)
+template <int ROWS, bool ALIGNED>
+__device__ __forceinline__ void fp4_tiles(
+    SmemFp4<ROWS>& sm, const uint16_t* __restrict__ hidden, int64_t ld_h,
+    const uint8_t* __restrict__ data, int64_t ld_d, const uint8_t* __restrict__ scales,
+    int64_t ld_s, int64_t n, int64_t v, int ksteps, int mblocks, int vblocks, Targets targets,
+    int64_t ignore, float* __restrict__ pm, float* __restrict__ ps, float* __restrict__ pt,
+    float inv_t, int32_t round_bf16, float* pw, void* z, int32_t z_bf16, int64_t ld_z,
+    int32_t z_vec) {
+  const LinearExtras ex{inv_t, round_bf16, pw, z, z_bf16, ld_z, z_vec};
+  constexpr int S = kSlots<ROWS>, EPI = kEpiRows<ROWS>, MI = EPI / 32;
+  using Loader = Fp4Loader<ROWS, ALIGNED>;
+  const int tid = threadIdx.x, lane = tid % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int li = lane % 16, g = lane / 16;
+  // Workgroup b takes tiles of XCD b % 8's range.
+  int first, end;
+  gemm::xcd_range(mblocks * vblocks, blockIdx.x % 8, first, end);
+  const int step = gridDim.x / 8;
+  const int begin = first + blockIdx.x / 8;
+  if (begin >= end) return;
+  if (tid < n) sm.target[tid] = targets[tid];
+
+  Loader load;
+  load.ld_h = ld_h;
+  load.n = n;
+  load.ld_d = ld_d;
+  load.ld_s = ld_s;
+  load.v = v;
+  load.ksteps = ksteps;
+  load.nslots = (ksteps + kSlotSteps - 1) / kSlotSteps;
+  load.last = ksteps - (load.nslots - 1) * kSlotSteps;
+  load.mblocks = mblocks;
+  load.tile = begin;
+  load.step = step;
+  load.end = end;
+  load.p = load.ring = 0;
+  load.panel = kPanels - 1;
+  load.rows(tid, wave, lane);
+  // Scales that pass through registers go to their panel once their loads are
+  // back, in the iteration that issued them.
+  auto issue = [&](auto between) {
+    uint16_t sc[2];
+    const int p = load.p;
+    load.issue(sm, hidden, data, scales, tid, wave, lane, sc);
+    uint8_t* to = sm.scale[load.panel] + (tid / 2) * 2 * kSlotSteps + (p % 2) * kSlotSteps +
+                  4 * (tid % 2);
+    between();
+    if constexpr (!ALIGNED)
+      *reinterpret_cast<uint32_t*>(to) = sc[0] | static_cast<uint32_t>(sc[1]) << 16;
+  };
+  for (int i = 0; i < S - 1; ++i) issue([] {});
+
+  int ring = 0, panel = kPanels - 1;
+  for (int tile = begin; tile < end; tile += step) {
+    const int64_t m0 = static_cast<int64_t>(tile % mblocks) * ROWS;
+    const int64_t v0 = static_cast<int64_t>(tile / mblocks) * BN;
+    f32x4 part[ROWS / 16][2];
+#pragma unroll
+    for (int i = 0; i < ROWS / 16; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) part[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int p = 0; p < load.nslots; ++p) {
+      // This slot's loads have landed once only those of the S - 2 slots issued
+      // after it are in flight; after the barrier that holds for every wave, and
+      // nobody reads the slot before it any more, whose place the next loads
+      // take.  (Past the tile's end the next slot may be the last one again: no
+      // more than kOdd can be counted on.)
+      if constexpr (S == 2) {
+        wait_vm_lgkm0<0>();
+      } else {
+        if (p % 2 == 1 && p + 1 < load.nslots) wait_vm_lgkm0<Loader::kEven>();
+        else wait_vm_lgkm0<Loader::kOdd>();
+      }
       __builtin_amdgcn_s_barrier();
-      issue((p + S - 1) % S, p + S - 1, sc[u]);
-      steps(p % S, p < nslots - 1 ? kSlotSteps : p == nslots - 1 ? last : 0);
+      asm volatile("" ::: "memory");
+      if (p % 2 == 0) panel = panel == kPanels - 1 ? 0 : panel + 1;
+      const Fp4Slot<ROWS>& slot = sm.slot[ring];
+      const uint8_t* scale = sm.scale[panel] + (p % 2) * kSlotSteps;
+      issue([&] {
+        if (p < load.nslots - 1 || load.last == kSlotSteps) {
+          slot_steps<ROWS, true>(slot, scale, kSlotSteps, wave, li, g, part);
+        } else {
+          slot_steps<ROWS, false>(slot, scale, load.last, wave, li, g, part);
+        }
+      });
+      if (p < load.nslots - 1) ring = ring == S - 1 ? 0 : ring + 1;
     }
+    // The last slot's place is free until the next tile's first slot is waited
+    // for: the epilogue's.
+    if (tid < EPI) {
+      int code = -2;
+      const int64_t r = m0 + tid;
+      if (r < n) {
+        const int64_t t = sm.target[r];
+        if (t != ignore) code = t >= v0 && t < v0 + BN && t < v ? static_cast<int>(t - v0) : -1;
+      }
+      sm.rd.code[tid] = code;
+    }
+    const int row0 = (wave / 4) * (EPI / 2), col0 = (wave % 4) * 64;
+    f32x4 acc[MI][4];
+    regroup<ROWS, MI>(part, reinterpret_cast<float*>(&sm.slot[ring]), wave, row0, col0, li, g, acc);
+    stats_epilogue<MI, 4, EPI, kThreads4, sizeof(Fp4Slot<ROWS>)>(
+        acc, sm.rd, &sm.slot[ring], row0, col0, li, g, tid, m0, v0, tile / mblocks, vblocks, n, v,
+        pm, ps, pt, ex);
+    ring = ring == S - 1 ? 0 : ring + 1;
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
-template <int ROWS>
+template <int ROWS, bool ALIGNED>
 __global__ __launch_bounds__(kThreads4) void linear_fp4_narrow(
     const uint16_t* __restrict__ hidden, int64_t ld_h, const uint8_t* __restrict__ data,
     int64_t ld_d, const uint8_t* __restrict__ scales, int64_t ld_s, int64_t n, int64_t v,
     int ksteps, int mblocks, int vblocks, const void* __restrict__ tgt, int32_t tgt32,
     int64_t ignore, float* __restrict__ pm, float* __restrict__ ps, float* __restrict__ pt,
     LinearExtras ex) {
-  constexpr int MI = ROWS / 32;
-  const Targets targets{tgt, tgt32};
   __shared__ __align__(16) SmemFp4<ROWS> sm;
-  const int tid = threadIdx.x, lane = tid % kWave;
-  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int logical = gemm::xcd_logical(blockIdx.x, mblocks * vblocks);
-  const int mb = logical % mblocks, vb = logical / mblocks;
-  const int64_t m0 = static_cast<int64_t>(mb) * ROWS, v0 = static_cast<int64_t>(vb) * BN;
-  if (tid < ROWS) sm.rd.code[tid] = row_code(m0 + tid, n, targets, ignore, v0, v);
-  f32x4 acc[MI][4];
-#pragma unroll
-  for (int i = 0; i < MI; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  mainloop_fp4<ROWS>(sm.st, hidden, ld_h, m0, n, data, ld_d, scales, ld_s, v0, v, ksteps, acc);
-  __syncthreads();
-  stats_epilogue<MI, 4, ROWS, kThreads4, sizeof(sm.st)>(
-      acc, sm.rd, &sm.st, (wave / 4) * (ROWS / 2), (wave % 4) * 64, lane % 16, lane / 16, tid, m0,
-      v0, vb, vblocks, n, v, pm, ps, pt, ex);
+  fp4_tiles<ROWS, ALIGNED>(sm, hidden, ld_h, data, ld_d, scales, ld_s, n, v, ksteps, mblocks,
+                           vblocks, Targets{tgt, tgt32}, ignore, pm, ps, pt, ex.inv_t, ex.round_bf16, ex.pw,
+                           ex.z, ex.z_bf16, ex.ld_z, ex.z_vec);
 }
 
-// The decoded copy: a wave takes 16 rows x 4 K steps, a lane one row's step (16
-// bytes of codes, 64 bytes of values: whole blocks of 1 KiB).
+// The decoded copy: a wave takes 16 rows x 8 K steps (a line of codes a row), a
+// lane a quarter of a row's step at a time, so that a wave's store is a whole
+// block of 1 KiB.
 __global__ __launch_bounds__(256) void fp4_decode_kernel(const uint8_t* __restrict__ data,
                                                          int64_t ld_d,
                                                          const uint8_t* __restrict__ scales,
-                                                         int64_t ld_s, int64_t v, int64_t ksteps,
+                                                         int64_t ld_s, int64_t v, int ksteps,
                                                          uint16_t* __restrict__ out) {
   const int lane = threadIdx.x % kWave;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 16 + lane % 16;
-  for (int64_t k = (static_cast<int64_t>(blockIdx.y) * 4 + threadIdx.x / kWave) * 4 + lane / 16;
-       k < ksteps; k += static_cast<int64_t>(gridDim.y) * 16) {
-    uint4 q = make_uint4(0, 0, 0, 0);
-    float scale = 1.0f;
-    if (row < v) {
-      q = *reinterpret_cast<const uint4*>(data + row * ld_d + k * 16);
-      scale = __uint_as_float(static_cast<uint32_t>(scales[row * ld_s + k]) << 23);
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * 16 + lane / 4;
+  const bool live = row < v;
+  const uint8_t* codes = data + (live ? row : 0) * ld_d + (lane % 4) * 4;
+  const uint8_t* sc = scales + (live ? row : 0) * ld_s;
+  uint16_t* to = out + static_cast<int64_t>(blockIdx.x) * ksteps * 512 + lane * 8;
+  for (int k0 = (static_cast<int>(blockIdx.y) * 4 + static_cast<int>(threadIdx.x) / kWave) * 8;
+       k0 < ksteps; k0 += static_cast<int>(gridDim.y) * 32) {
+    uint32_t q[8], e[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const int k = min(k0 + s, ksteps - 1);
+      q[s] = *reinterpret_cast<const uint32_t*>(codes + static_cast<int64_t>(k) * 16);
+      e[s] = sc[k];
     }
-    bf16x8* to = reinterpret_cast<bf16x8*>(
-        out + (static_cast<int64_t>(blockIdx.x) * ksteps + k) * 512 + (lane % 16) * 32);
-    to[0] = decode8(q.x, scale);
-    to[1] = decode8(q.y, scale);
-    to[2] = decode8(q.z, scale);
-    to[3] = decode8(q.w, scale);
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+      const float scale = __uint_as_float((live ? e[s] : 127u) << 23);
+      const bf16x8 x = decode8(live ? q[s] : 0u, scale);
+      if (k0 + s < ksteps)
+        *reinterpret_cast<bf16x8*>(to + static_cast<int64_t>(k0 + s) * 512) = x;
+    }
   }
 }
 
@@ -244,10 +441,10 @@ __global__ __launch_bounds__(256) void fp4_decode_kernel(const uint8_t* __restri
 int64_t fp4_decoded_bytes(int64_t v, int64_t h) { return (v + 255) / 256 * 256 * h * 2; }
 
 void launch_fp4_decode(const Fp4Weight& w, int64_t v, int64_t h, uint16_t* out, hipStream_t s) {
-  const int64_t ksteps = h / BK, blocks = (v + 255) / 256 * 16, ky = (ksteps + 15) / 16;
+  const int64_t ksteps = h / BK, blocks = (v + 255) / 256 * 16, ky = (ksteps + 31) / 32;
   hipLaunchKernelGGL(fp4_decode_kernel,
                      dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(ky < 64 ? ky : 64)),
-                     dim3(256), 0, s, w.data, w.ld_d, w.scales, w.ld_s, v, ksteps, out);
+                     dim3(256), 0, s, w.data, w.ld_d, w.scales, w.ld_s, v, static_cast<int>(ksteps), out);
 }
 
 void launch_fp4_partials(const uint16_t* hidden, int64_t ld_h, const Fp4Weight& w, int64_t n,
@@ -255,13 +452,20 @@ void launch_fp4_partials(const uint16_t* hidden, int64_t ld_h, const Fp4Weight& 
                          float* ps, float* pt, float inv_t, int32_t round_bf16, float* pw, void* z,
                          int32_t z_bf16, int64_t ld_z, hipStream_t s) {
   const int vblocks = static_cast<int>((v + BN - 1) / BN);
-  const int rows = n <= 32 ? 32 : 64;
+  const int rows = n <= 16 ? 16 : n <= 32 ? 32 : 64;
   const int mblocks = static_cast<int>((n + rows - 1) / rows);
   const int32_t z_vec = z && reinterpret_cast<uintptr_t>(z) % 16 == 0 &&
                         (ld_z * (z_bf16 ? 2 : 4)) % 16 == 0;
   const LinearExtras ex{inv_t, round_bf16, pw, z, z_bf16, ld_z, z_vec};
-  auto kern = rows == 32 ? linear_fp4_narrow<32> : linear_fp4_narrow<64>;
-  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(mblocks * vblocks)), dim3(kThreads4), 0, s,
+  // a workgroup a CU, as many on every XCD
+  const int per = (mblocks * vblocks + 7) / 8, cus = xcd_cus();
+  const int grid = 8 * (per < cus ? per : cus);
+  const bool aligned = h % 128 == 0 && w.ld_s % 4 == 0 &&
+                       reinterpret_cast<uintptr_t>(w.scales) % 4 == 0;
+  auto kern = rows == 16   ? (aligned ? linear_fp4_narrow<16, true> : linear_fp4_narrow<16, false>)
+              : rows == 32 ? (aligned ? linear_fp4_narrow<32, true> : linear_fp4_narrow<32, false>)
+                           : (aligned ? linear_fp4_narrow<64, true> : linear_fp4_narrow<64, false>);
+  hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads4), 0, s,
                      hidden, ld_h, w.data, w.ld_d, w.scales, w.ld_s, n, v,
                      static_cast<int>(h / BK), mblocks, vblocks, targets.p, targets.is32, ignore,
                      pm, ps, pt, ex);

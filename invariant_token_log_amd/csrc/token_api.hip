@@ -401,7 +401,9 @@ int32_t linear_token_logp_fp4_fwd(const void* hidden, int64_t ld_h, const void* 
                                   void* hip_stream) {
   int32_t st = check_head_sizes(n, h, v, m, top_k, row_chunk);
   if (st != LOGP_OK) return st;
-  if (ld_h < h || ld_d < h / 2 || ld_s < h / itl::kFp4Group) return LOGP_ERR_SHAPE;
+  if (ld_h < h || ld_d < h / 2 || ld_s < h / itl::kFp4Group || ld_h > itl::kMaxHiddenStride ||
+      ld_d > itl::kMaxFp4Stride || ld_s > itl::kMaxFp4Stride)
+    return LOGP_ERR_SHAPE;
   if (!itl::usable_temperature(temperature) ||
       (logits_rounding != LOGP_ROUND_NONE && logits_rounding != LOGP_ROUND_BF16))
     return LOGP_ERR_VALUE;

@@ -176,7 +176,9 @@ def test_head(L):
     expect(L.linear_token_logp_fp4_fwd, base, [
         (_lib.LOGP_ERR_SHAPE, dict(n=-1)), (_lib.LOGP_ERR_SHAPE, dict(h=96)), (_lib.LOGP_ERR_SHAPE, dict(v=0)),
         (_lib.LOGP_ERR_SHAPE, dict(m=257)), (_lib.LOGP_ERR_SHAPE, dict(ld_h=127)), (_lib.LOGP_ERR_SHAPE, dict(ld_d=63)),
-        (_lib.LOGP_ERR_SHAPE, dict(ld_s=3)), (_lib.LOGP_ERR_SHAPE, dict(rows=-1)), (_lib.LOGP_ERR_VALUE, dict(k=65)),
+        (_lib.LOGP_ERR_SHAPE, dict(ld_s=3)), (_lib.LOGP_ERR_SHAPE, dict(rows=-1)),
+        (_lib.LOGP_ERR_SHAPE, dict(ld_h=(1 << 25) + 8)), (_lib.LOGP_ERR_SHAPE, dict(ld_d=(1 << 23) + 16)),
+        (_lib.LOGP_ERR_SHAPE, dict(ld_s=(1 << 23) + 1)), (_lib.LOGP_ERR_VALUE, dict(k=65)),
         (_lib.LOGP_ERR_VALUE, dict(temp=0.0)), (_lib.LOGP_ERR_VALUE, dict(rnd=2)), (_lib.LOGP_ERR_DTYPE, dict(tdt=3)),
         (_lib.LOGP_ERR_NULL, dict(h_ptr=None)), (_lib.LOGP_ERR_NULL, dict(d=None)), (_lib.LOGP_ERR_NULL, dict(s=None)),
         (_lib.LOGP_ERR_NULL, dict(tokens=None)), (_lib.LOGP_ERR_NULL, dict(logp=None)), (_lib.LOGP_ERR_NULL, dict(ids=None)),
