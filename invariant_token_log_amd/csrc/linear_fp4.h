@@ -22,9 +22,11 @@ struct Fp4Weight {
 constexpr int64_t kMaxFp4Stride = int64_t{1} << 23;
 constexpr int64_t kMaxHiddenStride = int64_t{1} << 25;
 
-// Up to this many rows the products read the 4-bit rows themselves; more rows
-// take the bf16 kernels on a decoded copy.
-constexpr int64_t kFp4Direct = 256;
+// Up to this many rows the products read the 4-bit rows themselves, 97 us for
+// every 64 at V = 151936, H = 4096; more rows take the bf16 kernels on a decoded
+// copy, 256 us and 450 for every 512 (448 rows: 680 us against 716, 512 rows: 776
+// against 744).
+constexpr int64_t kFp4Direct = 448;
 
 // The decoded copy, K32-blocked with round_up(v, 256) rows (those past v
 // zeros), as launch_linear_partials takes it (wblk): exact.

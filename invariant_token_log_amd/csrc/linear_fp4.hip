@@ -403,36 +403,67 @@ __global__ __launch_bounds__(kThreads4) void linear_fp4_narrow(
                            ex.z, ex.z_bf16, ex.ld_z, ex.z_vec);
 }
 
-// The decoded copy: a wave takes 16 rows x 8 K steps (a line of codes a row), a
-// lane a quarter of a row's step at a time, so that a wave's store is a whole
-// block of 1 KiB.
+// Lane t of a quad gives a[i] to lane i and takes that lane's a[t] for it.
+__device__ __forceinline__ void quad_transpose(uint32_t (&a)[4], int t) {
+  auto swap = [&](uint32_t& x, uint32_t& y, bool high, auto partner) {
+    const uint32_t got = partner(high ? x : y);
+    x = high ? got : x;
+    y = high ? y : got;
+  };
+  auto by1 = [](uint32_t x) { return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), kDppXor1, 0xF, 0xF, true)); };
+  auto by2 = [](uint32_t x) { return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), kDppXor2, 0xF, 0xF, true)); };
+  swap(a[0], a[1], t & 1, by1);
+  swap(a[2], a[3], t & 1, by1);
+  swap(a[0], a[2], t & 2, by2);
+  swap(a[1], a[3], t & 2, by2);
+}
+
+// The decoded copy: a wave takes 16 rows x 8 K steps (a line of codes a row),
+// reads pieces of a step and turns them in quads of lanes, so that a lane holds
+// its quarter of a row's every step and a wave's store is a whole block of 1 KiB.
+// K parts of a row block are neighbours in the grid.
+struct __attribute__((packed)) Scale8 {
+  uint32_t w[2];
+};
+
 __global__ __launch_bounds__(256) void fp4_decode_kernel(const uint8_t* __restrict__ data,
                                                          int64_t ld_d,
                                                          const uint8_t* __restrict__ scales,
                                                          int64_t ld_s, int64_t v, int ksteps,
+                                                         int parts, int64_t first,
                                                          uint16_t* __restrict__ out) {
-  const int lane = threadIdx.x % kWave;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * 16 + lane / 4;
+  const int lane = threadIdx.x % kWave, t = lane % 4;
+  const int64_t block = first + blockIdx.x / parts;
+  const int k0 = (static_cast<int>(blockIdx.x % parts) * 4 + static_cast<int>(threadIdx.x) / kWave) * 8;
+  if (k0 >= ksteps) return;
+  const int64_t row = block * 16 + lane / 4;
   const bool live = row < v;
-  const uint8_t* codes = data + (live ? row : 0) * ld_d + (lane % 4) * 4;
-  const uint8_t* sc = scales + (live ? row : 0) * ld_s;
-  uint16_t* to = out + static_cast<int64_t>(blockIdx.x) * ksteps * 512 + lane * 8;
-  for (int k0 = (static_cast<int>(blockIdx.y) * 4 + static_cast<int>(threadIdx.x) / kWave) * 8;
-       k0 < ksteps; k0 += static_cast<int>(gridDim.y) * 32) {
-    uint32_t q[8], e[8];
+  const uint8_t* codes = data + (live ? row : 0) * ld_d;
+  const uint8_t* sc = scales + (live ? row : 0) * ld_s + k0;
+  uint32_t q[2][4], e[2] = {0, 0};
 #pragma unroll
-    for (int s = 0; s < 8; ++s) {
-      const int k = min(k0 + s, ksteps - 1);
-      q[s] = *reinterpret_cast<const uint32_t*>(codes + static_cast<int64_t>(k) * 16);
-      e[s] = sc[k];
-    }
+  for (int i = 0; i < 2; ++i) {
+    const uint4 x = *reinterpret_cast<const uint4*>(
+        codes + static_cast<int64_t>(min(k0 + 4 * i + t, ksteps - 1)) * 16);
+    q[i][0] = x.x; q[i][1] = x.y; q[i][2] = x.z; q[i][3] = x.w;
+  }
+  if (k0 + 8 <= ksteps) {
+    const Scale8 x = *reinterpret_cast<const Scale8*>(sc);
+    e[0] = x.w[0];
+    e[1] = x.w[1];
+  } else {
+    for (int s = 0; k0 + s < ksteps; ++s)
+      e[s / 4] |= static_cast<uint32_t>(sc[s]) << (8 * (s % 4));
+  }
+  quad_transpose(q[0], t);
+  quad_transpose(q[1], t);
+  uint16_t* to = out + (block * ksteps + k0) * 512 + lane * 8;
 #pragma unroll
-    for (int s = 0; s < 8; ++s) {
-      const float scale = __uint_as_float((live ? e[s] : 127u) << 23);
-      const bf16x8 x = decode8(live ? q[s] : 0u, scale);
-      if (k0 + s < ksteps)
-        *reinterpret_cast<bf16x8*>(to + static_cast<int64_t>(k0 + s) * 512) = x;
-    }
+  for (int s = 0; s < 8; ++s) {
+    const uint32_t b = e[s / 4];
+    const uint32_t scale = s % 4 == 3 ? b >> 1 : b << (23 - 8 * (s % 4));
+    const bf16x8 x = decode8(live ? q[s / 4][s % 4] : 0u, __uint_as_float(live ? scale : 0u));
+    if (k0 + s < ksteps) *reinterpret_cast<bf16x8*>(to + s * 512) = x;
   }
 }
 
@@ -441,10 +472,15 @@ __global__ __launch_bounds__(256) void fp4_decode_kernel(const uint8_t* __restri
 int64_t fp4_decoded_bytes(int64_t v, int64_t h) { return (v + 255) / 256 * 256 * h * 2; }
 
 void launch_fp4_decode(const Fp4Weight& w, int64_t v, int64_t h, uint16_t* out, hipStream_t s) {
-  const int64_t ksteps = h / BK, blocks = (v + 255) / 256 * 16, ky = (ksteps + 31) / 32;
-  hipLaunchKernelGGL(fp4_decode_kernel,
-                     dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(ky < 64 ? ky : 64)),
-                     dim3(256), 0, s, w.data, w.ld_d, w.scales, w.ld_s, v, static_cast<int>(ksteps), out);
+  const int ksteps = static_cast<int>(h / BK), parts = (ksteps + 31) / 32;
+  const int64_t blocks = (v + 255) / 256 * 16;
+  // a grid holds fewer than 2^32 threads
+  const int64_t most = (int64_t{1} << 23) / parts > 0 ? (int64_t{1} << 23) / parts : 1;
+  for (int64_t b = 0; b < blocks; b += most) {
+    const int64_t m = blocks - b < most ? blocks - b : most;
+    hipLaunchKernelGGL(fp4_decode_kernel, dim3(static_cast<unsigned>(m * parts)), dim3(256), 0, s,
+                       w.data, w.ld_d, w.scales, w.ld_s, v, ksteps, parts, b, out);
+  }
 }
 
 void launch_fp4_partials(const uint16_t* hidden, int64_t ld_h, const Fp4Weight& w, int64_t n,

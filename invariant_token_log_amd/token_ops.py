@@ -286,7 +286,7 @@ def linear_token_logp_fwd(hidden, weight, token_ids=None, top_k=0, ignore_index=
     head of frozen weights (no round_logits, prepared_weight or logits_out).
     weight may be Fp4Rows: the 4-bit head of frozen weights, with the bits of the
     bfloat16 weight they stand for (no prepared_weight or logits_out; more than
-    256 rows take a bfloat16 copy of the weight in the workspace).
+    448 rows take a bfloat16 copy of the weight in the workspace).
     round_logits and prepared_weight: as linear_logp_fwd.  logits_out [N, V]
     float32 (or bfloat16 with round_logits) receives the unscaled logits for
     linear_token_logp_bwd.  row_chunk: rows taken at a time, which bounds the
