@@ -9,7 +9,7 @@
 //
 // The gradient sorts the tokens with their positions, so that the occurrences of
 // a token form a run in ascending position, and sums every run in fp32:
-//   1. embed_sort_kernel: tiles of 4096 tokens, a workgroup each, a bitonic
+//   1. embed_sort_kernel: tiles of 2048 tokens, a workgroup each, a bitonic
 //      network in registers, lane moves and LDS (no order-dependent atomics, so
 //      the same bits every time).  More than one tile: embed_rank_kernel places
 //      every token by binary searches in the other tiles.
@@ -20,8 +20,10 @@
 //      chains of every eighth piece, then the chains in order.
 // A row of the gradient depends on its token's own occurrences and their
 // order, not on the batch around them.
-// Without accumulation the rows of absent tokens are written with zeros by
-// embed_zero_kernel; with a large vocabulary that is what takes the time.
+// Without accumulation the rows of absent tokens are written with zeros, which
+// with a large vocabulary is most of the work: beside the sort and the ranking
+// workgroups clear the table's first rows whole, beside the sums the absent
+// rows of the rest.
 #include "embedding.h"
 
 #include <type_traits>
@@ -85,8 +87,8 @@ __global__ __launch_bounds__(256) void embedding_fp4_kernel(
 // ---------------------------------------------------------------------------
 // Sort.
 // ---------------------------------------------------------------------------
-constexpr int kTile = 4096;      // tokens a workgroup sorts
-constexpr int kSortThreads = 1024;
+constexpr int kTile = 2048;      // tokens a workgroup sorts
+constexpr int kSortThreads = 512;
 constexpr int kPer = kTile / kSortThreads;  // tokens a thread: 4 in a row
 constexpr int kPiece = 32;       // occurrences a wave adds
 
@@ -98,59 +100,103 @@ struct Sorted {
   uint32_t* start;
 };
 
-__device__ __forceinline__ uint32_t shfl_xor_key(uint32_t x, int o) {
-  return static_cast<uint32_t>(__shfl_xor(static_cast<int>(x), o, kWave));
+// The value of lane ^ O, by lane moves within rows of 16 and swaps of rows.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_u32(uint32_t x) {
+  return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), CTRL, 0xF, 0xF, true));
 }
-__device__ __forceinline__ uint64_t shfl_xor_key(uint64_t x, int o) {
-  return static_cast<uint64_t>(shfl_xor_key(static_cast<uint32_t>(x >> 32), o)) << 32 |
-         shfl_xor_key(static_cast<uint32_t>(x), o);
+template <int O>
+__device__ __forceinline__ uint32_t lane_xor(uint32_t x) {
+  if constexpr (O == 1) return dpp_u32<kDppXor1>(x);
+  if constexpr (O == 2) return dpp_u32<kDppXor2>(x);
+  if constexpr (O == 4) return dpp_u32<0x1B>(dpp_u32<kDppRowHalfMirror>(x));  // i ^ 7 ^ 3
+  if constexpr (O == 8) return dpp_u32<kDppRowRor8>(x);
+  if constexpr (O == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    return threadIdx.x & 16 ? r[0] : r[1];
+  }
+  if constexpr (O == 32) {
+    const auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+    return threadIdx.x & 32 ? r[0] : r[1];
+  }
+}
+template <int O>
+__device__ __forceinline__ uint64_t lane_xor(uint64_t x) {
+  return static_cast<uint64_t>(lane_xor<O>(static_cast<uint32_t>(x >> 32))) << 32 |
+         lane_xor<O>(static_cast<uint32_t>(x));
 }
 
-// Ascending bitonic sort of the workgroup's 4096 keys, thread t holding keys 4 t
-// ..; only the stages that `count` keys need (the others are the greatest).
-// buf: 4096 keys of LDS.
+// Ascending bitonic sort of the workgroup's keys, thread t holding keys 4 t ..;
+// only the stages that `count` keys need (the others are the greatest).  buf:
+// kTile keys of LDS.
 template <typename K>
 __device__ __forceinline__ void sort_tile(K (&key)[kPer], K* buf, int count) {
   const int t = threadIdx.x;
+  auto keep = [&](K& mine, K other, bool low) { mine = (mine < other) == low ? mine : other; };
   for (int size = 2; size < 2 * count && size <= kTile; size *= 2) {
-    for (int s = size / 2; s > 0; s /= 2) {
-      if (s >= kPer * kWave) {
-        __syncthreads();
+    const bool up = ((kPer * t) & size) == 0;
+    for (int s = size / 2; s >= kPer * kWave; s /= 2) {
+      __syncthreads();
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) buf[j * kSortThreads + t] = key[j];
-        __syncthreads();
-        const int o = t ^ (s / kPer);
-        const bool low = ((kPer * t & s) == 0) == ((kPer * t & size) == 0);
+      for (int j = 0; j < kPer; ++j) buf[j * kSortThreads + t] = key[j];
+      __syncthreads();
+      const int o = t ^ (s / kPer);
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          const K other = buf[j * kSortThreads + o];
-          key[j] = (key[j] < other) == low ? key[j] : other;
-        }
-      } else if (s >= kPer) {
-        const bool low = ((kPer * t & s) == 0) == ((kPer * t & size) == 0);
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) {
-          const K other = shfl_xor_key(key[j], s / kPer);
-          key[j] = (key[j] < other) == low ? key[j] : other;
-        }
-      } else {
-        auto order = [&](int a, int b) {
-          const bool up = ((kPer * t + a) & size) == 0;
-          const K x = key[a], y = key[b];
-          const bool swap = (x > y) == up;
-          key[a] = swap ? y : x;
-          key[b] = swap ? x : y;
-        };
-        if (s == 2) {
-          order(0, 2);
-          order(1, 3);
-        } else {
-          order(0, 1);
-          order(2, 3);
-        }
-      }
+      for (int j = 0; j < kPer; ++j)
+        keep(key[j], buf[j * kSortThreads + o], ((kPer * t & s) == 0) == up);
     }
+#define ITL_LANES(O)                                                                            \
+  if (size >= 2 * kPer * O) {                                                                   \
+    const bool low = ((t & O) == 0) == up;                                                      \
+    _Pragma("unroll") for (int j = 0; j < kPer; ++j) keep(key[j], lane_xor<O>(key[j]), low);    \
   }
+    ITL_LANES(32) ITL_LANES(16) ITL_LANES(8) ITL_LANES(4) ITL_LANES(2) ITL_LANES(1)
+#undef ITL_LANES
+    auto order = [&](int a, int b) {
+      const K x = key[a], y = key[b];
+      const bool swap = (x > y) == (((kPer * t + a) & size) == 0);
+      key[a] = swap ? y : x;
+      key[b] = swap ? x : y;
+    };
+    if (size >= 4) {
+      order(0, 2);
+      order(1, 3);
+    }
+    order(0, 1);
+    order(2, 3);
+  }
+}
+
+// Zeros in `bytes` bytes (even) from p on, by `count` threads.
+__device__ __forceinline__ void zero_bytes(char* p, int64_t bytes, int t, int count) {
+  const int64_t head = min((16 - static_cast<int64_t>(reinterpret_cast<uintptr_t>(p) % 16)) % 16,
+                           bytes);
+  const int64_t body = (bytes - head) / 16;
+  for (int64_t i = 2 * t; i < head; i += 2 * count) *reinterpret_cast<uint16_t*>(p + i) = 0;
+  uint4* q = reinterpret_cast<uint4*>(p + head);
+  for (int64_t i = t; i < body; i += count) q[i] = make_uint4(0, 0, 0, 0);
+  for (int64_t i = head + 16 * body + 2 * t; i < bytes; i += 2 * count)
+    *reinterpret_cast<uint16_t*>(p + i) = 0;
+}
+
+// Rows [begin, end) of the table, which workgroups beside another kernel's clear:
+// `step` rows each, from workgroup `first` on.  (A launch that waits for one
+// workgroup's sort would leave the memory idle.)
+struct Clear {
+  char* table;
+  int64_t ld, row_bytes;  // bytes
+  int64_t begin, end;
+  int first, step;
+};
+__device__ __forceinline__ void clear_rows(const Clear& c, int threads) {
+  const int64_t r0 = c.begin + static_cast<int64_t>(static_cast<int>(blockIdx.x) - c.first) * c.step;
+  const int64_t r1 = min(r0 + c.step, c.end);
+  if (c.ld == c.row_bytes) {
+    zero_bytes(c.table + r0 * c.ld, (r1 - r0) * c.ld, threadIdx.x, threads);
+    return;
+  }
+  for (int64_t r = r0 + threadIdx.x / kWave; r < r1; r += threads / kWave)
+    zero_bytes(c.table + r * c.ld, c.row_bytes, threadIdx.x % kWave, kWave);
 }
 
 // Tile blockIdx.x of the tokens.  Keys are (token, position in the tile), the
@@ -160,10 +206,11 @@ __device__ __forceinline__ void sort_tile(K (&key)[kPer], K* buf, int count) {
 template <bool SMALL>
 __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(
     const void* __restrict__ tok, int32_t tok32, int64_t n, int64_t v, int64_t ignore, Sorted out,
-    uint64_t* __restrict__ tiles) {
+    uint64_t* __restrict__ tiles, Clear clear) {
   using K = typename std::conditional<SMALL, uint32_t, uint64_t>::type;
   constexpr int kShift = SMALL ? 12 : 32;
   __shared__ K buf[kTile];
+  if (static_cast<int>(blockIdx.x) >= clear.first) return clear_rows(clear, kSortThreads);
   const Targets tokens{tok, tok32};
   const int64_t base = static_cast<int64_t>(blockIdx.x) * kTile;
   const int count = static_cast<int>(n - base < kTile ? n - base : kTile);
@@ -209,44 +256,43 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(
   }
 }
 
-// Where key k would stand among the `count` ascending keys.
-__device__ __forceinline__ int lower_bound(const uint64_t* keys, int count, uint64_t k) {
-  int lo = 0;
-  while (count > 0) {
-    const int half = count / 2;
-    if (keys[lo + half] < k) {
-      lo += half + 1;
-      count -= half + 1;
-    } else {
-      count = half;
-    }
-  }
-  return lo;
-}
+// The place of every key among all tiles': eight lanes a key, each searching every
+// eighth tile for the key and for its token's first.  (Keys are distinct, so
+// the number of smaller ones is the place.)
+constexpr int kRankLanes = 8, kRankKeys = 256 / kRankLanes;
 
 __global__ __launch_bounds__(256) void embed_rank_kernel(const uint64_t* __restrict__ tiles,
-                                                         int64_t n, Sorted out) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= n) return;
-  const uint64_t key = tiles[i], first = key >> 32 << 32;
-  const int64_t own = i / kTile * kTile;
-  int64_t rank = 0, start = 0;
-  for (int64_t b = 0; b < n; b += kTile) {
+                                                         int64_t n, Sorted out, Clear clear) {
+  if (static_cast<int>(blockIdx.x) >= clear.first) return clear_rows(clear, 256);
+  const int sub = threadIdx.x % kRankLanes;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kRankKeys + threadIdx.x / kRankLanes;
+  const uint64_t key = tiles[i < n ? i : n - 1], first = key >> 32 << 32;
+  uint32_t rank = 0, start = 0;
+  for (int64_t b = static_cast<int64_t>(sub) * kTile; b < n; b += kRankLanes * kTile) {
     const int count = static_cast<int>(n - b < kTile ? n - b : kTile);
-    const int lo = lower_bound(tiles + b, count, first);
-    start += lo;
-    if (b == own) {
-      rank += i - own;
-    } else {
-      rank += lo;
-      // the same token in an earlier tile stands before this one
-      if (b < own && lo < count && tiles[b + lo] >> 32 == key >> 32)
-        rank += lower_bound(tiles + b + lo, count - lo, key);
+    const uint64_t* t = tiles + b;
+    int at = 0, from = 0;
+#pragma unroll
+    for (int step = kTile / 2; step; step /= 2) {  // kTile - 1 keys at most
+      const int x = at + step - 1, y = from + step - 1;
+      const uint64_t kx = t[min(x, count - 1)], ky = t[min(y, count - 1)];
+      if (x < count && kx < key) at += step;
+      if (y < count && ky < first) from += step;
     }
+    if (at == kTile - 1 && count == kTile && t[kTile - 1] < key) ++at;  // all of a whole tile
+    if (from == kTile - 1 && count == kTile && t[kTile - 1] < first) ++from;
+    rank += at;
+    start += from;
   }
+#define ITL_ADD(O)                  \
+  rank += lane_xor<O>(rank);        \
+  start += lane_xor<O>(start);
+  ITL_ADD(1) ITL_ADD(2) ITL_ADD(4)
+#undef ITL_ADD
+  if (sub || i >= n) return;
   out.id[rank] = static_cast<uint32_t>(key >> 32);
   out.pos[rank] = static_cast<uint32_t>(key);
-  out.start[rank] = static_cast<uint32_t>(start);
+  out.start[rank] = start;
 }
 
 // ---------------------------------------------------------------------------
@@ -258,33 +304,64 @@ __device__ __forceinline__ int64_t partial_row(int64_t s, int64_t start) {
   return 2 * (s / kPiece) + (s != start);
 }
 
-// Writes scale a[], added to what is there with accumulate.
+// The table's element c: scale a, added to what is there with accumulate.
+template <typename U>
+__device__ __forceinline__ void table_store_one(U* row, int64_t c, float scale, bool accumulate,
+                                                float a) {
+  store_one<U>(row + c, accumulate ? fmaf(a, scale, Elt<U>::load(row, c)) : a * scale);
+}
+// Its whole chunk from element c on.
 template <typename U, bool VEC>
-__device__ __forceinline__ void table_store(U* row, int64_t c, int64_t h, float scale,
-                                            bool accumulate, float (&a)[kE]) {
+__device__ __forceinline__ void table_store(U* row, int64_t c, float scale, bool accumulate,
+                                            float (&a)[kE]) {
   if (accumulate) {
     float old[kE];
-    widen_raw<U>(load_raw<U, VEC>(row, c, h), old);
+    widen_raw<U>(load_raw<U, VEC>(row, c, c + kE), old);
 #pragma unroll
     for (int e = 0; e < kE; ++e) a[e] = fmaf(a[e], scale, old[e]);
   } else {
 #pragma unroll
     for (int e = 0; e < kE; ++e) a[e] = a[e] * scale;
   }
-  store_raw<U, VEC>(row, c, h, round_raw<U>(a));
+  store_raw<U, VEC>(row, c, c + kE, round_raw<U>(a));
 }
 
-// A wave a slot; those that begin a piece add its rows, CH chunks a lane.
-template <typename T, typename U, int CH, bool VEC>
-__global__ __launch_bounds__(256) void embed_sum_kernel(const T* __restrict__ dy, int64_t ld_y,
-                                                        Sorted sorted, int64_t n, int64_t v,
-                                                        int64_t h, float scale, bool accumulate,
-                                                        U* __restrict__ dtable, int64_t ld_t,
-                                                        float* __restrict__ partial, int64_t ld_p) {
+// acc += R rows of the wave's piece, from its row i0 on; cl: where the lane's
+// chunks are read.
+template <typename T, int R, int CH, bool VEC, bool TINY>
+__device__ __forceinline__ void add_rows(const T* __restrict__ dy, int64_t ld_y, uint32_t pos,
+                                         int i0, const int64_t (&cl)[CH], int64_t h,
+                                         float (&acc)[CH][kE]) {
+  Raw<T> x[R][CH];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const T* row = dy + static_cast<int64_t>(__builtin_amdgcn_readlane(pos, i0 + i)) * ld_y;
+#pragma unroll
+    for (int c = 0; c < CH; ++c)
+      x[i][c] = load_raw<T, VEC>(row, cl[c], TINY ? h : cl[c] + kE);
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      float p[kE];
+      widen_raw<T>(x[i][c], p);
+#pragma unroll
+      for (int e = 0; e < kE; ++e) acc[c][e] = acc[c][e] + p[e];
+    }
+}
+
+// A wave a slot; those that begin a piece add its rows, `span` columns of them,
+// CH chunks of 8 a lane at a time.  A chunk that would pass the row's end is
+// read from its last 8 elements and stores its own; rows of fewer than 8 are
+// TINY.
+template <typename T, typename U, int CH, bool VEC, bool TINY>
+__device__ __forceinline__ void sum_slot(const T* __restrict__ dy, int64_t ld_y,
+                                         const Sorted& sorted, int64_t s, int64_t n, int64_t v,
+                                         int64_t h, int64_t c_begin, int64_t c_end, float scale,
+                                         bool accumulate, U* dtable, int64_t ld_t, float* partial,
+                                         int64_t ld_p) {
   const int lane = threadIdx.x % kWave;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int64_t s = static_cast<int64_t>(blockIdx.x) * 4 + wave;
-  if (s >= n) return;
   const uint32_t id = sorted.id[s], start = sorted.start[s];
   if (id >= v || (s - start) % kPiece) return;
   // lane l looks at slot s + l: the piece's rows, and whether the run goes on
@@ -295,49 +372,99 @@ __global__ __launch_bounds__(256) void embed_sum_kernel(const T* __restrict__ dy
   const int reach = ~run ? __builtin_ctzll(~run) : kWave;
   const int count = reach < kPiece ? reach : kPiece;
   const bool pieces = s != start || reach > kPiece;
-  const int64_t c0 = static_cast<int64_t>(blockIdx.y) * (CH * kWave * kE) + lane * kE;
-  float acc[CH][kE];
+  for (int64_t c0 = c_begin; c0 < c_end; c0 += CH * kWave * kE) {
+    int64_t cl[CH];
+    float acc[CH][kE];
 #pragma unroll
-  for (int c = 0; c < CH; ++c)
+    for (int c = 0; c < CH; ++c) {
+      const int64_t col = c0 + (c * kWave + lane) * kE;
+      cl[c] = TINY ? col : col + kE <= h ? col : h - kE;
 #pragma unroll
-    for (int e = 0; e < kE; ++e) acc[c][e] = 0.0f;
-  constexpr int kRows = 4;  // rows whose loads are in flight together
-  for (int i0 = 0; i0 < count; i0 += kRows) {
-    Raw<T> x[kRows][CH];
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      if (i0 + i < count) {
-        const T* row = dy + static_cast<int64_t>(__builtin_amdgcn_readlane(pos, i0 + i)) * ld_y;
-#pragma unroll
-        for (int c = 0; c < CH; ++c) x[i][c] = load_raw<T, VEC>(row, c0 + c * kWave * kE, h);
-      }
+      for (int e = 0; e < kE; ++e) acc[c][e] = 0.0f;
     }
+    int i = 0;
+    for (; i + 8 <= count; i += 8) add_rows<T, 8, CH, VEC, TINY>(dy, ld_y, pos, i, cl, h, acc);
+    if (count & 4) {
+      add_rows<T, 4, CH, VEC, TINY>(dy, ld_y, pos, i, cl, h, acc);
+      i += 4;
+    }
+    if (count & 2) {
+      add_rows<T, 2, CH, VEC, TINY>(dy, ld_y, pos, i, cl, h, acc);
+      i += 2;
+    }
+    if (count & 1) add_rows<T, 1, CH, VEC, TINY>(dy, ld_y, pos, i, cl, h, acc);
+    U* row = dtable + static_cast<int64_t>(id) * ld_t;
+    float* part = partial + partial_row(s, start) * ld_p;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      if (i0 + i < count) {
+    for (int c = 0; c < CH; ++c) {
+      const int64_t col = c0 + (c * kWave + lane) * kE;
+      if (col >= h) break;
+      if (!TINY && col + kE <= h) {
+        if (pieces) {
+          float4* to = reinterpret_cast<float4*>(part + col);
+          to[0] = make_float4(acc[c][0], acc[c][1], acc[c][2], acc[c][3]);
+          to[1] = make_float4(acc[c][4], acc[c][5], acc[c][6], acc[c][7]);
+        } else {
+          table_store<U, VEC>(row, col, scale, accumulate, acc[c]);
+        }
+      } else {
 #pragma unroll
-        for (int c = 0; c < CH; ++c) {
-          float p[kE];
-          widen_raw<T>(x[i][c], p);
-#pragma unroll
-          for (int e = 0; e < kE; ++e) acc[c][e] = acc[c][e] + p[e];
+        for (int e = 0; e < kE; ++e) {
+          const int64_t k = cl[c] + e;
+          if (k < col || k >= h) continue;
+          if (pieces)
+            part[k] = acc[c][e];
+          else
+            table_store_one<U>(row, k, scale, accumulate, acc[c][e]);
         }
       }
     }
   }
-#pragma unroll
-  for (int c = 0; c < CH; ++c) {
-    const int64_t col = c0 + c * kWave * kE;
-    if (col >= h) break;
-    if (pieces) {
-      float4* to = reinterpret_cast<float4*>(partial + partial_row(s, start) * ld_p + col);
-      to[0] = make_float4(acc[c][0], acc[c][1], acc[c][2], acc[c][3]);
-      to[1] = make_float4(acc[c][4], acc[c][5], acc[c][6], acc[c][7]);
-    } else {
-      table_store<U, VEC>(dtable + static_cast<int64_t>(id) * ld_t, col, h, scale, accumulate,
-                          acc[c]);
-    }
+}
+
+// Zeros in the rows of absent tokens, 64 rows from v0 on.
+template <typename U>
+__device__ __forceinline__ void zero_absent(const uint32_t* __restrict__ id, int64_t n, int64_t v0,
+                                            int64_t v, int64_t h, U* dtable, int64_t ld_t) {
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int64_t row = v0 + lane;
+  int64_t lo = 0, hi = n;
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) / 2;
+    if (id[mid] < row) lo = mid + 1; else hi = mid;
   }
+  const uint64_t absent = __builtin_amdgcn_ballot_w64(row < v && !(lo < n && id[lo] == row));
+  for (int i = wave; i < kWave; i += 4)
+    if ((absent >> i) & 1)
+      zero_bytes(reinterpret_cast<char*>(dtable + (v0 + i) * ld_t),
+                 h * static_cast<int64_t>(sizeof(U)), lane, kWave);
+}
+
+// Workgroups below sum_groups: four slots each, `splits` column spans; the others
+// clear the absent rows from row z0 on.  In one launch the sums, which wait for
+// a chain of loads, run beside the zeros, which fill the memory's time.
+template <typename T, typename U, int CH, bool VEC, bool TINY>
+__global__ __launch_bounds__(256) void embed_sum_kernel(const T* __restrict__ dy, int64_t ld_y,
+                                                        Sorted sorted, int64_t n, int64_t v,
+                                                        int64_t h, int splits, int64_t span,
+                                                        int64_t sum_groups, float scale,
+                                                        bool accumulate, U* __restrict__ dtable,
+                                                        int64_t ld_t, float* __restrict__ partial,
+                                                        int64_t ld_p, int64_t z0) {
+  const int64_t g = blockIdx.x;
+  if (g < sum_groups) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int64_t s = g / splits * 4 + wave, c0 = g % splits * span;
+    if (s < n)
+      sum_slot<T, U, CH, VEC, TINY>(dy, ld_y, sorted, s, n, v, h, c0,
+                                    c0 + span < h ? c0 + span : h, scale, accumulate, dtable, ld_t,
+                                    partial, ld_p);
+    return;
+  }
+  const int64_t step = (gridDim.x - sum_groups) * kWave;
+  for (int64_t v0 = z0 + (g - sum_groups) * kWave; v0 < v; v0 += step)
+    zero_absent<U>(sorted.id, n, v0, v, h, dtable, ld_t);
 }
 
 // The runs of several pieces: at most one begins in window blockIdx.x of kPiece
@@ -384,34 +511,13 @@ __global__ __launch_bounds__(256) void embed_join_kernel(const float* __restrict
   for (int g = 1; g < kJoinGroups; ++g)
 #pragma unroll
     for (int e = 0; e < kE; ++e) a[e] = a[e] + part[g][e * 32 + t];
-  table_store<U, VEC>(dtable + static_cast<int64_t>(id) * ld_t, col, h, scale, accumulate, a);
-}
-
-// Zeros in the rows of absent tokens, 64 rows a workgroup and step.
-template <typename U, bool VEC>
-__global__ __launch_bounds__(256) void embed_zero_kernel(const uint32_t* __restrict__ id, int64_t n,
-                                                         int64_t v, int64_t h,
-                                                         U* __restrict__ dtable, int64_t ld_t) {
-  const int lane = threadIdx.x % kWave;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  for (int64_t v0 = static_cast<int64_t>(blockIdx.x) * kWave; v0 < v;
-       v0 += static_cast<int64_t>(gridDim.x) * kWave) {
-    const int64_t row = v0 + lane;
-    int64_t lo = 0, hi = n;
-    while (lo < hi) {
-      const int64_t mid = (lo + hi) / 2;
-      if (id[mid] < row) lo = mid + 1; else hi = mid;
-    }
-    const uint64_t absent =
-        __builtin_amdgcn_ballot_w64(row < v && !(lo < n && id[lo] == row));
-    Raw<U> zero;
+  U* row = dtable + static_cast<int64_t>(id) * ld_t;
+  if (col + kE <= h) {
+    table_store<U, VEC>(row, col, scale, accumulate, a);
+  } else {
 #pragma unroll
-    for (int p = 0; p < kRaw<U>; ++p) zero.q[p] = make_uint4(0, 0, 0, 0);
-    for (int i = wave; i < kWave; i += 4) {
-      if (!((absent >> i) & 1)) continue;
-      for (int64_t c = lane * kE; c < h; c += kWave * kE)
-        store_raw<U, VEC>(dtable + (v0 + i) * ld_t, c, h, zero);
-    }
+    for (int e = 0; e < kE; ++e)
+      if (col + e < h) table_store_one<U>(row, col + e, scale, accumulate, a[e]);
   }
 }
 
@@ -435,6 +541,10 @@ BwdLayout bwd_layout(int64_t n, int64_t h) {
   return l;
 }
 
+// Bytes that workgroups beside the sort, and beside the ranking, clear: what
+// the memory takes in their time (7 us and 6).
+constexpr int64_t kSortClears = int64_t{40} << 20, kRankClears = int64_t{32} << 20;
+
 template <typename T, typename U>
 void bwd_typed(const void* dy, int64_t ld_y, Targets tokens, int64_t n, int64_t v, int64_t h,
                int64_t ignore, float scale, bool accumulate, void* dtable, int64_t ld_t, char* ws,
@@ -446,34 +556,52 @@ void bwd_typed(const void* dy, int64_t ld_y, Targets tokens, int64_t n, int64_t 
   uint64_t* tiles = n > kTile ? reinterpret_cast<uint64_t*>(ws + l.tiles) : nullptr;
   float* partial = reinterpret_cast<float*>(ws + l.partial);
   U* out = static_cast<U*>(dtable);
-  const bool vec_out = fits16(dtable, ld_t, sizeof(U));
+  const int size = sizeof(U);
+  const bool vec_out = fits16(dtable, ld_t, size);
+  // Rows below `clear.end` are cleared whole before the sums are written.
+  Clear clear{static_cast<char*>(dtable), ld_t * size, h * size, 0, 0, 0, 0};
+  // Workgroups for the next `bytes` bytes, about 256 KiB each.
+  auto clears = [&](int64_t bytes, int first) -> unsigned {
+    clear.first = first;
+    if (accumulate) return 0;
+    const int64_t rows = bytes / clear.row_bytes, left = v - clear.end;
+    clear.begin = clear.end;
+    clear.end += rows < left ? rows : left;
+    const int64_t step = (int64_t{256} << 10) / clear.row_bytes;
+    clear.step = step > 1 ? static_cast<int>(step) : 1;
+    return static_cast<unsigned>((clear.end - clear.begin + clear.step - 1) / clear.step);
+  };
   if (n) {
+    const unsigned groups = static_cast<unsigned>((n + kTile - 1) / kTile);
+    const unsigned more = clears(kSortClears, static_cast<int>(groups));
     auto sort = v < (1 << 20) - 1 ? embed_sort_kernel<true> : embed_sort_kernel<false>;
-    hipLaunchKernelGGL(sort, dim3(static_cast<unsigned>((n + kTile - 1) / kTile)),
-                       dim3(kSortThreads), 0, s, tokens.p, tokens.is32, n, v, ignore, sorted,
-                       tiles);
-    if (tiles)
-      hipLaunchKernelGGL(embed_rank_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256),
-                         0, s, tiles, n, sorted);
+    hipLaunchKernelGGL(sort, dim3(groups + more), dim3(kSortThreads), 0, s, tokens.p, tokens.is32,
+                       n, v, ignore, sorted, tiles, clear);
   }
-  if (!accumulate) {
-    const int64_t groups = (v + kWave - 1) / kWave;
-    hipLaunchKernelGGL((vec_out ? embed_zero_kernel<U, true> : embed_zero_kernel<U, false>),
-                       dim3(static_cast<unsigned>(groups < kMaxGroups ? groups : kMaxGroups)),
-                       dim3(256), 0, s, sorted.id, n, v, h, out, ld_t);
+  if (tiles) {
+    const unsigned groups = static_cast<unsigned>((n + kRankKeys - 1) / kRankKeys);
+    const unsigned more = clears(kRankClears, static_cast<int>(groups));
+    hipLaunchKernelGGL(embed_rank_kernel, dim3(groups + more), dim3(256), 0, s, tiles, n, sorted,
+                       clear);
   }
-  if (!n) return;
-  const bool vec = vec_out && fits16(dy, ld_y, sizeof(T));
-  constexpr int CH = sizeof(T) == 4 ? 2 : 4;  // four rows of 64 bytes a lane in flight
-  const bool narrow = h <= kWave * kE;
-  auto sum = narrow ? (vec ? embed_sum_kernel<T, U, 1, true> : embed_sum_kernel<T, U, 1, false>)
-                    : (vec ? embed_sum_kernel<T, U, CH, true> : embed_sum_kernel<T, U, CH, false>);
-  const int64_t cols = (narrow ? 1 : CH) * kWave * kE;
-  hipLaunchKernelGGL(sum,
-                     dim3(static_cast<unsigned>((n + 3) / 4),
-                          static_cast<unsigned>((h + cols - 1) / cols)),
-                     dim3(256), 0, s, static_cast<const T*>(dy), ld_y, sorted, n, v, h, scale,
-                     accumulate, out, ld_t, partial, l.ld_p);
+  const bool vec = vec_out && fits16(dy, ld_y, sizeof(T)) && h % kE == 0;
+  constexpr int CH = sizeof(T) == 4 ? 1 : 2;  // 32 bytes a lane and row
+  auto kern = h < kE ? embed_sum_kernel<T, U, CH, false, true>
+              : vec  ? embed_sum_kernel<T, U, CH, true, false>
+                     : embed_sum_kernel<T, U, CH, false, false>;
+  // A slot's columns are split while there are fewer waves than the GPU holds.
+  const int64_t unit = CH * kWave * kE, units = (h + unit - 1) / unit;
+  int64_t splits = n ? 8192 / n : 1;
+  splits = splits < 1 ? 1 : splits > units ? units : splits;
+  const int64_t span = (units + splits - 1) / splits * unit;
+  const int64_t sum_groups = (n + 3) / 4 * splits;
+  const int64_t z0 = accumulate ? v : clear.end;
+  const int64_t absent = (v - z0 + kWave - 1) / kWave;
+  const int64_t total = sum_groups + (absent < kMaxGroups ? absent : kMaxGroups);
+  if (total)
+    hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(total)), dim3(256), 0, s,
+                       static_cast<const T*>(dy), ld_y, sorted, n, v, h, static_cast<int>(splits),
+                       span, sum_groups, scale, accumulate, out, ld_t, partial, l.ld_p, z0);
   if (n > kPiece)
     hipLaunchKernelGGL((vec_out ? embed_join_kernel<U, true> : embed_join_kernel<U, false>),
                        dim3(static_cast<unsigned>((n + kPiece - 1) / kPiece),
