@@ -14,12 +14,11 @@ and its backward it must stay as it is.  draw tells the calls of one seed apart
 """
 
 import torch
-from torch.autograd.function import once_differentiable
 
 from . import _lib
 from .ops import _DTYPES, _INDEX, _dtype_code, _nbytes, _ptr, _row_vector
-from .token_ops import (Fp4Rows, _call, _fp4_operand, _norm_out, _norm_rows, _norm_weight,
-                        _same_device, _stride, _workspace)
+from .token_ops import (Fp4Rows, _call, _first_order, _fp4_operand, _norm_out, _norm_rows,
+                        _norm_weight, _same_device, _stride, _workspace)
 
 
 def _ids(t, device):
@@ -109,7 +108,7 @@ class _Embedding(torch.autograd.Function):
         return embedding_fwd(token_ids, weight, scale, ignore_index)
 
     @staticmethod
-    @once_differentiable
+    @_first_order
     def backward(ctx, g):
         (token_ids,) = ctx.saved_tensors
         return None, embedding_bwd(token_ids, g.contiguous(), *ctx.options), None, None
@@ -163,7 +162,7 @@ class _Dropout(torch.autograd.Function):
         return dropout_fwd(x, p, seed, residual, draw, first_row)
 
     @staticmethod
-    @once_differentiable
+    @_first_order
     def backward(ctx, g):
         p, seed, draw, first_row = ctx.options
         if seed is None:
@@ -191,6 +190,28 @@ def _drop_args(p, seed, draw, first_row, device):
     return (float(p), *_seed(seed, device), int(draw), int(first_row))
 
 
+def _layer_norm_forward(x, weight, bias, residual, eps, drop, stats, y_out, sum_out):
+    """(y, s), with the rows' means and then their rstd in stats [2 N] (or None)."""
+    px, n, h, ld_x = _norm_rows(x, "x")
+    code = _dtype_code(x)
+    pw, pb = _norm_weight(weight, x), _norm_bias(bias, x)
+    y, py, ld_y = _norm_out(y_out, "y_out", x, h)
+    pr, ld_r, ps, ld_s, s = None, 0, None, 0, x
+    if residual is not None:
+        pr, _, _, ld_r = _norm_rows(residual, "residual", x)
+    if residual is not None or drop[0] or sum_out is not None:
+        s, ps, ld_s = _norm_out(sum_out, "sum_out", x, h)
+    pm = stats.data_ptr() if stats is not None else None
+    _call("layer_norm_fwd", x.device, px, ld_x, pr, ld_r, pw, pb, code, n, h, eps, *drop, py, ld_y,
+          ps, ld_s, pm, pm + 4 * n if pm is not None else None)
+    return y, s
+
+
+def _stats(x):
+    return torch.empty(2 * (x.numel() // x.shape[-1] if x.numel() else 0), dtype=torch.float32,
+                       device=x.device)
+
+
 def layer_norm_fwd(x, weight, bias=None, residual=None, eps=1e-5, dropout=0.0, seed=None, draw=0,
                    first_row=0, return_stats=False, y_out=None, sum_out=None):
     """Layer norm of s = residual + dropped(x) (dropout_fwd's arguments; s = x
@@ -198,23 +219,42 @@ def layer_norm_fwd(x, weight, bias=None, residual=None, eps=1e-5, dropout=0.0, s
     y = (s - mean(s)) / sqrt(var(s) + eps) * weight + bias, mean and rstd [N]
     float32 (None unless asked for).  x [*lead, H] float32, bfloat16 or float16,
     weight and bias [H].  sum_out receives s and may be x or residual."""
-    px, n, h, ld_x = _norm_rows(x, "x")
-    code = _dtype_code(x)
-    pw, pb = _norm_weight(weight, x), _norm_bias(bias, x)
-    dev = x.device
-    drop = _drop_args(dropout, seed, draw, first_row, dev)
-    y, py, ld_y = _norm_out(y_out, "y_out", x, h)
-    pr, ld_r, ps, ld_s, s = None, 0, None, 0, x
-    if residual is not None:
-        pr, _, _, ld_r = _norm_rows(residual, "residual", x)
-    if residual is not None or drop[0] or sum_out is not None:
-        s, ps, ld_s = _norm_out(sum_out, "sum_out", x, h)
-    mean, rstd = None, None
-    if return_stats:
-        mean, rstd = torch.empty(2, n, dtype=torch.float32, device=dev)
-    _call("layer_norm_fwd", dev, px, ld_x, pr, ld_r, pw, pb, code, n, h, float(eps), *drop, py,
-          ld_y, ps, ld_s, _ptr(mean), _ptr(rstd))
+    if not x.is_cuda:
+        raise ValueError("tensors must be on a ROCm device")
+    stats = _stats(x) if return_stats else None
+    y, s = _layer_norm_forward(x, weight, bias, residual, float(eps),
+                               _drop_args(dropout, seed, draw, first_row, x.device), stats, y_out,
+                               sum_out)
+    mean, rstd = stats.view(2, -1) if return_stats else (None, None)
     return y, s, mean, rstd
+
+
+def _layer_norm_backward(s, weight, pm, prs, grad_y, grad_sum, drop, need_dresidual, need_dweight,
+                         need_dbias, dx_out, dresidual_out, workspace):
+    p_s, n, h, ld_s = _norm_rows(s, "s")
+    code = _dtype_code(s)
+    pw = _norm_weight(weight, s)
+    dev = s.device
+    pg, _, _, ld_g = _norm_rows(grad_y, "grad_y", s)
+    pd, ld_d = None, 0
+    if grad_sum is not None:
+        pd, _, _, ld_d = _norm_rows(grad_sum, "grad_sum", s)
+    dx, px, ld_x = _norm_out(dx_out, "dx_out", s, h)
+    dres, pr, ld_r = dx, None, 0
+    if not need_dresidual:
+        dres = None
+    elif drop[0]:
+        dres, pr, ld_r = _norm_out(dresidual_out, "dresidual_out", s, h)
+    if dresidual_out is not None and pr is None:
+        raise ValueError("dresidual_out is for a gradient through dropout that is asked for")
+    dw = torch.empty_like(weight) if need_dweight else None
+    db = torch.empty_like(weight) if need_dbias else None
+    ws = None
+    if need_dweight or need_dbias:
+        ws = _workspace(workspace, _lib.lib().layer_norm_bwd_workspace_bytes(n, h), dev)
+    _call("layer_norm_bwd", dev, p_s, ld_s, pw, pm, prs, pg, ld_g, pd, ld_d, code, n, h, *drop, px,
+          ld_x, pr, ld_r, _ptr(dw), _ptr(db), _ptr(ws), _nbytes(ws))
+    return dx, dres, dw, db
 
 
 def layer_norm_bwd(s, weight, mean, rstd, grad_y, grad_sum=None, dropout=0.0, seed=None, draw=0,
@@ -224,65 +264,51 @@ def layer_norm_bwd(s, weight, mean, rstd, grad_y, grad_sum=None, dropout=0.0, se
     mean, rstd and the gradients of y and (where given) of s.  Without dropout
     dresidual is dx itself.  dx_out and dresidual_out may be grad_y or grad_sum,
     not one another; what is not needed is None."""
-    p_s, n, h, ld_s = _norm_rows(s, "s")
-    code = _dtype_code(s)
-    pw = _norm_weight(weight, s)
-    dev = s.device
-    drop = _drop_args(dropout, seed, draw, first_row, dev)
-    pg, _, _, ld_g = _norm_rows(grad_y, "grad_y", s)
-    pd, ld_d = None, 0
-    if grad_sum is not None:
-        pd, _, _, ld_d = _norm_rows(grad_sum, "grad_sum", s)
+    n = _norm_rows(s, "s")[1]
     mean, rstd = _row_vector(mean, n, "mean"), _row_vector(rstd, n, "rstd")
-    _same_device(dev, mean=mean, rstd=rstd)
-    dx, px, ld_x = _norm_out(dx_out, "dx_out", s, h)
-    dres, pr, ld_r = dx, None, 0
-    if not need_dresidual:
-        dres = None
-    elif drop[0]:
-        dres, pr, ld_r = _norm_out(dresidual_out, "dresidual_out", s, h)
-    if dresidual_out is not None and pr is None:
-        raise ValueError("dresidual_out is for a gradient through dropout that is asked for")
-    dw = torch.empty(h, dtype=s.dtype, device=dev) if need_dweight else None
-    db = torch.empty(h, dtype=s.dtype, device=dev) if need_dbias else None
-    need = _lib.lib().layer_norm_bwd_workspace_bytes(n, h) if need_dweight or need_dbias else 0
-    ws = _workspace(workspace, need, dev)
-    _call("layer_norm_bwd", dev, p_s, ld_s, pw, mean.data_ptr(), rstd.data_ptr(), pg, ld_g, pd,
-          ld_d, code, n, h, *drop, px, ld_x, pr, ld_r, _ptr(dw), _ptr(db), _ptr(ws), _nbytes(ws))
-    return dx, dres, dw, db
+    _same_device(s.device, mean=mean, rstd=rstd)
+    return _layer_norm_backward(s, weight, mean.data_ptr(), rstd.data_ptr(), grad_y, grad_sum,
+                                _drop_args(dropout, seed, draw, first_row, s.device),
+                                need_dresidual, need_dweight, need_dbias, dx_out, dresidual_out,
+                                workspace)
 
 
 class _LayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, residual, eps, p, seed, draw, first_row):
-        y, s, mean, rstd = layer_norm_fwd(x, weight, bias, residual, eps, p, seed, draw, first_row,
-                                          return_stats=True)
+        if not x.is_cuda:
+            raise ValueError("tensors must be on a ROCm device")
+        stats = _stats(x)
+        y, s = _layer_norm_forward(x, weight, bias, residual, eps,
+                                   _drop_args(p, seed, draw, first_row, x.device), stats, None,
+                                   None)
         held = isinstance(seed, torch.Tensor)
-        ctx.save_for_backward(s, weight, mean, rstd, seed if held else None)
+        ctx.save_for_backward(s, weight, stats, seed if held else None)
         ctx.options = (p, None if held else seed, draw, first_row)
-        ctx.fused = residual is not None
         ctx.set_materialize_grads(False)
-        return (y, s) if ctx.fused else y
+        return y if residual is None else (y, s)
 
     @staticmethod
-    @once_differentiable
+    @_first_order
     def backward(ctx, gy, gs=None):
-        s, weight, mean, rstd, held = ctx.saved_tensors
+        s, weight, stats, held = ctx.saved_tensors
         p, seed, draw, first_row = ctx.options
         seed = held if seed is None else seed
         need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
+        # gradients may come in broadcast (a row for all rows, one value for all)
+        gs = gs.contiguous() if gs is not None else None
         if gy is None:  # only the stored sum was used, or nothing
-            gs = gs.contiguous() if gs is not None else None
             dx = gs
             if p and need_x and gs is not None:
                 dx = dropout_bwd(gs, p, seed, draw, first_row)
             zero = torch.zeros_like(weight) if need_w or need_b else None
-            return dx, zero if need_w else None, zero if need_b else None, gs, *[None] * 5
-        # gradients may come in broadcast (a row for all rows, one value for all)
-        gs = gs.contiguous() if gs is not None else None
-        dx, dres, dw, db = layer_norm_bwd(s, weight, mean, rstd, gy.contiguous(), gs, p, seed, draw,
-                                          first_row, need_r, need_w, need_b)
-        return dx, dw, db, dres, *[None] * 5
+            return (dx, zero if need_w else None, zero if need_b else None, gs, None, None, None,
+                    None, None)
+        pm = stats.data_ptr()
+        dx, dres, dw, db = _layer_norm_backward(
+            s, weight, pm, pm + 2 * stats.numel(), gy.contiguous(), gs,
+            _drop_args(p, seed, draw, first_row, s.device), need_r, need_w, need_b, None, None, None)
+        return dx, dw, db, dres, None, None, None, None, None
 
 
 def layer_norm(x, weight, bias=None, residual=None, eps=1e-5, dropout=0.0, seed=None, draw=0,

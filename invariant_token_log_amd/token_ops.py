@@ -52,18 +52,33 @@ class Fp4Rows(NamedTuple):
     scale: torch.Tensor
 
 
+_functions = {}  # the library's, by name
+
+
 def _call(name, device, *args):
     """The library function on the device's current stream (its last
     argument), with that device current; a non-zero status raises."""
-    fn = getattr(_lib.lib(), name)
+    fn = _functions.get(name)
+    if fn is None:
+        fn = _functions[name] = getattr(_lib.lib(), name)
     index = device.index
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
             st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     if st:
         check(name, st)
+
+
+def _first_order(backward):
+    """once_differentiable, at no cost where no second derivative is asked for."""
+    guarded = once_differentiable(backward)
+
+    def run(ctx, *grads):
+        return guarded(ctx, *grads) if torch.is_grad_enabled() else backward(ctx, *grads)
+
+    return run
 
 
 def _tokens(t, n, lead, device):
@@ -485,30 +500,34 @@ def _norm_rows(x, name, like=None):
     flatten without a copy."""
     if not x.is_cuda:
         raise ValueError("tensors must be on a ROCm device")
-    if like is not None and (x.shape != like.shape or x.dtype != like.dtype
-                             or x.device != like.device):
+    shape = x.shape
+    if like is not None and (shape != like.shape or x.dtype != like.dtype
+                             or x.get_device() != like.get_device()):
         raise ValueError(f"{name} must match x in shape, dtype and device")
-    if x.dim() < 1 or x.stride(-1) != 1 and x.shape[-1] > 1:
-        raise ValueError(f"{name} must have a contiguous last dimension")
-    h = x.shape[-1]
-    if x.is_contiguous():
+    dim = len(shape)
+    if dim and x.is_contiguous():
+        h = shape[-1]
         return x.data_ptr(), x.numel() // h if h else 0, h, h
-    x2 = x if x.dim() == 2 else x.view(-1, h)
+    if dim < 1 or x.stride(-1) != 1 and shape[-1] > 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+    h = shape[-1]
+    x2 = x if dim == 2 else x.view(-1, h)
     return x2.data_ptr(), x2.shape[0], h, x2.stride(0) if x2.shape[0] > 1 else h
 
 
 def _norm_out(given, name, like, h):
     """An output like `like`: (tensor, pointer, row stride)."""
     if given is None:
-        o = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        o = (torch.empty_like(like) if like.is_contiguous()
+             else torch.empty(like.shape, dtype=like.dtype, device=like.device))
         return o, o.data_ptr(), h
     p, _, _, ld = _norm_rows(given, name, like)
     return given, p, ld
 
 
 def _norm_weight(weight, x, name="weight"):
-    if (weight.shape != x.shape[-1:] or weight.dtype != x.dtype or weight.device != x.device
-            or not weight.is_contiguous()):
+    if (weight.dim() != 1 or weight.shape[0] != x.shape[-1] or weight.dtype != x.dtype
+            or weight.get_device() != x.get_device() or not weight.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous [H] of x's dtype and device")
     return weight.data_ptr()
 
