@@ -140,8 +140,9 @@ int32_t layer_norm_fwd(const void* x, int64_t ld_x, const void* residual, int64_
 
 size_t layer_norm_bwd_workspace_bytes(int64_t n, int64_t h) {
   if (n < 1 || h < 1 || h > itl::kMaxNorm) return 0;
-  return itl::ws_round(static_cast<size_t>(itl::layer_norm_bwd_blocks(n, h)) *
-                       static_cast<size_t>(h) * 8);
+  const int64_t wide = itl::layer_norm_bwd_blocks(itl::kF32, n, h);
+  const int64_t half = itl::layer_norm_bwd_blocks(itl::kBF16, n, h);
+  return itl::ws_round(static_cast<size_t>(wide > half ? wide : half) * static_cast<size_t>(h) * 8);
 }
 
 int32_t layer_norm_bwd(const void* s, int64_t ld_s, const void* weight, const float* mean,

@@ -35,7 +35,7 @@ struct LayerNormGrad {
 };
 
 // Partial rows (of 2 h floats each) of the weight's and bias's gradients.
-int64_t layer_norm_bwd_blocks(int64_t n, int64_t h);
+int64_t layer_norm_bwd_blocks(int dtype, int64_t n, int64_t h);
 
 void launch_layer_norm_bwd(int dtype, const LayerNormGrad& g, int64_t n, int64_t h, float* partial,
                            hipStream_t s);

@@ -26,6 +26,34 @@ namespace itl {
 
 namespace {
 
+// A row's chunk at element c, 0 past h.  VEC: 16-byte rows of whole chunks.
+template <typename T, bool VEC>
+__device__ __forceinline__ Raw<T> load_chunk(const T* row, int64_t c, int64_t h) {
+  if constexpr (VEC) {
+    Raw<T> r;
+#pragma unroll
+    for (int p = 0; p < kRaw<T>; ++p) r.q[p] = make_uint4(0, 0, 0, 0);
+    if (c < h) {
+#pragma unroll
+      for (int p = 0; p < kRaw<T>; ++p) r.q[p] = *(reinterpret_cast<const uint4*>(row + c) + p);
+    }
+    return r;
+  } else {
+    return load_raw<T, false>(row, c, h);
+  }
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_chunk(T* row, int64_t c, int64_t h, const Raw<T>& r) {
+  if constexpr (VEC) {
+    if (c < h) {
+#pragma unroll
+      for (int p = 0; p < kRaw<T>; ++p) *(reinterpret_cast<uint4*>(row + c) + p) = r.q[p];
+    }
+  } else {
+    store_raw<T, false>(row, c, h, r);
+  }
+}
+
 // s of one chunk: x, dropped and added to the residual, rounded to its type.
 template <typename T, bool DROP>
 __device__ __forceinline__ Raw<T> stream_chunk(const Raw<T>& x, const Raw<T>& residual, bool add,
@@ -104,11 +132,11 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void layer_norm_kernel(
   if (TEAM == kWave && r >= n) return;  // a wider team fills its workgroup: r < n
   Raw<T> s[CH], a[CH], w[CH], b[CH];
 #pragma unroll
-  for (int c = 0; c < CH; ++c) s[c] = load_raw<T, VEC>(x + r * ld_x, (c * TEAM + t) * kE, h);
+  for (int c = 0; c < CH; ++c) s[c] = load_chunk<T, VEC>(x + r * ld_x, (c * TEAM + t) * kE, h);
   if (residual) {
 #pragma unroll
     for (int c = 0; c < CH; ++c)
-      a[c] = load_raw<T, VEC>(residual + r * ld_r, (c * TEAM + t) * kE, h);
+      a[c] = load_chunk<T, VEC>(residual + r * ld_r, (c * TEAM + t) * kE, h);
   }
   const uint64_t seed = DROP ? drop_seed(drop) : 0;
   if (DROP || residual) {
@@ -117,15 +145,15 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void layer_norm_kernel(
       s[c] = stream_chunk<T, DROP>(s[c], a[c], residual != nullptr, drop, seed, r, c * TEAM + t);
   }
 #pragma unroll
-  for (int c = 0; c < CH; ++c) w[c] = load_raw<T, VEC>(weight, (c * TEAM + t) * kE, h);
+  for (int c = 0; c < CH; ++c) w[c] = load_chunk<T, VEC>(weight, (c * TEAM + t) * kE, h);
   if (bias) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) b[c] = load_raw<T, VEC>(bias, (c * TEAM + t) * kE, h);
+    for (int c = 0; c < CH; ++c) b[c] = load_chunk<T, VEC>(bias, (c * TEAM + t) * kE, h);
   }
   if (sum) {
 #pragma unroll
     for (int c = 0; c < CH; ++c)
-      store_raw<T, VEC>(sum + r * ld_s, (c * TEAM + t) * kE, h, s[c]);
+      store_chunk<T, VEC>(sum + r * ld_s, (c * TEAM + t) * kE, h, s[c]);
   }
   float m = 0.0f, ss = 0.0f;
 #pragma unroll
@@ -141,7 +169,7 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void layer_norm_kernel(
   }
 #pragma unroll
   for (int c = 0; c < CH; ++c)
-    store_raw<T, VEC>(y + r * ld_y, (c * TEAM + t) * kE, h,
+    store_chunk<T, VEC>(y + r * ld_y, (c * TEAM + t) * kE, h,
                       norm_chunk<T>(s[c], w[c], b[c], bias != nullptr, m, rstd));
 }
 
@@ -160,16 +188,16 @@ __global__ __launch_bounds__(kLongTeam) void layer_norm_long_kernel(
   const uint64_t seed = DROP ? drop_seed(drop) : 0;
   float m = 0.0f, ss = 0.0f;
   for (int64_t k = threadIdx.x; k * kE < h; k += kLongTeam) {
-    Raw<T> s = load_raw<T, VEC>(xr, k * kE, h), a;
-    if (residual) a = load_raw<T, VEC>(residual + r * ld_r, k * kE, h);
+    Raw<T> s = load_chunk<T, VEC>(xr, k * kE, h), a;
+    if (residual) a = load_chunk<T, VEC>(residual + r * ld_r, k * kE, h);
     s = stream_chunk<T, DROP>(s, a, residual != nullptr, drop, seed, r, k);
-    if (sum) store_raw<T, VEC>(sum + r * ld_s, k * kE, h, s);
+    if (sum) store_chunk<T, VEC>(sum + r * ld_s, k * kE, h, s);
     m = add_chunk<T>(s, m);
   }
   const T* sr = sum ? sum + r * ld_s : xr;
   m = team_reduce<kLongTeam, false>(m, buf[0]) * inv_h;
   for (int64_t k = threadIdx.x; k * kE < h; k += kLongTeam)
-    ss = add_squares<T>(load_raw<T, VEC>(sr, k * kE, h), k * kE, h, m, ss);
+    ss = add_squares<T>(load_chunk<T, VEC>(sr, k * kE, h), k * kE, h, m, ss);
   ss = team_reduce<kLongTeam, false>(ss, buf[1]);
   const float rstd = 1.0f / sqrtf(ss * inv_h + eps);
   if (threadIdx.x == 0) {
@@ -177,10 +205,10 @@ __global__ __launch_bounds__(kLongTeam) void layer_norm_long_kernel(
     if (rstd_out) rstd_out[r] = rstd;
   }
   for (int64_t k = threadIdx.x; k * kE < h; k += kLongTeam) {
-    const Raw<T> s = load_raw<T, VEC>(sr, k * kE, h), w = load_raw<T, VEC>(weight, k * kE, h);
+    const Raw<T> s = load_chunk<T, VEC>(sr, k * kE, h), w = load_chunk<T, VEC>(weight, k * kE, h);
     Raw<T> b;
-    if (bias) b = load_raw<T, VEC>(bias, k * kE, h);
-    store_raw<T, VEC>(y + r * ld_y, k * kE, h, norm_chunk<T>(s, w, b, bias != nullptr, m, rstd));
+    if (bias) b = load_chunk<T, VEC>(bias, k * kE, h);
+    store_chunk<T, VEC>(y + r * ld_y, k * kE, h, norm_chunk<T>(s, w, b, bias != nullptr, m, rstd));
   }
 }
 
@@ -211,12 +239,12 @@ __device__ __forceinline__ void grad_store(const GradRows<T>& g, int64_t r, int6
                                            int64_t h, const Drop& drop, uint64_t seed,
                                            float (&d)[kE]) {
   if constexpr (DROP) {
-    if (g.dres) store_raw<T, VEC>(g.dres + r * g.ld_dres, chunk * kE, h, round_raw<T>(d));
+    if (g.dres) store_chunk<T, VEC>(g.dres + r * g.ld_dres, chunk * kE, h, round_raw<T>(d));
     const uint4 u = drop_chunk(drop, seed, r, static_cast<uint32_t>(chunk));
 #pragma unroll
     for (int e = 0; e < kE; ++e) d[e] = drop_keeps(drop, u, e) ? d[e] * drop.factor : 0.0f;
   }
-  store_raw<T, VEC>(g.dx + r * g.ld_dx, chunk * kE, h, round_raw<T>(d));
+  store_chunk<T, VEC>(g.dx + r * g.ld_dx, chunk * kE, h, round_raw<T>(d));
 }
 
 // d of one chunk, in place of dy.
@@ -258,18 +286,30 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void layer_norm_bwd_kernel
     for (int e = 0; e < kE; ++e) accw[c][e] = accb[c][e] = 0.0f;
   Raw<T> w[CH];
 #pragma unroll
-  for (int c = 0; c < CH; ++c) w[c] = load_raw<T, VEC>(g.weight, (c * TEAM + t) * kE, h);
+  for (int c = 0; c < CH; ++c) w[c] = load_chunk<T, VEC>(g.weight, (c * TEAM + t) * kE, h);
+  // The next row's loads are on their way while this one's sums go round.
+  Raw<T> s[CH], dy[CH], ds[CH];
+  float m = 0.0f, rs = 0.0f;
+  auto load = [&](int64_t r, Raw<T> (&a)[CH], Raw<T> (&b)[CH], Raw<T> (&c)[CH]) {
+#pragma unroll
+    for (int k = 0; k < CH; ++k) {
+      const int64_t c0 = (k * TEAM + t) * kE;
+      a[k] = load_chunk<T, VEC>(g.s + r * g.ld_s, c0, h);
+      b[k] = load_chunk<T, VEC>(g.dy + r * g.ld_dy, c0, h);
+      if (g.ds) c[k] = load_chunk<T, VEC>(g.ds + r * g.ld_ds, c0, h);
+    }
+  };
+  if (p < n) {
+    load(p, s, dy, ds);
+    m = g.mean[p];
+    rs = g.rstd[p];
+  }
   int turn = 0;
   for (int64_t r = p; r < n; r += teams, turn ^= 1) {
-    Raw<T> s[CH], dy[CH], ds[CH];
-    const float m = g.mean[r], rs = g.rstd[r];
-#pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const int64_t c0 = (c * TEAM + t) * kE;
-      s[c] = load_raw<T, VEC>(g.s + r * g.ld_s, c0, h);
-      dy[c] = load_raw<T, VEC>(g.dy + r * g.ld_dy, c0, h);
-      if (g.ds) ds[c] = load_raw<T, VEC>(g.ds + r * g.ld_ds, c0, h);
-    }
+    Raw<T> s2[CH], dy2[CH], ds2[CH];
+    const int64_t next = r + teams < n ? r + teams : r;
+    load(next, s2, dy2, ds2);
+    const float m2 = g.mean[next], rs2 = g.rstd[next];
     float sum_g = 0.0f, sum_gu = 0.0f;
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
@@ -295,6 +335,14 @@ __global__ __launch_bounds__(TEAM < 256 ? 256 : TEAM) void layer_norm_bwd_kernel
       grad_chunk<T>(s[c], dy[c], w[c], ds[c], g.ds != nullptr, m, rs, mean_g, mean_gu, d);
       grad_store<T, VEC, DROP>(g, r, c * TEAM + t, h, drop, seed, d);
     }
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      s[c] = s2[c];
+      dy[c] = dy2[c];
+      ds[c] = ds2[c];
+    }
+    m = m2;
+    rs = rs2;
   }
   if (!partial) return;
   float* out = partial + p * 2 * h;
@@ -321,9 +369,9 @@ __global__ __launch_bounds__(kLongTeam) void layer_norm_bwd_long_kernel(GradRows
   float sum_g = 0.0f, sum_gu = 0.0f;
   for (int64_t k = threadIdx.x; k * kE < h; k += kLongTeam) {
     float sv[kE], gv[kE], wv[kE];
-    widen_raw<T>(load_raw<T, VEC>(g.s + r * g.ld_s, k * kE, h), sv);
-    widen_raw<T>(load_raw<T, VEC>(g.dy + r * g.ld_dy, k * kE, h), gv);
-    widen_raw<T>(load_raw<T, VEC>(g.weight, k * kE, h), wv);
+    widen_raw<T>(load_chunk<T, VEC>(g.s + r * g.ld_s, k * kE, h), sv);
+    widen_raw<T>(load_chunk<T, VEC>(g.dy + r * g.ld_dy, k * kE, h), gv);
+    widen_raw<T>(load_chunk<T, VEC>(g.weight, k * kE, h), wv);
 #pragma unroll
     for (int e = 0; e < kE; ++e) {
       const float gw = gv[e] * wv[e];
@@ -334,11 +382,11 @@ __global__ __launch_bounds__(kLongTeam) void layer_norm_bwd_long_kernel(GradRows
   const float mean_g = team_reduce<kLongTeam, false>(sum_g, buf[0]) * inv_h;
   const float mean_gu = team_reduce<kLongTeam, false>(sum_gu, buf[1]) * inv_h;
   for (int64_t k = threadIdx.x; k * kE < h; k += kLongTeam) {
-    const Raw<T> s = load_raw<T, VEC>(g.s + r * g.ld_s, k * kE, h);
-    const Raw<T> dy = load_raw<T, VEC>(g.dy + r * g.ld_dy, k * kE, h);
-    const Raw<T> w = load_raw<T, VEC>(g.weight, k * kE, h);
+    const Raw<T> s = load_chunk<T, VEC>(g.s + r * g.ld_s, k * kE, h);
+    const Raw<T> dy = load_chunk<T, VEC>(g.dy + r * g.ld_dy, k * kE, h);
+    const Raw<T> w = load_chunk<T, VEC>(g.weight, k * kE, h);
     Raw<T> ds;
-    if (g.ds) ds = load_raw<T, VEC>(g.ds + r * g.ld_ds, k * kE, h);
+    if (g.ds) ds = load_chunk<T, VEC>(g.ds + r * g.ld_ds, k * kE, h);
     float d[kE];
     grad_chunk<T>(s, dy, w, ds, g.ds != nullptr, m, rs, mean_g, mean_gu, d);
     grad_store<T, VEC, DROP>(g, r, k, h, drop, seed, d);
@@ -356,8 +404,8 @@ __global__ __launch_bounds__(256) void layer_norm_columns_kernel(GradRows<T> g, 
   float accw[kE] = {}, accb[kE] = {};
   for (int64_t r = blockIdx.y; r < n; r += teams) {
     float sv[kE], gv[kE];
-    widen_raw<T>(load_raw<T, VEC>(g.s + r * g.ld_s, c0, h), sv);
-    widen_raw<T>(load_raw<T, VEC>(g.dy + r * g.ld_dy, c0, h), gv);
+    widen_raw<T>(load_chunk<T, VEC>(g.s + r * g.ld_s, c0, h), sv);
+    widen_raw<T>(load_chunk<T, VEC>(g.dy + r * g.ld_dy, c0, h), gv);
     const float m = g.mean[r], rs = g.rstd[r];
 #pragma unroll
     for (int e = 0; e < kE; ++e) {
@@ -416,7 +464,9 @@ template <typename T>
 Shape fwd_shape(int64_t h) {
   return layer_shape(h, 1024, h > 8192 && sizeof(T) == 4 ? 2 : 4);
 }
-Shape bwd_shape(int64_t h) { return layer_shape(h, 512, h > 8192 ? 3 : 4); }
+Shape bwd_shape(int size, int64_t h) {
+  return layer_shape(h, 512, h <= 8192 ? 4 : size == 4 ? 0 : 3);
+}
 
 template <typename T>
 void layer_norm_typed(const NormRows& rows, const Drop* drop, const void* weight, const void* bias,
@@ -426,7 +476,7 @@ void layer_norm_typed(const NormRows& rows, const Drop* drop, const void* weight
   const int size = sizeof(T);
   const bool vec = fits16(rows.x, rows.ld_x, size) && fits16(rows.residual, rows.ld_r, size) &&
                    fits16(rows.sum, rows.ld_s, size) && fits16(weight, 8, size) &&
-                   fits16(bias, 8, size) && fits16(y, ld_y, size);
+                   fits16(bias, 8, size) && fits16(y, ld_y, size) && h % kE == 0;
   const float inv_h = static_cast<float>(1.0 / static_cast<double>(h));
   const T* x = static_cast<const T*>(rows.x);
   const T* residual = static_cast<const T*>(rows.residual);
@@ -467,18 +517,18 @@ void layer_norm_typed(const NormRows& rows, const Drop* drop, const void* weight
 template <typename T>
 void layer_norm_bwd_typed(const LayerNormGrad& a, int64_t n, int64_t h, float* partial,
                           hipStream_t s) {
-  const Shape sh = bwd_shape(h);
   const int size = sizeof(T);
+  const Shape sh = bwd_shape(size, h);
   const bool vec = fits16(a.s, a.ld_s, size) && fits16(a.dy, a.ld_dy, size) &&
                    fits16(a.ds, a.ld_ds, size) && fits16(a.dx, a.ld_dx, size) &&
-                   fits16(a.dres, a.ld_dres, size) && fits16(a.weight, 8, size);
+                   fits16(a.dres, a.ld_dres, size) && fits16(a.weight, 8, size) && h % kE == 0;
   const float inv_h = static_cast<float>(1.0 / static_cast<double>(h));
   const GradRows<T> g{static_cast<const T*>(a.s), a.ld_s, static_cast<const T*>(a.weight), a.mean,
                       a.rstd, static_cast<const T*>(a.dy), a.ld_dy, static_cast<const T*>(a.ds),
                       a.ld_ds, static_cast<T*>(a.dx), a.ld_dx, static_cast<T*>(a.dres), a.ld_dres};
   const Drop drop = a.drop ? *a.drop : Drop{};
   const bool sums = a.dweight || a.dbias;
-  const int64_t teams = n ? layer_norm_bwd_blocks(n, h) : 0;
+  const int64_t teams = n ? layer_norm_bwd_blocks(size == 4 ? kF32 : kBF16, n, h) : 0;
   if (n && sh.ch == 0) {
     if (sums)
       hipLaunchKernelGGL((vec ? layer_norm_columns_kernel<T, true>
@@ -516,7 +566,10 @@ void layer_norm_bwd_typed(const LayerNormGrad& a, int64_t n, int64_t h, float* p
   } break;
     switch (sh.team * 16 + sh.ch) {
       ITL_GO(64, 1) ITL_GO(64, 2) ITL_GO(256, 1) ITL_GO(256, 2) ITL_GO(256, 3) ITL_GO(256, 4)
-      ITL_GO(512, 3)
+      default:
+        if constexpr (sizeof(T) == 2) {
+          switch (sh.team * 16 + sh.ch) { ITL_GO(512, 3) }
+        }
     }
 #undef ITL_GO
   }
@@ -529,10 +582,17 @@ void layer_norm_bwd_typed(const LayerNormGrad& a, int64_t n, int64_t h, float* p
 
 }  // namespace
 
-int64_t layer_norm_bwd_blocks(int64_t n, int64_t h) {
-  const Shape sh = bwd_shape(h);
-  // Eight waves a CU; for the column kernel as many over its column blocks.
-  const int64_t most = sh.ch ? 256 * 8 / (sh.team / kWave) : 512 * 2048 / ((h + 2047) / 2048 * 2048);
+int64_t layer_norm_bwd_blocks(int dtype, int64_t n, int64_t h) {
+  const Shape sh = bwd_shape(dtype == kF32 ? 4 : 2, h);
+  // Eight waves a CU where the registers allow them (a team of 256 holding at
+  // most 32 bytes a lane of each row), else four: fewer partial rows.  bf16, us
+  // with the sum over the rows, eight against four: 8192 x 4096 72 (93), 4096 x
+  // 8192 93 (64), 8192 x 1024 36 (30); fp32 4096 x 4096 73 (71).  For the column
+  // kernel as many over its column blocks.
+  const int size = dtype == kF32 ? 4 : 2;
+  const int waves = sh.team == 512 || (sh.team == 256 && sh.ch * size <= 4) ? 8 : 4;
+  const int64_t most = sh.ch ? 256 * waves / (sh.team / kWave)
+                             : 512 * 2048 / ((h + 2047) / 2048 * 2048);
   return n < most ? n : most;
 }
 
