@@ -11,8 +11,8 @@
 // a token form a run in ascending position, and sums every run in fp32:
 //   1. embed_sort_kernel: tiles of 2048 tokens, a workgroup each, a bitonic
 //      network in registers, lane moves and LDS (no order-dependent atomics, so
-//      the same bits every time).  More than one tile: embed_rank_kernel places
-//      every token by binary searches in the other tiles.
+//      the same bits every time).  More than one tile: embed_merge_kernel merges
+//      eight at a time, placing every token by binary searches in the others.
 //   2. embed_sum_kernel: a wave for every piece of 32 occurrences; a run of one
 //      piece goes straight to the table, a longer one leaves a partial row a
 //      piece.
@@ -21,7 +21,7 @@
 // A row of the gradient depends on its token's own occurrences and their
 // order, not on the batch around them.
 // Without accumulation the rows of absent tokens are written with zeros, which
-// with a large vocabulary is most of the work: beside the sort and the ranking
+// with a large vocabulary is most of the work: beside the sort and the last merge
 // workgroups clear the table's first rows whole, beside the sums the absent
 // rows of the rest.
 #include "embedding.h"
@@ -201,7 +201,7 @@ __device__ __forceinline__ void clear_rows(const Clear& c, int threads) {
 
 // Tile blockIdx.x of the tokens.  Keys are (token, position in the tile), the
 // token of an entry that is left out being v.  One tile: the sorted arrays; more:
-// the tile's sorted keys (token << 32 | position) for embed_rank_kernel.
+// the tile's sorted keys (token << 32 | position) for embed_merge_kernel.
 // SMALL: v < 2^20 - 1, so that a key fits 32 bits.
 template <bool SMALL>
 __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(
@@ -256,33 +256,38 @@ __global__ __launch_bounds__(kSortThreads) void embed_sort_kernel(
   }
 }
 
-// The place of every key among all tiles': eight lanes a key, each searching every
-// eighth tile for the key and for its token's first.  (Keys are distinct, so
-// the number of smaller ones is the place.)
-constexpr int kRankLanes = 8, kRankKeys = 256 / kRankLanes;
+// Merges groups of eight sorted runs of `width` keys: eight lanes a key, each
+// searching one run of the group for it.  (Keys are distinct, so the number of
+// smaller ones is the place.)  LAST, one group: the sorted arrays, a token's
+// first key searched for too.
+constexpr int kFan = 8, kRankKeys = 256 / kFan;
 
-__global__ __launch_bounds__(256) void embed_rank_kernel(const uint64_t* __restrict__ tiles,
-                                                         int64_t n, Sorted out, Clear clear) {
+template <bool LAST>
+__global__ __launch_bounds__(256) void embed_merge_kernel(const uint64_t* __restrict__ runs,
+                                                          int64_t n, int64_t width,
+                                                          uint64_t* __restrict__ to, Sorted out,
+                                                          Clear clear) {
   if (static_cast<int>(blockIdx.x) >= clear.first) return clear_rows(clear, 256);
-  const int sub = threadIdx.x % kRankLanes;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kRankKeys + threadIdx.x / kRankLanes;
-  const uint64_t key = tiles[i < n ? i : n - 1], first = key >> 32 << 32;
+  const int sub = threadIdx.x % kFan;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kRankKeys + threadIdx.x / kFan;
+  const uint64_t key = runs[i < n ? i : n - 1], first = key >> 32 << 32;
+  const int64_t base = (i < n ? i : n - 1) / (kFan * width) * (kFan * width);
+  const int64_t b = base + sub * width;
   uint32_t rank = 0, start = 0;
-  for (int64_t b = static_cast<int64_t>(sub) * kTile; b < n; b += kRankLanes * kTile) {
-    const int count = static_cast<int>(n - b < kTile ? n - b : kTile);
-    const uint64_t* t = tiles + b;
-    int at = 0, from = 0;
-#pragma unroll
-    for (int step = kTile / 2; step; step /= 2) {  // kTile - 1 keys at most
-      const int x = at + step - 1, y = from + step - 1;
-      const uint64_t kx = t[min(x, count - 1)], ky = t[min(y, count - 1)];
-      if (x < count && kx < key) at += step;
-      if (y < count && ky < first) from += step;
+  if (b < n) {
+    const uint32_t count = static_cast<uint32_t>(n - b < width ? n - b : width);
+    const uint64_t* t = runs + b;
+    for (uint32_t step = static_cast<uint32_t>(width) / 2; step; step /= 2) {  // width - 1 at most
+      const uint32_t x = rank + step - 1, y = start + step - 1;
+      const uint64_t kx = t[min(x, count - 1)], ky = LAST ? t[min(y, count - 1)] : 0;
+      if (x < count && kx < key) rank += step;
+      if (LAST && y < count && ky < first) start += step;
     }
-    if (at == kTile - 1 && count == kTile && t[kTile - 1] < key) ++at;  // all of a whole tile
-    if (from == kTile - 1 && count == kTile && t[kTile - 1] < first) ++from;
-    rank += at;
-    start += from;
+    if (count == width) {  // all of a whole run
+      const uint64_t k = t[width - 1];
+      if (rank == width - 1 && k < key) ++rank;
+      if (LAST && start == width - 1 && k < first) ++start;
+    }
   }
 #define ITL_ADD(O)                  \
   rank += lane_xor<O>(rank);        \
@@ -290,9 +295,13 @@ __global__ __launch_bounds__(256) void embed_rank_kernel(const uint64_t* __restr
   ITL_ADD(1) ITL_ADD(2) ITL_ADD(4)
 #undef ITL_ADD
   if (sub || i >= n) return;
-  out.id[rank] = static_cast<uint32_t>(key >> 32);
-  out.pos[rank] = static_cast<uint32_t>(key);
-  out.start[rank] = start;
+  if constexpr (LAST) {
+    out.id[rank] = static_cast<uint32_t>(key >> 32);
+    out.pos[rank] = static_cast<uint32_t>(key);
+    out.start[rank] = start;
+  } else {
+    to[base + rank] = key;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -521,10 +530,10 @@ __global__ __launch_bounds__(256) void embed_join_kernel(const float* __restrict
   }
 }
 
-// Workspace: id, pos, start [n]; the tiles' keys when there are several; the
-// partial rows.
+// Workspace: id, pos, start [n]; the tiles' keys when there are several, twice
+// when they are merged more than once; the partial rows.
 struct BwdLayout {
-  int64_t id, pos, start, tiles, partial, ld_p, total;
+  int64_t id, pos, start, tiles, tiles2, partial, ld_p, total;
 };
 BwdLayout bwd_layout(int64_t n, int64_t h) {
   auto round = [](int64_t x) { return (x + 255) / 256 * 256; };
@@ -534,14 +543,15 @@ BwdLayout bwd_layout(int64_t n, int64_t h) {
   l.pos = round(4 * n);
   l.start = 2 * l.pos;
   l.tiles = 3 * l.pos;
-  l.partial = l.tiles + (n > kTile ? round(8 * n) : 0);
+  l.tiles2 = l.tiles + (n > kTile ? round(8 * n) : 0);
+  l.partial = l.tiles2 + (n > kFan * kTile ? round(8 * n) : 0);
   // runs of several pieces need more than kPiece tokens
   const int64_t rows = n > kPiece ? 2 * ((n + kPiece - 1) / kPiece) : 0;
   l.total = l.partial + round(rows * l.ld_p * 4);
   return l;
 }
 
-// Bytes that workgroups beside the sort, and beside the ranking, clear: what
+// Bytes that workgroups beside the sort, and beside the last merge, clear: what
 // the memory takes in their time (7 us and 6).
 constexpr int64_t kSortClears = int64_t{40} << 20, kRankClears = int64_t{32} << 20;
 
@@ -580,9 +590,19 @@ void bwd_typed(const void* dy, int64_t ld_y, Targets tokens, int64_t n, int64_t 
   }
   if (tiles) {
     const unsigned groups = static_cast<unsigned>((n + kRankKeys - 1) / kRankKeys);
+    uint64_t* other = reinterpret_cast<uint64_t*>(ws + l.tiles2);
+    int64_t width = kTile;
+    for (; kFan * width < n; width *= kFan) {
+      clear.first = static_cast<int>(groups);
+      hipLaunchKernelGGL(embed_merge_kernel<false>, dim3(groups), dim3(256), 0, s, tiles, n, width,
+                         other, sorted, clear);
+      uint64_t* t = tiles;
+      tiles = other;
+      other = t;
+    }
     const unsigned more = clears(kRankClears, static_cast<int>(groups));
-    hipLaunchKernelGGL(embed_rank_kernel, dim3(groups + more), dim3(256), 0, s, tiles, n, sorted,
-                       clear);
+    hipLaunchKernelGGL(embed_merge_kernel<true>, dim3(groups + more), dim3(256), 0, s, tiles, n,
+                       width, other, sorted, clear);
   }
   const bool vec = vec_out && fits16(dy, ld_y, sizeof(T)) && h % kE == 0;
   constexpr int CH = sizeof(T) == 4 ? 1 : 2;  // 32 bytes a lane and row

@@ -78,7 +78,8 @@ def draw_ids(n, v, kind, gen):
 
 CASES = [(1, 1, "one"), (1, 50, "one"), (3, 5, "text"), (32, 4, "one"), (33, 4, "one"), (64, 100, "once"),
          (527, 40, "runs"), (1000, 333, "text"), (2047, 90, "text"), (2048, 700, "once"), (2049, 5, "text"), (4095, 1000, "text"), (4096, 7, "one"), (4097, 300, "text"),
-         (8200, 64, "runs"), (9000, 20000, "once"), (500, 1500000, "text"), (12289, 3, "text"), (20000, 1500000, "text"), (70000, 400, "text")]
+         (8200, 64, "runs"), (9000, 20000, "once"), (500, 1500000, "text"), (12289, 3, "text"), (20000, 1500000, "text"), (16384, 900, "once"), (16385, 900, "text"),
+         (70000, 400, "text"), (131073, 2000, "text"), (270000, 50, "runs")]
 
 
 @pytest.mark.parametrize("n,v,kind", CASES)

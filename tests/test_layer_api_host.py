@@ -199,3 +199,12 @@ def test_head_binding():
         itl.linear_token_logp_fwd(itl.QuantizedRows(x.to(torch.float8_e4m3fn), torch.ones(4)), q)
     with pytest.raises(ValueError, match="ROCm device"):
         itl.linear_token_logp_fwd(x, q)
+
+
+def test_embedding_gradient_workspace_of_long_batches(L):
+    """Past eight tiles of 2048 tokens the keys are merged twice, in two buffers."""
+    def keys(n):
+        return L.embedding_bwd_workspace_bytes(n, 100, 8) - 3 * ((4 * n + 255) // 256 * 256) - \
+            (2 * ((n + 31) // 32) * 32 + 255) // 256 * 256
+
+    assert keys(2048) == 0 and keys(2304) == 8 * 2304 and keys(16384) == 8 * 16384 and keys(16640) == 16 * 16640
