@@ -263,12 +263,15 @@ __device__ __forceinline__ void store_logits_staged(const f32x4 (&acc)[MI][NJ], 
   }
 }
 
+// (ex by value: taken by reference it was kept in memory, which the compiler puts
+// into 16 bytes of LDS a thread and finds by reading the dispatch packet: up to
+// 13 us a launch.)
 template <int MI, int NJ, int BM, int NT, int SCRATCH>
 __device__ __forceinline__ void stats_epilogue(f32x4 (&acc)[MI][NJ], Reduce<BM>& rd, void* scratch,
                                                int row0, int col0, int li, int g, int tid,
                                                int64_t m0, int64_t v0, int vb, int vblocks,
                                                int64_t n, int64_t v, float* pm, float* ps,
-                                               float* pt, const LinearExtras& ex) {
+                                               float* pt, LinearExtras ex) {
   // The bf16-rounded variant: z becomes RNE_bf16(accumulator), widened
   // exactly, before anything reads it (logits output, temperature, every
   // statistic and the target copy).
