@@ -100,7 +100,8 @@ int32_t dropout_fwd(const void* x, int64_t ld_x, const void* residual, int64_t l
  *   m = mean(s), rstd = 1 / sqrt(mean((s - m)^2) + eps)
  * The stored s is what is normed, so the fused call has the bits of dropout_fwd
  * followed by the norm of its output.  Sums in fp32 through a tree fixed by h
- * alone.
+ * alone; squares past fp32's range (differences from the mean of about 1e19)
+ * give rstd 0, a sum past it a row of NaN.
  *   x [n, ld_x], residual [n, ld_r] (NULL: none), weight [h], bias [h] (NULL:
  *   none), y [n, ld_y], sum_out [n, ld_s] (NULL only where s is x): dtype, any
  *   alignment.  sum_out may be exactly x or residual, y exactly x when sum_out

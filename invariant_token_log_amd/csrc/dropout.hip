@@ -36,7 +36,8 @@ __global__ __launch_bounds__(256) void dropout_kernel(const T* x, int64_t ld_x, 
   if (residual) {
     widen_raw<T>(b, q);
 #pragma unroll
-    for (int e = 0; e < kE; ++e) p[e] = drop_keeps(drop, u, e) ? fmaf(p[e], drop.factor, q[e]) : q[e];
+    for (int e = 0; e < kE; ++e)
+      p[e] = drop_keeps(drop, u, e) ? fmaf(p[e], drop.factor, q[e]) : q[e];
   } else {
 #pragma unroll
     for (int e = 0; e < kE; ++e) p[e] = drop_keeps(drop, u, e) ? p[e] * drop.factor : 0.0f;

@@ -189,7 +189,8 @@ struct Clear {
   int first, step;
 };
 __device__ __forceinline__ void clear_rows(const Clear& c, int threads) {
-  const int64_t r0 = c.begin + static_cast<int64_t>(static_cast<int>(blockIdx.x) - c.first) * c.step;
+  const int64_t block = static_cast<int>(blockIdx.x) - c.first;
+  const int64_t r0 = c.begin + block * c.step;
   const int64_t r1 = min(r0 + c.step, c.end);
   if (c.ld == c.row_bytes) {
     zero_bytes(c.table + r0 * c.ld, (r1 - r0) * c.ld, threadIdx.x, threads);
@@ -700,8 +701,9 @@ void launch_embedding_bwd(int dtype, const void* dy, int64_t ld_y, Targets token
                           int64_t v, int64_t h, int64_t ignore, float scale, bool f32_out,
                           bool accumulate, void* dtable, int64_t ld_t, char* ws, hipStream_t s) {
   auto run = dtype == kF32   ? bwd_typed<float, float>
-             : dtype == kF16 ? (f32_out ? bwd_typed<_Float16, float> : bwd_typed<_Float16, _Float16>)
-                             : (f32_out ? bwd_typed<uint16_t, float> : bwd_typed<uint16_t, uint16_t>);
+             : dtype == kF16 ? f32_out ? bwd_typed<_Float16, float> : bwd_typed<_Float16, _Float16>
+             : f32_out       ? bwd_typed<uint16_t, float>
+                             : bwd_typed<uint16_t, uint16_t>;
   run(dy, ld_y, tokens, n, v, h, ignore, scale, accumulate, dtable, ld_t, ws, s);
 }
 

@@ -404,8 +404,8 @@ __global__ __launch_bounds__(kThreads4) void linear_fp4_narrow(
     LinearExtras ex) {
   __shared__ __align__(16) SmemFp4<ROWS> sm;
   fp4_tiles<ROWS, ALIGNED>(sm, hidden, ld_h, data, ld_d, scales, ld_s, n, v, ksteps, mblocks,
-                           vblocks, Targets{tgt, tgt32}, ignore, pm, ps, pt, ex.inv_t, ex.round_bf16, ex.pw,
-                           ex.z, ex.z_bf16, ex.ld_z, ex.z_vec);
+                           vblocks, Targets{tgt, tgt32}, ignore, pm, ps, pt, ex.inv_t,
+                           ex.round_bf16, ex.pw, ex.z, ex.z_bf16, ex.ld_z, ex.z_vec);
 }
 
 // Lane t of a quad gives a[i] to lane i and takes that lane's a[t] for it.
@@ -415,8 +415,12 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&a)[4], int t) {
     x = high ? got : x;
     y = high ? y : got;
   };
-  auto by1 = [](uint32_t x) { return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), kDppXor1, 0xF, 0xF, true)); };
-  auto by2 = [](uint32_t x) { return static_cast<uint32_t>(__builtin_amdgcn_mov_dpp(static_cast<int>(x), kDppXor2, 0xF, 0xF, true)); };
+  auto by1 = [](uint32_t x) -> uint32_t {
+    return __builtin_amdgcn_mov_dpp(static_cast<int>(x), kDppXor1, 0xF, 0xF, true);
+  };
+  auto by2 = [](uint32_t x) -> uint32_t {
+    return __builtin_amdgcn_mov_dpp(static_cast<int>(x), kDppXor2, 0xF, 0xF, true);
+  };
   swap(a[0], a[1], t & 1, by1);
   swap(a[2], a[3], t & 1, by1);
   swap(a[0], a[2], t & 2, by2);
@@ -439,7 +443,8 @@ __global__ __launch_bounds__(256) void fp4_decode_kernel(const uint8_t* __restri
                                                          uint16_t* __restrict__ out) {
   const int lane = threadIdx.x % kWave, t = lane % 4;
   const int64_t block = first + blockIdx.x / parts;
-  const int k0 = (static_cast<int>(blockIdx.x % parts) * 4 + static_cast<int>(threadIdx.x) / kWave) * 8;
+  const int wave = threadIdx.x / kWave;
+  const int k0 = (static_cast<int>(blockIdx.x % parts) * 4 + wave) * 8;
   if (k0 >= ksteps) return;
   const int64_t row = block * 16 + lane / 4;
   const bool live = row < v;

@@ -130,6 +130,14 @@ def _seed(seed, device):
     return value - 2 ** 64 if value >= 2 ** 63 else value, None
 
 
+def _place(draw, first_row):
+    """(draw, first_row) as the library's integers hold them."""
+    draw, first_row = int(draw), int(first_row)
+    if draw >> 32 or first_row >> 63:
+        raise ValueError("draw must be in [0, 2^32) and first_row in [0, 2^63)")
+    return draw, first_row
+
+
 def dropout_fwd(x, p, seed, residual=None, draw=0, first_row=0, out=None):
     """residual + dropped(x) (dropped(x) without a residual), rounded once to x's
     dtype: an element of x [*lead, H] (float32, bfloat16, float16) is dropped with
@@ -142,8 +150,8 @@ def dropout_fwd(x, p, seed, residual=None, draw=0, first_row=0, out=None):
         pr, _, _, ld_r = _norm_rows(residual, "residual", x)
     out, po, ld_o = _norm_out(out, "out", x, h)
     value, at = _seed(seed, x.device)
-    _call("dropout_fwd", x.device, px, ld_x, pr, ld_r, code, n, h, float(p), value, at, int(draw),
-          int(first_row), po, ld_o)
+    _call("dropout_fwd", x.device, px, ld_x, pr, ld_r, code, n, h, float(p), value, at,
+          *_place(draw, first_row), po, ld_o)
     return out
 
 
@@ -187,7 +195,7 @@ def _drop_args(p, seed, draw, first_row, device):
         return 0.0, 0, None, 0, 0
     if seed is None:
         raise ValueError("dropout needs a seed")
-    return (float(p), *_seed(seed, device), int(draw), int(first_row))
+    return (float(p), *_seed(seed, device), *_place(draw, first_row))
 
 
 def _layer_norm_forward(x, weight, bias, residual, eps, drop, stats, y_out, sum_out):
@@ -301,13 +309,14 @@ class _LayerNorm(torch.autograd.Function):
             dx = gs
             if p and need_x and gs is not None:
                 dx = dropout_bwd(gs, p, seed, draw, first_row)
-            zero = torch.zeros_like(weight) if need_w or need_b else None
-            return (dx, zero if need_w else None, zero if need_b else None, gs, None, None, None,
-                    None, None)
+            dw = torch.zeros_like(weight) if need_w else None
+            db = torch.zeros_like(weight) if need_b else None
+            return dx, dw, db, gs, None, None, None, None, None
         pm = stats.data_ptr()
         dx, dres, dw, db = _layer_norm_backward(
             s, weight, pm, pm + 2 * stats.numel(), gy.contiguous(), gs,
-            _drop_args(p, seed, draw, first_row, s.device), need_r, need_w, need_b, None, None, None)
+            _drop_args(p, seed, draw, first_row, s.device), need_r, need_w, need_b, None, None,
+            None)
         return dx, dw, db, dres, None, None, None, None, None
 
 

@@ -644,8 +644,9 @@ def norm_linear_token_logp(x, norm_weight, weight, token_ids=None, residual=None
     differentiable in x, residual, norm_weight and weight (rms_norm, then
     linear_token_logp); with a QuantizedRows weight the normed rows are
     quantised in the norm and the 8-bit head scores them, with Fp4Rows the 4-bit
-    head scores them as they are (no gradient through either).  The gradient of norm_weight sums over all rows, padding rows (whose part is 0)
-    included: they must be finite for it."""
+    head scores them as they are (no gradient through either).  The gradient of
+    norm_weight sums over all rows, padding rows (whose part is 0) included: they
+    must be finite for it."""
     if isinstance(weight, (QuantizedRows, Fp4Rows)):
         fp4 = isinstance(weight, Fp4Rows)
         bits = 4 if fp4 else 8

@@ -170,3 +170,34 @@ def test_graph_draws_anew():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, itl.dropout_fwd(x, 0.3, SEED + k))
+
+
+@pytest.mark.parametrize("place", [dict(draw=-1), dict(draw=2 ** 32), dict(draw=2 ** 64), dict(first_row=-1),
+                                   dict(first_row=2 ** 63), dict(first_row=2 ** 64 + 1)])
+def test_refused_places(place):
+    """Numbers past the generator's counter, and those a 64-bit integer would wrap."""
+    x = torch.ones(2, 64, device=dev())
+    with pytest.raises(ValueError, match="draw must be"):
+        itl.dropout(x, 0.5, SEED, **place)
+    with pytest.raises(ValueError, match="draw must be"):
+        itl.layer_norm(x, x[0], dropout=0.5, seed=SEED, **place)
+
+
+def test_last_places():
+    """The last draw, and rows past 2^32: a part of a batch is numbered as the whole."""
+    x = torch.ones(4, 64, device=dev())
+    y = itl.dropout_fwd(x, 0.5, SEED, draw=2 ** 32 - 1, first_row=2 ** 32 - 2)
+    assert torch.equal(y.cpu(), dropped(x.cpu(), 0.5, SEED, 2 ** 32 - 1, 2 ** 32 - 2).float())
+    assert torch.equal(y[2:], itl.dropout_fwd(x[2:], 0.5, SEED, draw=2 ** 32 - 1, first_row=2 ** 32))
+
+
+def test_widest_rows():
+    """Rows of 2^24 elements, the most: the ends are as the same columns' of the plain form."""
+    h = 2 ** 24
+    x = torch.ones(1, h, dtype=torch.bfloat16, device=dev())
+    y = itl.dropout_fwd(x, 0.25, SEED)
+    again = itl.dropout_fwd(x[:, :4096].contiguous(), 0.25, SEED)
+    assert torch.equal(y[:, :4096], again) and int((y != 0).sum()) + int((y == 0).sum()) == h
+    assert abs(float((y == 0).float().mean()) - 0.25) < 6 * (0.1875 / h) ** 0.5
+    with pytest.raises(RuntimeError):
+        itl.dropout_fwd(torch.empty(1, h + 8, dtype=torch.bfloat16, device=dev()), 0.25, SEED)

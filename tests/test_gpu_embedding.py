@@ -228,3 +228,16 @@ def test_lookup_fp4(h, out_dtype):
     rows = itl.Fp4Rows(wide[:, :h // 2], torch.cat([q.scale, q.scale], 1)[:, :h // 32])
     again = itl.embedding_fwd(ids.int().to(dev()), rows, scale=1.3, out_dtype=TYPES[out_dtype])
     assert torch.equal(again.nan_to_num(9.0), y.nan_to_num(9.0))
+
+
+def test_widest_rows():
+    """Rows of 2^24 elements, the most, with a token of two pieces, one of one and one absent."""
+    h, n = 2 ** 24, 34
+    dy = torch.zeros(n, h, dtype=torch.bfloat16, device=dev())
+    dy[:, 0], dy[:, h - 1], dy[:, h // 2 + 3] = 0.5, 1.0, 2.0
+    ids = torch.tensor([1] * 17 + [0] + [1] * 16, device=dev())
+    g = itl.embedding_bwd(ids, dy, 3)
+    for c, x in ((0, 0.5), (h - 1, 1.0), (h // 2 + 3, 2.0), (1, 0.0), (h - 2, 0.0)):
+        assert g[:, c].tolist() == [x, 33 * x, 0.0]
+    assert int(torch.count_nonzero(g)) == 6
+    assert torch.equal(itl.embedding_fwd(ids[16:18], g), g[[1, 0]])
