@@ -114,8 +114,6 @@ enum logp_token_flags {
  * most one given token a row, the chunk's logits (fp32, bf16 with
  * LOGP_TOKEN_ROUND_BF16), 2.5 GB for 4096 rows of 151936 columns.  row_chunk 0
  * takes 4096 rows where the chunk's logits are in the workspace, else 65536.
- * With LOGP_TOKEN_FP4 and more than 448 rows it also holds a bf16 copy of the
- * weight (v rounded up to a multiple of 256, times 2 h bytes).
  * Any row_chunk gives the same bits.  0 for arguments the call would reject.
  */
 size_t linear_token_logp_fwd_workspace_bytes(int64_t n, int64_t h, int64_t v, int64_t m,

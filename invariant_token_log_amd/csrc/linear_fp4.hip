@@ -9,7 +9,7 @@
 // values, and the sums and statistics are exactly those of linear_logp.hip: a
 // row has the bits of the bf16 head on the decoded weight.
 //
-// Few rows: bound by the weight's bytes, 17 / 32 of a byte a value.  A workgroup
+// Few rows (linear_fp4_narrow): bound by the weight's bytes, 17 / 32 of a byte a value.  A workgroup
 // takes tiles of 256 columns x ROWS hidden rows, eight waves of 32 columns x
 // ROWS rows, so that every weight is decoded once.  Slots of 256 K values hold
 // whole 128-byte lines of the weight's rows and the hidden rows' pieces, panels
@@ -22,6 +22,15 @@
 // CUs, the last 82 nearly alone), without the loads 52, 62 and 86.  Two to four
 // slots, whole or half lines, four waves a workgroup and three workgroups a CU
 // (81, 96, 153) made no difference or a worse one.
+//
+// Many rows (linear_fp4_wide): bound by the matrix cores.  Blocks of 256 hidden
+// rows x 256 columns like those of the bf16 head, the weight's codes in LDS in
+// place of its values (a quarter of the bytes to bring and to read) and decoded
+// beside the products of the step, 20 vector instructions to 32 products.  A wave
+// holds a step's hidden rows in two halves, one read while the other's products
+// run: whole steps ahead, as the bf16 head holds them, do not fit its registers
+// beside the decoding.  1000 rows: 840 to 890 us (1.4 to 1.48 PFLOP/s), what the
+// bf16 head takes on a decoded copy of the weight, whose making took 256 more.
 #include "linear_fp4.h"
 
 #include "fp4.h"
@@ -50,7 +59,7 @@ constexpr int kPanels = 3;  // those of slots p .. p + 2, each of which may begi
 template <int ROWS>
 constexpr int kEpiRows = ROWS < 32 ? 32 : ROWS;
 template <int ROWS>
-constexpr int kMostRows = ROWS == 64 ? static_cast<int>(kFp4Direct) : ROWS;
+constexpr int kMostRows = ROWS == 64 ? static_cast<int>(kFp4Narrow) : ROWS;
 
 template <int ROWS>
 struct Fp4Slot {
@@ -408,101 +417,238 @@ __global__ __launch_bounds__(kThreads4) void linear_fp4_narrow(
                            ex.round_bf16, ex.pw, ex.z, ex.z_bf16, ex.ld_z, ex.z_vec);
 }
 
-// Lane t of a quad gives a[i] to lane i and takes that lane's a[t] for it.
-__device__ __forceinline__ void quad_transpose(uint32_t (&a)[4], int t) {
-  auto swap = [&](uint32_t& x, uint32_t& y, bool high, auto partner) {
-    const uint32_t got = partner(high ? x : y);
-    x = high ? got : x;
-    y = high ? y : got;
-  };
-  auto by1 = [](uint32_t x) -> uint32_t {
-    return __builtin_amdgcn_mov_dpp(static_cast<int>(x), kDppXor1, 0xF, 0xF, true);
-  };
-  auto by2 = [](uint32_t x) -> uint32_t {
-    return __builtin_amdgcn_mov_dpp(static_cast<int>(x), kDppXor2, 0xF, 0xF, true);
-  };
-  swap(a[0], a[1], t & 1, by1);
-  swap(a[2], a[3], t & 1, by1);
-  swap(a[0], a[2], t & 2, by2);
-  swap(a[1], a[3], t & 2, by2);
-}
+// ---------------------------------------------------------------------------
+// Many rows: blocks of 256 hidden rows x 256 columns, eight waves of 128 x 64.
+// ---------------------------------------------------------------------------
+constexpr int kWideSteps = 4;                       // K steps a slot
+constexpr int kWideBytes = kWideSteps * BK / 2;     // of a weight row: 64
+constexpr int kWideSlots = 3;
 
-// The decoded copy: a wave takes 16 rows x 8 K steps (a line of codes a row),
-// reads pieces of a step and turns them in quads of lanes, so that a lane holds
-// its quarter of a row's every step and a wave's store is a whole block of 1 KiB.
-// K parts of a row block are neighbours in the grid.
-struct __attribute__((packed)) Scale8 {
-  uint32_t w[2];
+struct SmemFp4Wide {
+  uint16_t a[kWideSteps][256 * BK];         // a K step's hidden rows each
+  uint8_t w[kWideSlots][BN * kWideBytes];
+  uint32_t scale[kWideSlots][BN];
+  Reduce<256> rd;
+  int slot;  // tile-queue broadcast
 };
+constexpr int kWideScratch = sizeof(SmemFp4Wide::a) + sizeof(SmemFp4Wide::w);
 
-__global__ __launch_bounds__(256) void fp4_decode_kernel(const uint8_t* __restrict__ data,
-                                                         int64_t ld_d,
-                                                         const uint8_t* __restrict__ scales,
-                                                         int64_t ld_s, int64_t v, int ksteps,
-                                                         int parts, int64_t first,
-                                                         uint16_t* __restrict__ out) {
-  const int lane = threadIdx.x % kWave, t = lane % 4;
-  const int64_t block = first + blockIdx.x / parts;
-  const int wave = threadIdx.x / kWave;
-  const int k0 = (static_cast<int>(blockIdx.x % parts) * 4 + wave) * 8;
-  if (k0 >= ksteps) return;
-  const int64_t row = block * 16 + lane / 4;
-  const bool live = row < v;
-  const uint8_t* codes = data + (live ? row : 0) * ld_d;
-  const uint8_t* sc = scales + (live ? row : 0) * ld_s + k0;
-  uint32_t q[2][4], e[2] = {0, 0};
+// The main loop of one role.  LOADER, waves 0 to 3: all direct loads, in step
+// kt the four of the hidden rows of step kt + 4 and a quarter of the weight slot
+// after next; waves 4 to 7 the scales of that slot, a thread a column, through
+// registers.  (Of the loads in flight before step kt, those of the hidden rows
+// of step kt + 1 were issued in step kt - 3 and the last of a slot that begins
+// with step kt + 1 in step kt - 4: ten may be left, the five of kt - 1 and of
+// kt - 2.)  Weight piece s of row r lies at s ^ (r / 4) % 4 of its 64 bytes, which
+// puts the 64 reads of a wave on different banks.
+template <bool LOADER>
+__device__ __forceinline__ void fp4_wide_loop(SmemFp4Wide& sm, const uint16_t* __restrict__ hb,
+                                              int64_t m0, int64_t rows,
+                                              const uint8_t* __restrict__ data, int64_t ld_d,
+                                              const uint8_t* __restrict__ scales, int64_t ld_s,
+                                              int64_t v0, int64_t v, int ksteps,
+                                              f32x4 (&acc)[8][4]) {
+  const int tid = threadIdx.x, lane = tid % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int wm = wave / 4, wn = wave % 4, li = lane % 16, g = lane / 16;
+  const int nslots = (ksteps + kWideSteps - 1) / kWideSteps;
+  const int last = ksteps - (nslots - 1) * kWideSteps;  // steps of the last slot: K is a multiple of 64
+  const int vmax = static_cast<int>(min(v - 1 - v0, int64_t{BN - 1}));
+  gemm::LoaderSrc<true> sa;
+  uint32_t wofs[4];
+  uint32_t back = 0;  // of a piece past the last slot's end
+  const uint8_t* wb = data + v0 * ld_d;
+  const uint8_t* sb = scales;
+  if constexpr (LOADER) {
+    const int lrow = lane / 4, c = (lane % 4) ^ (lrow >> 2 & 3);
+    sa.init(hb, static_cast<int64_t>(ksteps) * 512, m0, rows, wave, lrow,
+            ((lane % 4) ^ gemm::swz(lrow)) * 8);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      wofs[j] = min((wave + 4 * j) * 16 + lrow, vmax) * static_cast<uint32_t>(ld_d) + c * 16;
+    back = max(c - last + 1, 0) * 16;
+  } else {
+    sb = scales + (v0 + min(tid - 256, vmax)) * ld_s;
+  }
+  auto issue_a = [&](int stage, int step) {
+    if constexpr (LOADER) {
+      const int64_t k = static_cast<int64_t>(min(step, ksteps - 1)) * 512;
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        __builtin_amdgcn_global_load_lds(sa.at(u, k), sm.a[stage] + (wave + 4 * u) * 512, 16, 0, 0);
+    }
+  };
+  auto issue_w = [&](int place, int slot, int j) {
+    if constexpr (LOADER) {
+      const int p = min(slot, nslots - 1);
+      __builtin_amdgcn_global_load_lds(
+          wb + static_cast<int64_t>(p) * kWideBytes + (wofs[j] - (p == nslots - 1 ? back : 0)),
+          sm.w[place] + (wave + 4 * j) * 1024, 16, 0, 0);
+    }
+  };
+  uint16_t sc[2];
+  auto load_scale = [&](int slot) {
+    if constexpr (!LOADER) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        sc[i] = reinterpret_cast<const ScalePair*>(sb + min(slot * kWideSteps + 2 * i, ksteps - 2))->w;
+    }
+  };
+  auto store_scale = [&](int place) {
+    if constexpr (!LOADER)
+      sm.scale[place][tid - 256] = sc[0] | static_cast<uint32_t>(sc[1]) << 16;
+  };
+  const int aoff = (wm * 128 + li) * BK + ((g ^ gemm::swz(li)) * 8);
+  const int col = wn * 64 + li, sw = li >> 2 & 3;
+  bf16x8 a[2][4], b[4];  // a step's hidden rows in two halves; its weights
+  uint32_t q[4], e[4];   // their codes, the slot's scales
+  auto read_a = [&](int stage, int half) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      a[half][i] =
+          *reinterpret_cast<const bf16x8*>(sm.a[stage] + aoff + (4 * half + i) * 16 * BK);
+  };
+  auto read_q = [&](int stage, int place) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      q[j] = *reinterpret_cast<const uint32_t*>(sm.w[place] + (col + 16 * j) * kWideBytes +
+                                                ((stage ^ sw) * 16) + g * 4);
+  };
+  auto read_e = [&](int place) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) e[j] = sm.scale[place][col + 16 * j];
+  };
+  // Steps -4 to -1.
+#pragma unroll
+  for (int j = 0; j < 4; ++j) issue_w(0, 0, j);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    issue_a(j, j);
+    issue_w(1, 1, j);
+  }
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const uint4 x = *reinterpret_cast<const uint4*>(
-        codes + static_cast<int64_t>(min(k0 + 4 * i + t, ksteps - 1)) * 16);
-    q[i][0] = x.x; q[i][1] = x.y; q[i][2] = x.z; q[i][3] = x.w;
+    load_scale(i);
+    store_scale(i);
   }
-  if (k0 + 8 <= ksteps) {
-    const Scale8 x = *reinterpret_cast<const Scale8*>(sc);
-    e[0] = x.w[0];
-    e[1] = x.w[1];
-  } else {
-    for (int s = 0; k0 + s < ksteps; ++s)
-      e[s / 4] |= static_cast<uint32_t>(sc[s]) << (8 * (s % 4));
-  }
-  quad_transpose(q[0], t);
-  quad_transpose(q[1], t);
-  uint16_t* to = out + (block * ksteps + k0) * 512 + lane * 8;
+  wait_vm_lgkm0<LOADER ? 16 : 0>();
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  read_a(0, 0);
+  read_q(0, 0);
+  read_e(0);
+  int p0 = 0, p1 = 1, p2 = 2;  // places of this slot and the next two
+  // A step: the products of one half of its hidden rows while the other half is
+  // read; then, everything of it being read and step kt + 1 there, the barrier,
+  // and those of the other half while the next step's first half is read.
+  for (int p = 0; p < nslots; ++p) {
 #pragma unroll
-  for (int s = 0; s < 8; ++s) {
-    const uint32_t b = e[s / 4];
-    const uint32_t scale = s % 4 == 3 ? b >> 1 : b << (23 - 8 * (s % 4));
-    const bf16x8 x = decode8(live ? q[s / 4][s % 4] : 0u, __uint_as_float(live ? scale : 0u));
-    if (k0 + s < ksteps) *reinterpret_cast<bf16x8*>(to + s * 512) = x;
+    for (int t = 0; t < kWideSteps; ++t) {
+      read_a(t, 1);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        b[j] = decode8(q[j], __uint_as_float(t == 3 ? e[j] >> 1 : e[j] << (23 - 8 * (t % 3))));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[0][i], b[j], acc[i][j], 0, 0, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+#pragma unroll
+      for (int o = 0; o < 8; ++o) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      wait_vm_lgkm0<LOADER ? 10 : 63>();
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      issue_a(t, 4 * p + t + 4);
+      issue_w(p2, p + 2, t);
+      if (t == 0) load_scale(p + 2);
+      if (t == 3) store_scale(p2);
+      read_a((t + 1) % 4, 0);
+      read_q((t + 1) % 4, t == 3 ? p1 : p0);
+      if (t == 3) read_e(p1);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          acc[4 + i][j] =
+              __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[1][i], b[j], acc[4 + i][j], 0, 0, 0);
+      if constexpr (LOADER) __builtin_amdgcn_sched_group_barrier(0x020, 5, 0);
+#pragma unroll
+      for (int o = 0; o < 12; ++o) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      if (t == 1 && p == nslots - 1 && last == 2) break;
+    }
+    const int x = p0;
+    p0 = p1;
+    p1 = p2;
+    p2 = x;
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+__global__ __launch_bounds__(kThreads4) void linear_fp4_wide(
+    const uint16_t* __restrict__ hb, const uint8_t* __restrict__ data, int64_t ld_d,
+    const uint8_t* __restrict__ scales, int64_t ld_s, int64_t n, int64_t v, int ksteps,
+    int mblocks, int vblocks, const void* __restrict__ tgt, int32_t tgt32, int64_t ignore,
+    float* __restrict__ pm, float* __restrict__ ps, float* __restrict__ pt, LinearExtras ex,
+    int* queue, int queued) {
+  __shared__ __align__(16) SmemFp4Wide sm;
+  const int tid = threadIdx.x, lane = tid % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int logical = gemm::queue_tile(queue, mblocks * vblocks, queued, &sm.slot);
+  if (logical < 0) return;
+  int mb, vb;
+  gemm::tile_coords(logical, mblocks, vblocks, mb, vb);
+  const int64_t m0 = static_cast<int64_t>(mb) * 256, v0 = static_cast<int64_t>(vb) * BN;
+  if (tid < 256) sm.rd.code[tid] = row_code(m0 + tid, n, Targets{tgt, tgt32}, ignore, v0, v);
+  f32x4 acc[8][4];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const int64_t rows = static_cast<int64_t>(mblocks) * 256;
+  if (gemm::loader_wave())
+    fp4_wide_loop<true>(sm, hb, m0, rows, data, ld_d, scales, ld_s, v0, v, ksteps, acc);
+  else
+    fp4_wide_loop<false>(sm, hb, m0, rows, data, ld_d, scales, ld_s, v0, v, ksteps, acc);
+  __syncthreads();
+  stats_epilogue<8, 4, 256, kThreads4, kWideScratch>(acc, sm.rd, &sm.a, (wave / 4) * 128,
+                                                     (wave % 4) * 64, lane % 16, lane / 16, tid,
+                                                     m0, v0, vb, vblocks, n, v, pm, ps, pt, ex);
 }
 
 }  // namespace
 
-int64_t fp4_decoded_bytes(int64_t v, int64_t h) { return (v + 255) / 256 * 256 * h * 2; }
-
-void launch_fp4_decode(const Fp4Weight& w, int64_t v, int64_t h, uint16_t* out, hipStream_t s) {
-  const int ksteps = static_cast<int>(h / BK), parts = (ksteps + 31) / 32;
-  const int64_t blocks = (v + 255) / 256 * 16;
-  // a grid holds fewer than 2^32 threads
-  const int64_t most = (int64_t{1} << 23) / parts > 0 ? (int64_t{1} << 23) / parts : 1;
-  for (int64_t b = 0; b < blocks; b += most) {
-    const int64_t m = blocks - b < most ? blocks - b : most;
-    hipLaunchKernelGGL(fp4_decode_kernel, dim3(static_cast<unsigned>(m * parts)), dim3(256), 0, s,
-                       w.data, w.ld_d, w.scales, w.ld_s, v, ksteps, parts, b, out);
-  }
-}
-
 void launch_fp4_partials(const uint16_t* hidden, int64_t ld_h, const Fp4Weight& w, int64_t n,
                          int64_t h, int64_t v, Targets targets, int64_t ignore, float* pm,
                          float* ps, float* pt, float inv_t, int32_t round_bf16, float* pw, void* z,
-                         int32_t z_bf16, int64_t ld_z, hipStream_t s) {
+                         int32_t z_bf16, int64_t ld_z, uint16_t* hb, hipStream_t s) {
   const int vblocks = static_cast<int>((v + BN - 1) / BN);
-  const int rows = n <= 16 ? 16 : n <= 32 ? 32 : 64;
+  const int rows = n <= 16 ? 16 : n <= 32 ? 32 : n <= kFp4Narrow ? 64 : 256;
   const int mblocks = static_cast<int>((n + rows - 1) / rows);
   const int32_t z_vec = z && reinterpret_cast<uintptr_t>(z) % 16 == 0 &&
                         (ld_z * (z_bf16 ? 2 : 4)) % 16 == 0;
   const LinearExtras ex{inv_t, round_bf16, pw, z, z_bf16, ld_z, z_vec};
+  if (rows == 256) {
+    const int64_t np = static_cast<int64_t>(mblocks) * 256;
+    int* queue = reinterpret_cast<int*>(hb + np * h);  // cleared by launch_block_rows
+    launch_block_rows(hidden, ld_h, n, np, h, hb, s, queue, gemm::kQueueBytes / 4);
+    const gemm::QueuePlan qp = gemm::queue_plan(mblocks * vblocks, xcd_cus());
+    hipLaunchKernelGGL(linear_fp4_wide, dim3(static_cast<unsigned>(qp.grid)), dim3(kThreads4), 0, s,
+                       hb, w.data, w.ld_d, w.scales, w.ld_s, n, v, static_cast<int>(h / BK),
+                       mblocks, vblocks, targets.p, targets.is32, ignore, pm, ps, pt, ex, queue,
+                       qp.queued);
+    return;
+  }
   // a workgroup a CU, as many on every XCD
   const int per = (mblocks * vblocks + 7) / 8, cus = xcd_cus();
   const int grid = 8 * (per < cus ? per : cus);

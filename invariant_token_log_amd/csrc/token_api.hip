@@ -67,15 +67,13 @@ StreamLayout stream_layout(int64_t n, int64_t v, int32_t dtype, int32_t w, int32
 }
 
 // The head's forward, rc rows at a time: tile statistics [rc, T] (m, s, w),
-// the one given token's logits, the rows' activity, the re-laid hidden rows,
-// the chunk's logits and, once for all chunks, the decoded copy of a 4-bit
-// weight.
+// the one given token's logits, the rows' activity, the re-laid hidden rows
+// and the chunk's logits.
 struct HeadLayout {
   int64_t rc, ntiles, ld_z;
   int tile;  // vocabulary columns of a statistic tile
   bool single, own_z;
-  bool direct;  // 4-bit weight, read as it is
-  size_t pm, ps, pw, pt, act, hb, z, wd, total;
+  size_t pm, ps, pw, pt, act, hb, z, total;
 };
 
 HeadLayout head_layout(int64_t n, int64_t h, int64_t v, int64_t m, int32_t top_k, int32_t flags,
@@ -99,15 +97,10 @@ HeadLayout head_layout(int64_t n, int64_t h, int64_t v, int64_t m, int32_t top_k
   l.pt = 3 * table;
   l.act = l.pt + ws_round(rows * 4);
   l.hb = l.act + ws_round(rows * 4);
-  l.direct = (flags & LOGP_TOKEN_FP4) && n <= itl::kFp4Direct;
   const int64_t hb = flags & LOGP_TOKEN_Q8 ? itl::q8_fwd_scratch_bytes(l.rc, h)
-                     : l.direct            ? 0
                                            : itl::linear_fwd_blocked_bytes(l.rc, h);
   l.z = l.hb + ws_round(static_cast<size_t>(hb));
-  l.wd = l.z + (l.own_z ? ws_round(rows * static_cast<size_t>(l.ld_z) * zsize) : 0);
-  l.total = l.wd + ((flags & LOGP_TOKEN_FP4) && !l.direct
-                        ? ws_round(static_cast<size_t>(itl::fp4_decoded_bytes(v, h)))
-                        : 0);
+  l.total = l.z + (l.own_z ? ws_round(rows * static_cast<size_t>(l.ld_z) * zsize) : 0);
   return l;
 }
 
@@ -163,12 +156,6 @@ void run_head(const HeadArgs& a, const HeadLayout& l, char* ws, hipStream_t s) {
   int32_t* act = reinterpret_cast<int32_t*>(ws + l.act);
   const int ntiles = static_cast<int>(l.ntiles);
   const int esize = a.q8 ? 1 : 2;
-  const uint16_t* wblk = a.wblk;
-  if (a.fp4 && !l.direct) {
-    uint16_t* decoded = reinterpret_cast<uint16_t*>(ws + l.wd);
-    itl::launch_fp4_decode(*a.fp4, a.v, a.h, decoded, s);
-    wblk = decoded;
-  }
   for (int64_t r0 = 0; r0 < a.n; r0 += l.rc) {
     const int64_t rows = l.rc < a.n - r0 ? l.rc : a.n - r0;
     const itl::TokenView tok = token_rows(a.tok, r0);
@@ -193,15 +180,15 @@ void run_head(const HeadArgs& a, const HeadLayout& l, char* ws, hipStream_t s) {
                               a.hidden_scale + r0, static_cast<const uint8_t*>(a.weight), a.ld_w,
                               a.weight_scale, rows, a.h, a.v, tg, ignore, pm, ps, pt, a.inv_t, pw,
                               static_cast<float*>(z), ld_z, ws + l.hb, s);
-    else if (l.direct)
+    else if (a.fp4)
       itl::launch_fp4_partials(reinterpret_cast<const uint16_t*>(hidden), a.ld_h, *a.fp4, rows, a.h,
                                a.v, tg, ignore, pm, ps, pt, a.inv_t, a.round_bf16, pw, z, z_bf16,
-                               ld_z, s);
+                               ld_z, reinterpret_cast<uint16_t*>(ws + l.hb), s);
     else
       itl::launch_linear_partials(reinterpret_cast<const uint16_t*>(hidden), a.ld_h,
                                   static_cast<const uint16_t*>(a.weight), a.ld_w, rows, a.h, a.v,
                                   tg, ignore, pm, ps, pt, a.inv_t, a.round_bf16, pw, z, z_bf16,
-                                  ld_z, wblk, reinterpret_cast<uint16_t*>(ws + l.hb), s);
+                                  ld_z, a.wblk, reinterpret_cast<uint16_t*>(ws + l.hb), s);
     const bool read_z = !l.single && z;
     const int zdt = z_bf16 ? itl::kBF16 : itl::kF32;
     itl::launch_token_finish(zdt, read_z && rows_aligned16(z, ld_z, z_bf16 ? 2 : 4), l.tile,

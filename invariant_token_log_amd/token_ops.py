@@ -300,8 +300,7 @@ def linear_token_logp_fwd(hidden, weight, token_ids=None, top_k=0, ignore_index=
     token_ids [N, M].  hidden and weight may both be QuantizedRows: the 8-bit
     head of frozen weights (no round_logits, prepared_weight or logits_out).
     weight may be Fp4Rows: the 4-bit head of frozen weights, with the bits of the
-    bfloat16 weight they stand for (no prepared_weight or logits_out; more than
-    448 rows take a bfloat16 copy of the weight in the workspace).
+    bfloat16 weight they stand for (no prepared_weight or logits_out).
     round_logits and prepared_weight: as linear_logp_fwd.  logits_out [N, V]
     float32 (or bfloat16 with round_logits) receives the unscaled logits for
     linear_token_logp_bwd.  row_chunk: rows taken at a time, which bounds the

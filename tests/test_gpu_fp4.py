@@ -47,7 +47,9 @@ def same(a, b):
 
 @pytest.mark.parametrize("n,h,v", [(1, 64, 1), (1, 64, 300), (5, 128, 256), (3, 192, 257), (16, 256, 1000), (32, 320, 515),
                                    (33, 448, 5003), (64, 512, 300), (65, 576, 700), (200, 1024, 999), (256, 1600, 513),
-                                   (448, 448, 1100), (449, 448, 1100), (500, 1024, 5003), (7, 4096, 3001), (40, 4096, 777)])
+                                   (448, 448, 1100), (449, 448, 1100), (500, 1024, 5003), (7, 4096, 3001), (40, 4096, 777),
+                                   (128, 192, 513), (129, 64, 300), (129, 128, 1), (150, 192, 257), (257, 320, 515),
+                                   (511, 576, 5003), (130, 4096, 777), (1025, 1088, 4097)])
 def test_head_has_the_bits_of_the_decoded_weight(n, h, v):
     q, values = table(v, h)
     w = values.bfloat16().to(dev())
