@@ -22,11 +22,6 @@ struct Fp4Weight {
 constexpr int64_t kMaxFp4Stride = int64_t{1} << 23;
 constexpr int64_t kMaxHiddenStride = int64_t{1} << 25;
 
-// Up to this many rows the weight streams once for every 64 rows, past them the
-// matrix cores take blocks of 256 (V = 151936, H = 4096: 128 rows 224 us, 129 to
-// 256 rows 260 to 284, where four times 64 would take 400).
-constexpr int64_t kFp4Narrow = 128;
-
 // launch_linear_partials on a 4-bit weight, the same bits as on the bf16 weight
 // that it stands for.  hb: linear_fwd_blocked_bytes(n, h) bytes.
 void launch_fp4_partials(const uint16_t* hidden, int64_t ld_h, const Fp4Weight& w, int64_t n,

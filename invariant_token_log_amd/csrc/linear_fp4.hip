@@ -9,22 +9,22 @@
 // values, and the sums and statistics are exactly those of linear_logp.hip: a
 // row has the bits of the bf16 head on the decoded weight.
 //
-// Few rows (linear_fp4_narrow): bound by the weight's bytes, 17 / 32 of a byte a value.  A workgroup
-// takes tiles of 256 columns x ROWS hidden rows, eight waves of 32 columns x
-// ROWS rows, so that every weight is decoded once.  Slots of 256 K values hold
-// whole 128-byte lines of the weight's rows and the hidden rows' pieces, panels
-// of two slots the scales (16 bytes a row: taken slot by slot their requests
-// were as many as the weight's, 16 us of 92), all brought by direct loads.  The
-// slots of a workgroup's tiles follow one another, so that the next tile's first
-// ones are on their way during a tile's epilogue.
+// Few rows (linear_fp4_narrow): bound by the weight's bytes, 17 / 32 of a byte a
+// value.  A workgroup takes tiles of 256 columns x ROWS hidden rows, eight waves
+// of 32 columns x ROWS rows, so that every weight is decoded once.  Slots of 256
+// K values hold whole 128-byte lines of the weight's rows and the hidden rows'
+// pieces, panels of two slots the scales (16 bytes a row: taken slot by slot
+// their requests were as many as the weight's, 16 us of 92), all brought by
+// direct loads.  The slots of a workgroup's tiles follow one another, so that the
+// next tile's first ones are on their way during a tile's epilogue.
 // V = 151936, H = 4096 (330 MB, 51 us at 6.45 TB/s): 76 us at 16 rows, 95 at 32,
 // 133 at 64; without the products and decoding 65, 71 and 93 (594 tiles on 256
 // CUs, the last 82 nearly alone), without the loads 52, 62 and 86.  Two to four
 // slots, whole or half lines, four waves a workgroup and three workgroups a CU
 // (81, 96, 153) made no difference or a worse one.
 //
-// Many rows (linear_fp4_wide): bound by the matrix cores.  Blocks of 256 hidden
-// rows x 256 columns like those of the bf16 head, the weight's codes in LDS in
+// Many rows (linear_fp4_wide): bound by the matrix cores.  Blocks of 256 (128)
+// hidden rows x 256 columns like those of the bf16 head, the weight's codes in LDS in
 // place of its values (a quarter of the bytes to bring and to read) and decoded
 // beside the products of the step, 20 vector instructions to 32 products.  A wave
 // holds a step's hidden rows in two halves, one read while the other's products
@@ -58,8 +58,6 @@ constexpr int kPanels = 3;  // those of slots p .. p + 2, each of which may begi
 // Rows of the epilogue, whose waves take 64 columns x half of them.
 template <int ROWS>
 constexpr int kEpiRows = ROWS < 32 ? 32 : ROWS;
-template <int ROWS>
-constexpr int kMostRows = ROWS == 64 ? static_cast<int>(kFp4Narrow) : ROWS;
 
 template <int ROWS>
 struct Fp4Slot {
@@ -72,7 +70,7 @@ struct SmemFp4 {
   Fp4Slot<ROWS> slot[kSlots<ROWS>];
   uint8_t scale[kPanels][BN * 2 * kSlotSteps];
   Reduce<kEpiRows<ROWS>> rd;
-  int64_t target[kMostRows<ROWS>];
+  int64_t target[ROWS];
 };
 
 // Two scale bytes at any address.
@@ -107,20 +105,18 @@ struct Fp4Loader {
   static constexpr int kOdd = 4 + NH, kEven = kOdd + (ALIGNED ? 2 : 0);
   int64_t ld_h, n, ld_d, ld_s, v;
   int ksteps, nslots, last;  // last: steps of a tile's last slot
-  int mblocks, tile, step, end;
+  int tile, step, end;
   int p, ring, panel;  // the next slot: of its tile, its place, its panel's
-  int64_t w0, h0, s0;  // where the tile's rows begin
+  int64_t w0, s0;      // where the tile's rows begin
   uint32_t wofs[4], hofs[NH], sofs[2];
 
   // Rows past the data read the last one: every load stays in bounds, and what
   // it brings is masked or not read.
   __device__ __forceinline__ void rows(int tid, int wave, int lane) {
-    const int64_t m0 = static_cast<int64_t>(tile % mblocks) * ROWS;
-    const int64_t v0 = static_cast<int64_t>(tile / mblocks) * BN;
+    const int64_t v0 = static_cast<int64_t>(tile) * BN;
     const int vmax = static_cast<int>(min(v - 1 - v0, int64_t{BN - 1}));
-    const int hmax = static_cast<int>(min(n - 1 - m0, int64_t{ROWS - 1}));
+    const int hmax = static_cast<int>(n) - 1;
     w0 = v0 * ld_d;
-    h0 = m0 * ld_h;
     s0 = v0 * ld_s;
     const uint32_t lw = static_cast<uint32_t>(ld_d), lh = static_cast<uint32_t>(ld_h) * 2;
     const uint32_t ls = static_cast<uint32_t>(ld_s);
@@ -171,7 +167,7 @@ struct Fp4Loader {
     Fp4Slot<ROWS>& to = sm.slot[ring];
     const uint8_t* wb = data + w0 + static_cast<int64_t>(p) * kSlotBytes;
     const uint8_t* hb =
-        reinterpret_cast<const uint8_t*>(hidden + h0 + static_cast<int64_t>(p) * kSlotK);
+        reinterpret_cast<const uint8_t*>(hidden + static_cast<int64_t>(p) * kSlotK);
     const bool whole = p < nslots - 1 || last == kSlotSteps;
     if (whole) {
 #pragma unroll
@@ -299,8 +295,8 @@ template <int ROWS, bool ALIGNED>
 __device__ __forceinline__ void fp4_tiles(
     SmemFp4<ROWS>& sm, const uint16_t* __restrict__ hidden, int64_t ld_h,
     const uint8_t* __restrict__ data, int64_t ld_d, const uint8_t* __restrict__ scales,
-    int64_t ld_s, int64_t n, int64_t v, int ksteps, int mblocks, int vblocks, Targets targets,
-    int64_t ignore, float* __restrict__ pm, float* __restrict__ ps, float* __restrict__ pt,
+    int64_t ld_s, int64_t n, int64_t v, int ksteps, int vblocks, Targets targets, int64_t ignore,
+    float* __restrict__ pm, float* __restrict__ ps, float* __restrict__ pt,
     float inv_t, int32_t round_bf16, float* pw, void* z, int32_t z_bf16, int64_t ld_z,
     int32_t z_vec) {
   const LinearExtras ex{inv_t, round_bf16, pw, z, z_bf16, ld_z, z_vec};
@@ -311,7 +307,7 @@ __device__ __forceinline__ void fp4_tiles(
   const int li = lane % 16, g = lane / 16;
   // Workgroup b takes tiles of XCD b % 8's range.
   int first, end;
-  gemm::xcd_range(mblocks * vblocks, blockIdx.x % 8, first, end);
+  gemm::xcd_range(vblocks, blockIdx.x % 8, first, end);
   const int step = gridDim.x / 8;
   const int begin = first + blockIdx.x / 8;
   if (begin >= end) return;
@@ -326,7 +322,6 @@ __device__ __forceinline__ void fp4_tiles(
   load.ksteps = ksteps;
   load.nslots = (ksteps + kSlotSteps - 1) / kSlotSteps;
   load.last = ksteps - (load.nslots - 1) * kSlotSteps;
-  load.mblocks = mblocks;
   load.tile = begin;
   load.step = step;
   load.end = end;
@@ -349,8 +344,7 @@ __device__ __forceinline__ void fp4_tiles(
 
   int ring = 0, panel = kPanels - 1;
   for (int tile = begin; tile < end; tile += step) {
-    const int64_t m0 = static_cast<int64_t>(tile % mblocks) * ROWS;
-    const int64_t v0 = static_cast<int64_t>(tile / mblocks) * BN;
+    const int64_t v0 = static_cast<int64_t>(tile) * BN;
     f32x4 part[ROWS / 16][2];
 #pragma unroll
     for (int i = 0; i < ROWS / 16; ++i)
@@ -386,9 +380,8 @@ __device__ __forceinline__ void fp4_tiles(
     // for: the epilogue's.
     if (tid < EPI) {
       int code = -2;
-      const int64_t r = m0 + tid;
-      if (r < n) {
-        const int64_t t = sm.target[r];
+      if (tid < n) {
+        const int64_t t = sm.target[tid];
         if (t != ignore) code = t >= v0 && t < v0 + BN && t < v ? static_cast<int>(t - v0) : -1;
       }
       sm.rd.code[tid] = code;
@@ -397,8 +390,8 @@ __device__ __forceinline__ void fp4_tiles(
     f32x4 acc[MI][4];
     regroup<ROWS, MI>(part, reinterpret_cast<float*>(&sm.slot[ring]), wave, row0, col0, li, g, acc);
     stats_epilogue<MI, 4, EPI, kThreads4, sizeof(Fp4Slot<ROWS>)>(
-        acc, sm.rd, &sm.slot[ring], row0, col0, li, g, tid, m0, v0, tile / mblocks, vblocks, n, v,
-        pm, ps, pt, ex);
+        acc, sm.rd, &sm.slot[ring], row0, col0, li, g, tid, 0, v0, tile, vblocks, n, v, pm, ps,
+        pt, ex);
     ring = ring == S - 1 ? 0 : ring + 1;
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -408,61 +401,68 @@ template <int ROWS, bool ALIGNED>
 __global__ __launch_bounds__(kThreads4) void linear_fp4_narrow(
     const uint16_t* __restrict__ hidden, int64_t ld_h, const uint8_t* __restrict__ data,
     int64_t ld_d, const uint8_t* __restrict__ scales, int64_t ld_s, int64_t n, int64_t v,
-    int ksteps, int mblocks, int vblocks, const void* __restrict__ tgt, int32_t tgt32,
+    int ksteps, int vblocks, const void* __restrict__ tgt, int32_t tgt32,
     int64_t ignore, float* __restrict__ pm, float* __restrict__ ps, float* __restrict__ pt,
     LinearExtras ex) {
   __shared__ __align__(16) SmemFp4<ROWS> sm;
-  fp4_tiles<ROWS, ALIGNED>(sm, hidden, ld_h, data, ld_d, scales, ld_s, n, v, ksteps, mblocks,
-                           vblocks, Targets{tgt, tgt32}, ignore, pm, ps, pt, ex.inv_t,
+  fp4_tiles<ROWS, ALIGNED>(sm, hidden, ld_h, data, ld_d, scales, ld_s, n, v, ksteps, vblocks,
+                           Targets{tgt, tgt32}, ignore, pm, ps, pt, ex.inv_t,
                            ex.round_bf16, ex.pw, ex.z, ex.z_bf16, ex.ld_z, ex.z_vec);
 }
 
 // ---------------------------------------------------------------------------
-// Many rows: blocks of 256 hidden rows x 256 columns, eight waves of 128 x 64.
+// Many rows: blocks of ROWS hidden rows x 256 columns, eight waves of ROWS / 2 x 64.
+// 256 rows: the hidden rows K32-blocked, tiles from the queue of mfma_gemm.h;
+// 128: one block of rows as they are.
 // ---------------------------------------------------------------------------
 constexpr int kWideSteps = 4;                       // K steps a slot
 constexpr int kWideBytes = kWideSteps * BK / 2;     // of a weight row: 64
 constexpr int kWideSlots = 3;
 
+template <int ROWS>
 struct SmemFp4Wide {
-  uint16_t a[kWideSteps][256 * BK];         // a K step's hidden rows each
+  uint16_t a[kWideSteps][ROWS * BK];        // a K step's hidden rows each
   uint8_t w[kWideSlots][BN * kWideBytes];
   uint32_t scale[kWideSlots][BN];
-  Reduce<256> rd;
+  Reduce<ROWS> rd;
   int slot;  // tile-queue broadcast
 };
-constexpr int kWideScratch = sizeof(SmemFp4Wide::a) + sizeof(SmemFp4Wide::w);
 
 // The main loop of one role.  LOADER, waves 0 to 3: all direct loads, in step
-// kt the four of the hidden rows of step kt + 4 and a quarter of the weight slot
-// after next; waves 4 to 7 the scales of that slot, a thread a column, through
-// registers.  (Of the loads in flight before step kt, those of the hidden rows
-// of step kt + 1 were issued in step kt - 3 and the last of a slot that begins
-// with step kt + 1 in step kt - 4: ten may be left, the five of kt - 1 and of
-// kt - 2.)  Weight piece s of row r lies at s ^ (r / 4) % 4 of its 64 bytes, which
-// puts the 64 reads of a wave on different banks.
-template <bool LOADER>
-__device__ __forceinline__ void fp4_wide_loop(SmemFp4Wide& sm, const uint16_t* __restrict__ hb,
+// kt those of the hidden rows of step kt + 4 (NA a wave) and a quarter of the
+// weight slot after next; waves 4 to 7 the scales of that slot, a thread a column,
+// through registers.  (Of the loads in flight before step kt, those of the hidden
+// rows of step kt + 1 were issued in step kt - 3 and the last of a slot that
+// begins with step kt + 1 in step kt - 4: those of kt - 1 and kt - 2 may be left.)
+// Weight piece s of row r lies at s ^ (r / 4) % 4 of its 64 bytes, which puts the 64
+// reads of a wave on different banks.
+template <int ROWS, bool LOADER>
+__device__ __forceinline__ void fp4_wide_loop(SmemFp4Wide<ROWS>& sm,
+                                              const uint16_t* __restrict__ hidden, int64_t ld_h,
                                               int64_t m0, int64_t rows,
                                               const uint8_t* __restrict__ data, int64_t ld_d,
                                               const uint8_t* __restrict__ scales, int64_t ld_s,
                                               int64_t v0, int64_t v, int ksteps,
-                                              f32x4 (&acc)[8][4]) {
+                                              f32x4 (&acc)[ROWS / 32][4]) {
+  constexpr bool kBlocked = ROWS == 256;
+  constexpr int MH = ROWS / 64, NA = ROWS / 64;  // of a half; hidden loads a wave and step
   const int tid = threadIdx.x, lane = tid % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int wm = wave / 4, wn = wave % 4, li = lane % 16, g = lane / 16;
   const int nslots = (ksteps + kWideSteps - 1) / kWideSteps;
-  const int last = ksteps - (nslots - 1) * kWideSteps;  // steps of the last slot: K is a multiple of 64
+  const int last = ksteps - (nslots - 1) * kWideSteps;  // 2 or 4: K is a multiple of 64
   const int vmax = static_cast<int>(min(v - 1 - v0, int64_t{BN - 1}));
-  gemm::LoaderSrc<true> sa;
+  const uint16_t* ha[NA];
   uint32_t wofs[4];
   uint32_t back = 0;  // of a piece past the last slot's end
   const uint8_t* wb = data + v0 * ld_d;
   const uint8_t* sb = scales;
   if constexpr (LOADER) {
     const int lrow = lane / 4, c = (lane % 4) ^ (lrow >> 2 & 3);
-    sa.init(hb, static_cast<int64_t>(ksteps) * 512, m0, rows, wave, lrow,
-            ((lane % 4) ^ gemm::swz(lrow)) * 8);
+#pragma unroll
+    for (int u = 0; u < NA; ++u)
+      ha[u] = gemm::lane_chunk<kBlocked>(hidden, ld_h, m0, rows, wave + 4 * u, lrow,
+                                         ((lane % 4) ^ gemm::swz(lrow)) * 8);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       wofs[j] = min((wave + 4 * j) * 16 + lrow, vmax) * static_cast<uint32_t>(ld_d) + c * 16;
@@ -472,10 +472,10 @@ __device__ __forceinline__ void fp4_wide_loop(SmemFp4Wide& sm, const uint16_t* _
   }
   auto issue_a = [&](int stage, int step) {
     if constexpr (LOADER) {
-      const int64_t k = static_cast<int64_t>(min(step, ksteps - 1)) * 512;
+      const int64_t k = static_cast<int64_t>(min(step, ksteps - 1)) * (kBlocked ? 512 : BK);
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        __builtin_amdgcn_global_load_lds(sa.at(u, k), sm.a[stage] + (wave + 4 * u) * 512, 16, 0, 0);
+      for (int u = 0; u < NA; ++u)
+        __builtin_amdgcn_global_load_lds(ha[u] + k, sm.a[stage] + (wave + 4 * u) * 512, 16, 0, 0);
     }
   };
   auto issue_w = [&](int place, int slot, int j) {
@@ -491,22 +491,24 @@ __device__ __forceinline__ void fp4_wide_loop(SmemFp4Wide& sm, const uint16_t* _
     if constexpr (!LOADER) {
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        sc[i] = reinterpret_cast<const ScalePair*>(sb + min(slot * kWideSteps + 2 * i, ksteps - 2))->w;
+        sc[i] = reinterpret_cast<const ScalePair*>(
+                    sb + min(slot * kWideSteps + 2 * i, ksteps - 2))
+                    ->w;
     }
   };
   auto store_scale = [&](int place) {
     if constexpr (!LOADER)
       sm.scale[place][tid - 256] = sc[0] | static_cast<uint32_t>(sc[1]) << 16;
   };
-  const int aoff = (wm * 128 + li) * BK + ((g ^ gemm::swz(li)) * 8);
+  const int aoff = (wm * (ROWS / 2) + li) * BK + ((g ^ gemm::swz(li)) * 8);
   const int col = wn * 64 + li, sw = li >> 2 & 3;
-  bf16x8 a[2][4], b[4];  // a step's hidden rows in two halves; its weights
+  bf16x8 a[2][MH], b[4];  // a step's hidden rows in two halves; its weights
   uint32_t q[4], e[4];   // their codes, the slot's scales
   auto read_a = [&](int stage, int half) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < MH; ++i)
       a[half][i] =
-          *reinterpret_cast<const bf16x8*>(sm.a[stage] + aoff + (4 * half + i) * 16 * BK);
+          *reinterpret_cast<const bf16x8*>(sm.a[stage] + aoff + (MH * half + i) * 16 * BK);
   };
   auto read_q = [&](int stage, int place) {
 #pragma unroll
@@ -531,7 +533,7 @@ __device__ __forceinline__ void fp4_wide_loop(SmemFp4Wide& sm, const uint16_t* _
     load_scale(i);
     store_scale(i);
   }
-  wait_vm_lgkm0<LOADER ? 16 : 0>();
+  wait_vm_lgkm0<LOADER ? 3 * (NA + 1) + 1 : 0>();
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
   read_a(0, 0);
@@ -549,18 +551,18 @@ __device__ __forceinline__ void fp4_wide_loop(SmemFp4Wide& sm, const uint16_t* _
       for (int j = 0; j < 4; ++j) {
         b[j] = decode8(q[j], __uint_as_float(t == 3 ? e[j] >> 1 : e[j] << (23 - 8 * (t % 3))));
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < MH; ++i)
           acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[0][i], b[j], acc[i][j], 0, 0, 0);
       }
       __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, MH, 0);
 #pragma unroll
-      for (int o = 0; o < 8; ++o) {
+      for (int o = 0; o < 2 * MH; ++o) {
         __builtin_amdgcn_sched_group_barrier(0x008, 2, 0);
-        __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 8 / MH, 0);
       }
       __builtin_amdgcn_sched_barrier(0);
-      wait_vm_lgkm0<LOADER ? 10 : 63>();
+      wait_vm_lgkm0<LOADER ? 2 * (NA + 1) : 63>();
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
@@ -574,16 +576,16 @@ __device__ __forceinline__ void fp4_wide_loop(SmemFp4Wide& sm, const uint16_t* _
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          acc[4 + i][j] =
-              __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[1][i], b[j], acc[4 + i][j], 0, 0, 0);
-      if constexpr (LOADER) __builtin_amdgcn_sched_group_barrier(0x020, 5, 0);
+        for (int i = 0; i < MH; ++i)
+          acc[MH + i][j] =
+              __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[1][i], b[j], acc[MH + i][j], 0, 0, 0);
+      if constexpr (LOADER) __builtin_amdgcn_sched_group_barrier(0x020, NA + 1, 0);
 #pragma unroll
-      for (int o = 0; o < 12; ++o) {
+      for (int o = 0; o < 2 * MH + 4; ++o) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
         __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       }
-      __builtin_amdgcn_sched_group_barrier(0x008, 4, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 2 * MH - 4, 0);
       __builtin_amdgcn_sched_barrier(0);
       if (t == 1 && p == nslots - 1 && last == 2) break;
     }
@@ -595,35 +597,40 @@ __device__ __forceinline__ void fp4_wide_loop(SmemFp4Wide& sm, const uint16_t* _
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 }
 
+template <int ROWS>
 __global__ __launch_bounds__(kThreads4) void linear_fp4_wide(
-    const uint16_t* __restrict__ hb, const uint8_t* __restrict__ data, int64_t ld_d,
-    const uint8_t* __restrict__ scales, int64_t ld_s, int64_t n, int64_t v, int ksteps,
-    int mblocks, int vblocks, const void* __restrict__ tgt, int32_t tgt32, int64_t ignore,
+    const uint16_t* __restrict__ hidden, int64_t ld_h, const uint8_t* __restrict__ data,
+    int64_t ld_d, const uint8_t* __restrict__ scales, int64_t ld_s, int64_t n, int64_t v,
+    int ksteps, int mblocks, int vblocks, const void* __restrict__ tgt, int32_t tgt32, int64_t ignore,
     float* __restrict__ pm, float* __restrict__ ps, float* __restrict__ pt, LinearExtras ex,
     int* queue, int queued) {
-  __shared__ __align__(16) SmemFp4Wide sm;
+  __shared__ __align__(16) SmemFp4Wide<ROWS> sm;
   const int tid = threadIdx.x, lane = tid % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int logical = gemm::queue_tile(queue, mblocks * vblocks, queued, &sm.slot);
+  const int logical = ROWS == 256 ? gemm::queue_tile(queue, mblocks * vblocks, queued, &sm.slot)
+                                  : gemm::xcd_logical(blockIdx.x, mblocks * vblocks);
   if (logical < 0) return;
   int mb, vb;
   gemm::tile_coords(logical, mblocks, vblocks, mb, vb);
-  const int64_t m0 = static_cast<int64_t>(mb) * 256, v0 = static_cast<int64_t>(vb) * BN;
-  if (tid < 256) sm.rd.code[tid] = row_code(m0 + tid, n, Targets{tgt, tgt32}, ignore, v0, v);
-  f32x4 acc[8][4];
+  const int64_t m0 = static_cast<int64_t>(mb) * ROWS, v0 = static_cast<int64_t>(vb) * BN;
+  if (tid < ROWS) sm.rd.code[tid] = row_code(m0 + tid, n, Targets{tgt, tgt32}, ignore, v0, v);
+  constexpr int MI = ROWS / 32;
+  f32x4 acc[MI][4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  const int64_t rows = static_cast<int64_t>(mblocks) * 256;
+  const int64_t rows = ROWS == 256 ? static_cast<int64_t>(mblocks) * 256 : n;
   if (gemm::loader_wave())
-    fp4_wide_loop<true>(sm, hb, m0, rows, data, ld_d, scales, ld_s, v0, v, ksteps, acc);
+    fp4_wide_loop<ROWS, true>(sm, hidden, ld_h, m0, rows, data, ld_d, scales, ld_s, v0, v, ksteps,
+                              acc);
   else
-    fp4_wide_loop<false>(sm, hb, m0, rows, data, ld_d, scales, ld_s, v0, v, ksteps, acc);
+    fp4_wide_loop<ROWS, false>(sm, hidden, ld_h, m0, rows, data, ld_d, scales, ld_s, v0, v, ksteps,
+                               acc);
   __syncthreads();
-  stats_epilogue<8, 4, 256, kThreads4, kWideScratch>(acc, sm.rd, &sm.a, (wave / 4) * 128,
-                                                     (wave % 4) * 64, lane % 16, lane / 16, tid,
-                                                     m0, v0, vb, vblocks, n, v, pm, ps, pt, ex);
+  stats_epilogue<MI, 4, ROWS, kThreads4, sizeof(sm.a) + sizeof(sm.w)>(
+      acc, sm.rd, &sm.a, (wave / 4) * (ROWS / 2), (wave % 4) * 64, lane % 16, lane / 16, tid, m0,
+      v0, vb, vblocks, n, v, pm, ps, pt, ex);
 }
 
 }  // namespace
@@ -633,24 +640,35 @@ void launch_fp4_partials(const uint16_t* hidden, int64_t ld_h, const Fp4Weight& 
                          float* ps, float* pt, float inv_t, int32_t round_bf16, float* pw, void* z,
                          int32_t z_bf16, int64_t ld_z, uint16_t* hb, hipStream_t s) {
   const int vblocks = static_cast<int>((v + BN - 1) / BN);
-  const int rows = n <= 16 ? 16 : n <= 32 ? 32 : n <= kFp4Narrow ? 64 : 256;
+  // The weight streams for up to 64 rows; then its decoding, which a block of 128
+  // rows does no more often, takes longer than the stream (V = 151936, H = 4096:
+  // 64 rows 144 us against 166 in such a block, 128 rows 224 in two streams against
+  // 177; 129 to 256 rows 256 to 277 in a block of 256).
+  const int rows = n <= 16 ? 16 : n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256;
   const int mblocks = static_cast<int>((n + rows - 1) / rows);
   const int32_t z_vec = z && reinterpret_cast<uintptr_t>(z) % 16 == 0 &&
                         (ld_z * (z_bf16 ? 2 : 4)) % 16 == 0;
   const LinearExtras ex{inv_t, round_bf16, pw, z, z_bf16, ld_z, z_vec};
+  if (rows == 128) {
+    hipLaunchKernelGGL(linear_fp4_wide<128>, dim3(static_cast<unsigned>(mblocks * vblocks)),
+                       dim3(kThreads4), 0, s, hidden, ld_h, w.data, w.ld_d, w.scales, w.ld_s, n, v,
+                       static_cast<int>(h / BK), mblocks, vblocks, targets.p, targets.is32, ignore,
+                       pm, ps, pt, ex, static_cast<int*>(nullptr), 0);
+    return;
+  }
   if (rows == 256) {
     const int64_t np = static_cast<int64_t>(mblocks) * 256;
     int* queue = reinterpret_cast<int*>(hb + np * h);  // cleared by launch_block_rows
     launch_block_rows(hidden, ld_h, n, np, h, hb, s, queue, gemm::kQueueBytes / 4);
     const gemm::QueuePlan qp = gemm::queue_plan(mblocks * vblocks, xcd_cus());
-    hipLaunchKernelGGL(linear_fp4_wide, dim3(static_cast<unsigned>(qp.grid)), dim3(kThreads4), 0, s,
-                       hb, w.data, w.ld_d, w.scales, w.ld_s, n, v, static_cast<int>(h / BK),
-                       mblocks, vblocks, targets.p, targets.is32, ignore, pm, ps, pt, ex, queue,
-                       qp.queued);
+    hipLaunchKernelGGL(linear_fp4_wide<256>, dim3(static_cast<unsigned>(qp.grid)), dim3(kThreads4),
+                       0, s, hb, h * 16, w.data, w.ld_d, w.scales, w.ld_s, n, v,
+                       static_cast<int>(h / BK), mblocks, vblocks, targets.p, targets.is32, ignore,
+                       pm, ps, pt, ex, queue, qp.queued);
     return;
   }
   // a workgroup a CU, as many on every XCD
-  const int per = (mblocks * vblocks + 7) / 8, cus = xcd_cus();
+  const int per = (vblocks + 7) / 8, cus = xcd_cus();
   const int grid = 8 * (per < cus ? per : cus);
   const bool aligned = h % 128 == 0 && w.ld_s % 4 == 0 &&
                        reinterpret_cast<uintptr_t>(w.scales) % 4 == 0;
@@ -659,8 +677,8 @@ void launch_fp4_partials(const uint16_t* hidden, int64_t ld_h, const Fp4Weight& 
                            : (aligned ? linear_fp4_narrow<64, true> : linear_fp4_narrow<64, false>);
   hipLaunchKernelGGL(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads4), 0, s,
                      hidden, ld_h, w.data, w.ld_d, w.scales, w.ld_s, n, v,
-                     static_cast<int>(h / BK), mblocks, vblocks, targets.p, targets.is32, ignore,
-                     pm, ps, pt, ex);
+                     static_cast<int>(h / BK), vblocks, targets.p, targets.is32, ignore, pm, ps,
+                     pt, ex);
 }
 
 }  // namespace itl
