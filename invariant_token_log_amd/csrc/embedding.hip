@@ -4,8 +4,8 @@
 //   y[i] = rne(scale E[t_i])
 //   dE[t] = rne([dE[t] +] scale sum over i ascending with t_i = t of dy[i])
 //
-// The lookup is bound by memory: one 16-byte access a thread, a row's column
-// chunks side by side.
+// The lookup is bound by memory: 16-byte accesses, a row's column chunks side by
+// side, several rows a thread.
 //
 // The gradient sorts the tokens with their positions, so that the occurrences of
 // a token form a run in ascending position, and sums every run in fp32:
@@ -35,7 +35,15 @@ namespace itl {
 
 namespace {
 
-template <typename T, bool VEC>
+// Rows a thread takes when whole 16-byte accesses of one row a thread would make
+// more than kLookupGroups workgroups, their loads in flight together.  V = 151936, H = 4096, one,
+// two, four, eight rows, us: 16384 bf16 rows 44.5, 40.1, 41.3, 43.0, from 4 bits 49.5,
+// 45.8, 42.9, 44.7; 4096 from 4 bits 14.6, 13.9, 13.6, 14.3 (the floors are 41.6, 26.4
+// and 6.6 at 6.45 TB/s; the tokens' most frequent rows come from the caches).  16 rows
+// take 2.6 us with one and 3.0 with two, unaligned rows 5 to 10% longer with two.
+constexpr int kLookupRows = 2, kLookupRowsFp4 = 4, kLookupGroups = 4096;
+
+template <typename T, bool VEC, int R>
 __global__ __launch_bounds__(256) void embedding_kernel(const T* __restrict__ table, int64_t ld_t,
                                                         int64_t v, int64_t h,
                                                         const void* __restrict__ tok,
@@ -43,45 +51,73 @@ __global__ __launch_bounds__(256) void embedding_kernel(const T* __restrict__ ta
                                                         float scale, int tx, T* __restrict__ out,
                                                         int64_t ld_o) {
   const Targets tokens{tok, tok32};
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * (256 / tx) + threadIdx.x / tx;
+  const int64_t rows = 256 / tx;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * R * rows + threadIdx.x / tx;
   const int64_t c = (static_cast<int64_t>(blockIdx.y) * tx + threadIdx.x % tx) * kE;
-  if (r >= n || c >= h) return;
-  const int64_t t = tokens[r];
-  float x[kE];
-  if (t >= 0 && t < v && t != ignore) {
-    widen_raw<T>(load_raw<T, VEC>(table + t * ld_t, c, h), x);
+  if (r0 >= n || c >= h) return;
+  int64_t t[R];
+  Raw<T> raw[R];
 #pragma unroll
-    for (int e = 0; e < kE; ++e) x[e] = x[e] * scale;
-  } else {
-    const float fill = t == ignore ? 0.0f : __uint_as_float(0x7fc00000u);
+  for (int i = 0; i < R; ++i) t[i] = tokens[min(r0 + i * rows, n - 1)];
 #pragma unroll
-    for (int e = 0; e < kE; ++e) x[e] = fill;
+  for (int i = 0; i < R; ++i)
+    if (t[i] >= 0 && t[i] < v && t[i] != ignore)
+      raw[i] = load_raw<T, VEC>(table + t[i] * ld_t, c, h);
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int64_t r = r0 + i * rows;
+    float x[kE];
+    if (t[i] >= 0 && t[i] < v && t[i] != ignore) {
+      widen_raw<T>(raw[i], x);
+#pragma unroll
+      for (int e = 0; e < kE; ++e) x[e] = x[e] * scale;
+    } else {
+      const float fill = t[i] == ignore ? 0.0f : __uint_as_float(0x7fc00000u);
+#pragma unroll
+      for (int e = 0; e < kE; ++e) x[e] = fill;
+    }
+    if (r < n) store_raw<T, VEC>(out + r * ld_o, c, h, round_raw<T>(x));
   }
-  store_raw<T, VEC>(out + r * ld_o, c, h, round_raw<T>(x));
 }
 
-template <typename T, bool VEC>
+template <typename T, bool VEC, int R>
 __global__ __launch_bounds__(256) void embedding_fp4_kernel(
     const uint8_t* __restrict__ data, int64_t ld_d, const uint8_t* __restrict__ scales,
     int64_t ld_s, int64_t v, int64_t h, const void* __restrict__ tok, int32_t tok32, int64_t n,
     int64_t ignore, float scale, int tx, T* __restrict__ out, int64_t ld_o) {
   const Targets tokens{tok, tok32};
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * (256 / tx) + threadIdx.x / tx;
+  const int64_t rows = 256 / tx;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * R * rows + threadIdx.x / tx;
   const int64_t c = (static_cast<int64_t>(blockIdx.y) * tx + threadIdx.x % tx) * kE;
-  if (r >= n || c >= h) return;
-  const int64_t t = tokens[r];
-  float x[kE];
-  if (t >= 0 && t < v && t != ignore) {
-    const uint32_t q = *reinterpret_cast<const uint32_t*>(data + t * ld_d + c / 2);
-    const float s = fp4_scale(scales[t * ld_s + c / kFp4Group]);
+  if (r0 >= n || c >= h) return;
+  int64_t t[R];
+  uint32_t q[R];
+  uint8_t sb[R];
 #pragma unroll
-    for (int e = 0; e < kE; ++e) x[e] = fp4_value(q >> (4 * e)) * s * scale;
-  } else {
-    const float fill = t == ignore ? 0.0f : __uint_as_float(0x7fc00000u);
+  for (int i = 0; i < R; ++i) t[i] = tokens[min(r0 + i * rows, n - 1)];
 #pragma unroll
-    for (int e = 0; e < kE; ++e) x[e] = fill;
+  for (int i = 0; i < R; ++i) {
+    q[i] = sb[i] = 0;
+    if (t[i] >= 0 && t[i] < v && t[i] != ignore) {
+      q[i] = *reinterpret_cast<const uint32_t*>(data + t[i] * ld_d + c / 2);
+      sb[i] = scales[t[i] * ld_s + c / kFp4Group];
+    }
   }
-  store_raw<T, VEC>(out + r * ld_o, c, h, round_raw<T>(x));
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int64_t r = r0 + i * rows;
+    float x[kE];
+    if (t[i] >= 0 && t[i] < v && t[i] != ignore) {
+      const float s = fp4_scale(sb[i]);
+#pragma unroll
+      for (int e = 0; e < kE; ++e) x[e] = fp4_value(q[i] >> (4 * e)) * s * scale;
+    } else {
+      const float fill = t[i] == ignore ? 0.0f : __uint_as_float(0x7fc00000u);
+#pragma unroll
+      for (int e = 0; e < kE; ++e) x[e] = fill;
+    }
+    if (r < n) store_raw<T, VEC>(out + r * ld_o, c, h, round_raw<T>(x));
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -552,8 +588,8 @@ BwdLayout bwd_layout(int64_t n, int64_t h) {
   return l;
 }
 
-// Bytes that workgroups beside the sort, and beside the last merge, clear: what
-// the memory takes in their time (7 us and 6).
+// Bytes that workgroups beside the sort, and beside the last merge, clear: about
+// what the memory takes in their time (16384 tokens: 11.5 us each with them).
 constexpr int64_t kSortClears = int64_t{40} << 20, kRankClears = int64_t{32} << 20;
 
 template <typename T, typename U>
@@ -631,15 +667,16 @@ void bwd_typed(const void* dy, int64_t ld_y, Targets tokens, int64_t n, int64_t 
                        ld_t);
 }
 
-// Rows a launch, with tx threads along a row.
+// Rows a launch, with tx threads along a row and one or `several` rows a thread.
 template <typename F>
-void over_rows(int64_t n, int64_t chunks, F launch) {
+void over_rows(int64_t n, int64_t chunks, int several, bool vec, F launch) {
   const int tx = row_threads(chunks);
-  const int64_t rows = 256 / tx;
+  const int64_t across = (chunks + tx - 1) / tx;
+  const bool more = vec && n * tx / 256 * across > kLookupGroups;
+  const int64_t rows = 256 / tx * (more ? several : 1);
   for (int64_t r0 = 0; r0 < n; r0 += kMaxGroups * rows) {
     const int64_t m = n - r0 < kMaxGroups * rows ? n - r0 : kMaxGroups * rows;
-    launch(dim3(static_cast<unsigned>((m + rows - 1) / rows),
-                static_cast<unsigned>((chunks + tx - 1) / tx)),
+    launch(more, dim3(static_cast<unsigned>((m + rows - 1) / rows), static_cast<unsigned>(across)),
            tx, r0, m);
   }
 }
@@ -653,8 +690,10 @@ void embedding_typed(const void* table, int64_t ld_t, int64_t v, int64_t h, Targ
                      int64_t n, int64_t ignore, float scale, void* out, int64_t ld_o,
                      hipStream_t s) {
   const bool vec = fits16(table, ld_t, sizeof(T)) && fits16(out, ld_o, sizeof(T));
-  auto kern = vec ? embedding_kernel<T, true> : embedding_kernel<T, false>;
-  over_rows(n, (h + kE - 1) / kE, [&](dim3 grid, int tx, int64_t r0, int64_t m) {
+  over_rows(n, (h + kE - 1) / kE, kLookupRows, vec,
+            [&](bool more, dim3 grid, int tx, int64_t r0, int64_t m) {
+    auto kern = more ? embedding_kernel<T, true, kLookupRows>
+                     : vec ? embedding_kernel<T, true, 1> : embedding_kernel<T, false, 1>;
     hipLaunchKernelGGL(kern, grid, dim3(256), 0, s, static_cast<const T*>(table), ld_t, v, h,
                        tokens_at(tokens, r0), tokens.is32, m, ignore, scale, tx,
                        static_cast<T*>(out) + r0 * ld_o, ld_o);
@@ -666,8 +705,10 @@ void embedding_fp4_typed(const uint8_t* data, int64_t ld_d, const uint8_t* scale
                          int64_t v, int64_t h, Targets tokens, int64_t n, int64_t ignore,
                          float scale, void* out, int64_t ld_o, hipStream_t s) {
   const bool vec = fits16(out, ld_o, sizeof(T));
-  auto kern = vec ? embedding_fp4_kernel<T, true> : embedding_fp4_kernel<T, false>;
-  over_rows(n, h / kE, [&](dim3 grid, int tx, int64_t r0, int64_t m) {
+  over_rows(n, h / kE, kLookupRowsFp4, vec,
+            [&](bool more, dim3 grid, int tx, int64_t r0, int64_t m) {
+    auto kern = more ? embedding_fp4_kernel<T, true, kLookupRowsFp4>
+                     : vec ? embedding_fp4_kernel<T, true, 1> : embedding_fp4_kernel<T, false, 1>;
     hipLaunchKernelGGL(kern, grid, dim3(256), 0, s, data, ld_d, scales, ld_s, v, h,
                        tokens_at(tokens, r0), tokens.is32, m, ignore, scale, tx,
                        static_cast<T*>(out) + r0 * ld_o, ld_o);

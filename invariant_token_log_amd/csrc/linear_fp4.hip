@@ -601,9 +601,9 @@ template <int ROWS>
 __global__ __launch_bounds__(kThreads4) void linear_fp4_wide(
     const uint16_t* __restrict__ hidden, int64_t ld_h, const uint8_t* __restrict__ data,
     int64_t ld_d, const uint8_t* __restrict__ scales, int64_t ld_s, int64_t n, int64_t v,
-    int ksteps, int mblocks, int vblocks, const void* __restrict__ tgt, int32_t tgt32, int64_t ignore,
-    float* __restrict__ pm, float* __restrict__ ps, float* __restrict__ pt, LinearExtras ex,
-    int* queue, int queued) {
+    int ksteps, int mblocks, int vblocks, const void* __restrict__ tgt, int32_t tgt32,
+    int64_t ignore, float* __restrict__ pm, float* __restrict__ ps, float* __restrict__ pt,
+    LinearExtras ex, int* queue, int queued) {
   __shared__ __align__(16) SmemFp4Wide<ROWS> sm;
   const int tid = threadIdx.x, lane = tid % kWave;
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);

@@ -241,3 +241,15 @@ def test_widest_rows():
         assert g[:, c].tolist() == [x, 33 * x, 0.0]
     assert int(torch.count_nonzero(g)) == 6
     assert torch.equal(itl.embedding_fwd(ids[16:18], g), g[[1, 0]])
+
+
+def test_lookup_fp4_many_rows():
+    gen = torch.Generator().manual_seed(4)
+    data = torch.randint(0, 256, (1000, 16), generator=gen, dtype=torch.uint8)
+    scale = torch.randint(110, 130, (1000, 1), generator=gen, dtype=torch.uint8)
+    ids = torch.randint(-1, 1001, (300001,), generator=gen)
+    ids[300000], ids[299998], ids[7] = 3, 1000, -100
+    y = itl.embedding_fwd(ids.to(dev()), itl.Fp4Rows(data.to(dev()), scale.to(dev()))).double().cpu()
+    live = (ids >= 0) & (ids < 1000)
+    assert torch.equal(y[live], fp4_values(data, scale)[ids[live]]) and not y[7].any()
+    assert y[~live & (ids != -100)].isnan().all()
