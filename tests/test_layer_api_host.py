@@ -162,6 +162,12 @@ def test_seeds():
     assert layer_ops._drop_args(0.0, None, 3, 4, dev) == (0.0, 0, None, 0, 0)
 
 
+def test_embedding_of_4bit_rows_has_no_gradient():
+    q = itl.Fp4Rows(torch.zeros(4, 16, dtype=torch.uint8), torch.zeros(4, 1, dtype=torch.uint8))
+    with pytest.raises(TypeError, match="no gradient"):
+        itl.embedding(torch.zeros(2, dtype=torch.int64), q)
+
+
 def test_head(L):
     flags = _lib.LOGP_TOKEN_FP4
     need = L.linear_token_logp_fwd_workspace_bytes(8, 128, 3000, 2, 3, flags, 0)
