@@ -7,7 +7,9 @@
 // backward pass is the same kernel on the gradient.  A dropped element is not
 // multiplied, so an infinity or a NaN there is dropped too.
 // Bound by memory: every element is read and written once.  The generator takes
-// twenty 32 x 32 bit products for 8 elements, which run beside the loads.
+// twenty 32 x 32 bit products for 8 elements, which run beside the loads.  8192 x
+// 4096 bf16: 29 to 31 us with a residual (201 MB, 6.5 to 6.9 TB/s), 21 to 23 without,
+// what a copy of as many bytes takes and no more than with p = 0.
 #include "dropout.h"
 
 #include "launch.h"
