@@ -207,3 +207,38 @@ def test_no_gradient():
         itl.norm_linear_token_logp(x, w, q)
     with pytest.raises(ValueError, match="4-bit head takes no"):
         itl.norm_linear_token_logp(x.detach(), w, q, save_logits=True)
+
+
+@pytest.mark.parametrize("n", [60, 100, 700])
+def test_head_captured_and_on_two_streams(n):
+    """Each kernel of the head replayed with new rows between eager calls, and two
+    calls at once."""
+    h, v = 512, 9000
+    q, _ = table(v, h)
+    x, tok = rows(n, h).to(dev()), given(n, v, 1)
+
+    def run():
+        return itl.linear_token_logp_fwd(x, q, tok, top_k=3, return_entropy=True)
+
+    run()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for k in range(3):
+        x.copy_(rows(n, h, seed=10 + k))
+        graph.replay()
+        torch.cuda.synchronize()
+        same(run(), out)
+    torch.cuda.synchronize()
+    streams, outs = [torch.cuda.Stream() for _ in range(2)], []
+    for st in streams:
+        with torch.cuda.stream(st):
+            outs.append(run())
+    torch.cuda.synchronize()
+    same(outs[0], out)
+    same(outs[1], out)
