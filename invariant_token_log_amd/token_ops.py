@@ -488,6 +488,8 @@ def linear_token_logp(hidden, weight, token_ids=None, top_k=0, ignore_index=-100
     entropy.  save_logits keeps the logits from forward to backward ([N, V]
     float32, bfloat16 with round_logits), which then computes one product less;
     the same bits.  prepared_weight: as linear_logp."""
+    if isinstance(weight, (QuantizedRows, Fp4Rows)):
+        raise TypeError("8-bit and 4-bit rows have no gradient: linear_token_logp_fwd scores them")
     return TokenLogp(*_LinearTokenLogp.apply(hidden, weight, token_ids, int(top_k),
                                              int(ignore_index), float(temperature),
                                              bool(return_entropy), bool(round_logits),

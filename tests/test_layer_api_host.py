@@ -162,10 +162,13 @@ def test_seeds():
     assert layer_ops._drop_args(0.0, None, 3, 4, dev) == (0.0, 0, None, 0, 0)
 
 
-def test_embedding_of_4bit_rows_has_no_gradient():
+def test_rows_of_few_bits_have_no_gradient():
     q = itl.Fp4Rows(torch.zeros(4, 16, dtype=torch.uint8), torch.zeros(4, 1, dtype=torch.uint8))
     with pytest.raises(TypeError, match="no gradient"):
         itl.embedding(torch.zeros(2, dtype=torch.int64), q)
+    for rows in (q, itl.QuantizedRows(torch.zeros(4, 64), torch.zeros(4))):
+        with pytest.raises(TypeError, match="no gradient"):
+            itl.linear_token_logp(torch.zeros(2, 32), rows)
 
 
 def test_head(L):
