@@ -17,12 +17,15 @@
 // Each thread adds its elements in ascending order, the lanes of a wave follow
 // in a butterfly and the waves in order: a row's results depend on h and the
 // row alone.
-// Measured, us (TB/s; a copy reaches 6.45).  Forward with a residual: 8192 x 4096
-// bf16 50, with dropout 52 (5.2), 4096 x 8192 bf16 54 (5.0), 4096 x 4096 fp32 55
-// (4.9), 8192 x 1024 bf16 15 (4.5), 2048 x 16384 bf16 46 (5.8); 2047 x 5117 fp16,
-// rows off 16 bytes, 24 (3.5).  Gradient, with the gradient of s: 58 (4.7), with
-// dropout 66 (5.3), 57, 65, 25, 30 for the columns and 53, and 45; the sum over the
-// rows is 4 to 6 more.
+// Measured, us (TB/s; a copy reaches 6.45).  Forward with a residual, calls in a
+// row: 8192 x 4096 bf16 44, with dropout 42 (6.4), 4096 x 8192 bf16 44, 4096 x 4096
+// fp32 44, 2048 x 16384 bf16 46, 8192 x 1024 bf16 15 (4.5); 2047 x 5117 fp16, rows off
+// 16 bytes, 24 (3.5); behind a gradient, whose output the caches still write back,
+// 50 to 55 for the first four.  (Mean and squares in one exchange a row, the squares
+// from every wave's own mean: 44 with dropout, 78 for the longest.)  Gradient, with
+// the gradient of s: 55 to 58 (4.8), with dropout 66 to 76 (4.8), 57, 66, 30 for the
+// columns and 53, 25, and 45; the sum over the rows is 4 to 6 more.  Rows two ahead,
+// one exchange a row and the masks before it made no difference to the gradient.
 #include "layer_norm.h"
 
 #include "launch.h"
