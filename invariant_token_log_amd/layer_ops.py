@@ -103,8 +103,9 @@ def embedding_bwd(token_ids, grad, num_rows, scale=1.0, ignore_index=-100, out_d
 # The backward passes of the autograd functions run in a thread of their own, where
 # every object of the interpreter that they touch comes from another core's cache:
 # what the forward has checked is not checked again, sizes come along as integers
-# (training calls on few rows: layer norm 142 -> 126 us, dropout 84 -> 74, embedding 97
-# -> 88; a call of nothing but tensors handed on takes 40 to 67).
+# (training calls on few rows: layer norm 142 -> 126 to 131 us, dropout 84 -> 74, embedding
+# 97 -> 88; a call of nothing but tensors handed on takes 40 to 67).  Hooks on saved
+# tensors may have moved them: addresses and strides are those of the backward.
 class _Embedding(torch.autograd.Function):
     @staticmethod
     def forward(ctx, token_ids, weight, scale, ignore_index):
@@ -185,6 +186,11 @@ def dropout_bwd(grad, p, seed, draw=0, first_row=0, dx_out=None):
     return dropout_fwd(grad, p, seed, None, draw, first_row, dx_out)
 
 
+def _seed_again(drop, saved):
+    """drop with the seed where it is now: hooks on saved tensors may have moved it."""
+    return (*drop[:2], saved[0].data_ptr(), *drop[3:]) if saved else drop
+
+
 def _dropout_back(g, drop, code, n, h):
     """dropout's gradient of x from contiguous rows g."""
     dx = torch.empty_like(g)
@@ -205,10 +211,11 @@ class _Dropout(torch.autograd.Function):
     @staticmethod
     @_first_order
     def backward(ctx, g):
-        ctx.saved_tensors  # a seed that has changed raises
+        saved = ctx.saved_tensors  # a seed that has changed raises
+        drop, code, n, h = ctx.sizes
         g = g.contiguous()
         need = ctx.needs_input_grad
-        dx = _dropout_back(g, *ctx.sizes) if need[0] else None
+        dx = _dropout_back(g, _seed_again(drop, saved), code, n, h) if need[0] else None
         return dx, None, None, g if need[3] else None, None, None
 
 
@@ -237,7 +244,7 @@ def _layer_norm_forward(x, weight, bias, residual, eps, drop, stats, y_out, sum_
     code = _dtype_code(x)
     pw, pb = _norm_weight(weight, x), _norm_bias(bias, x)
     y, py, ld_y = _norm_out(y_out, "y_out", x, h)
-    pr, ld_r, ps, ld_s, s = None, 0, None, ld_x, x
+    pr, ld_r, ps, ld_s, s = None, 0, None, 0, x
     if residual is not None:
         pr, _, _, ld_r = _norm_rows(residual, "residual", x)
     if residual is not None or drop[0] or sum_out is not None:
@@ -245,7 +252,7 @@ def _layer_norm_forward(x, weight, bias, residual, eps, drop, stats, y_out, sum_
     pm = stats.data_ptr() if stats is not None else None
     _call("layer_norm_fwd", x.device, px, ld_x, pr, ld_r, pw, pb, code, n, h, eps, *drop, py, ld_y,
           ps, ld_s, pm, pm + 4 * n if pm is not None else None)
-    return y, s, (code, n, h, ld_s, drop)
+    return y, s, (code, n, h, drop)
 
 
 def _stats(x):
@@ -325,8 +332,9 @@ class _LayerNorm(torch.autograd.Function):
     @staticmethod
     @_first_order
     def backward(ctx, gy, gs=None):
-        s, weight, stats = ctx.saved_tensors[:3]  # a seed that has changed raises
-        code, n, h, ld_s, drop, nbytes = ctx.sizes
+        s, weight, stats, *held = ctx.saved_tensors  # a seed that has changed raises
+        code, n, h, drop, nbytes = ctx.sizes
+        drop = _seed_again(drop, held)
         need_x, need_w, need_b, need_r = ctx.needs_input_grad[:4]
         # gradients may come in broadcast (a row for all rows, one value for all)
         gs = gs.contiguous() if gs is not None else None
@@ -338,6 +346,9 @@ class _LayerNorm(torch.autograd.Function):
             db = torch.zeros_like(weight) if need_b else None
             return dx, dw, db, gs, None, None, None, None, None
         gy = gy.contiguous()
+        ld_s = h
+        if s.dtype != gy.dtype or not s.is_contiguous():
+            _, _, _, ld_s = _norm_rows(s, "s", gy)
         dx = dres = torch.empty_like(gy)
         pr = pw = pb = ws = None
         dw = db = None

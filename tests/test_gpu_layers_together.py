@@ -8,6 +8,7 @@ bf16 between the operators: about ten roundings of 2^-9 on average, at most 2^-8
 each, that a gradient passes, so the relative distance of a whole gradient from
 the float64 one (taken with the same masks) stays below 10 * 2^-8."""
 
+import contextlib
 import math
 
 import pytest
@@ -171,3 +172,31 @@ def test_past_two_to_the_31_elements():
     last = itl.quantize_rows_fp4(table[-3:])
     assert torch.equal(q.data[-3:], last.data) and torch.equal(q.scale[-3:], last.scale)
     assert torch.equal(itl.embedding_fwd(ids, q)[0], itl.embedding_fwd(torch.tensor([2], device=dev()), last)[0])
+
+
+def test_saved_tensors_that_hooks_move():
+    """Saved tensors that live elsewhere between forward and backward: a strided row
+    comes back contiguous, a seed at another address (its first place is used again)."""
+    gen = torch.Generator().manual_seed(3)
+    buf = torch.randn(33, 136, generator=gen).to(dev())
+    w, b = torch.randn(2, 128, generator=gen).to(dev())
+    g = torch.randn(33, 128, generator=gen).to(dev())
+    ids = torch.randint(0, 50, (33,), generator=gen).to(dev())
+
+    def grads(hooks):
+        x = buf[:, :128].detach().requires_grad_()
+        table = torch.randn(50, 128, generator=torch.Generator().manual_seed(4)).to(dev()).requires_grad_()
+        with hooks:
+            seed = torch.tensor([77], device=dev())
+            y = itl.layer_norm(x, w, b)
+            z, s = itl.layer_norm(x, w, b, residual=itl.embedding(ids, table), dropout=0.3, seed=seed, draw=1)
+            u = itl.dropout(x, 0.4, seed, draw=2)
+            del seed
+        over = [torch.full((1,), 5 + i, dtype=torch.int64, device=dev()) for i in range(64)]
+        out = torch.autograd.grad([y, z, s, u], [x, table], [g, g, g, g])
+        del over
+        return out
+
+    want = grads(contextlib.nullcontext())
+    got = grads(torch.autograd.graph.save_on_cpu())
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
