@@ -169,6 +169,10 @@ def _dropout(x, residual, out, drop):
 
 
 def _dropout_args(p, seed, draw, first_row, device):
+    if seed is None:
+        if p:
+            raise ValueError("dropout needs a seed")
+        seed = 0
     return (float(p), *_seed(seed, device), *_place(draw, first_row))
 
 
@@ -176,7 +180,7 @@ def dropout_fwd(x, p, seed, residual=None, draw=0, first_row=0, out=None):
     """residual + dropped(x) (dropped(x) without a residual), rounded once to x's
     dtype: an element of x [*lead, H] (float32, bfloat16, float16) is dropped with
     probability p (to 2^-16), the others are scaled by the reciprocal of what is
-    kept.  out may be x or residual."""
+    kept.  seed may be None where p is 0.  out may be x or residual."""
     return _dropout(x, residual, out, _dropout_args(p, seed, draw, first_row, x.device))[0]
 
 
@@ -232,8 +236,6 @@ def _drop_args(p, seed, draw, first_row, device):
     """The library's (p, seed, its address, draw, first row)."""
     if not p:
         return 0.0, 0, None, 0, 0
-    if seed is None:
-        raise ValueError("dropout needs a seed")
     return _dropout_args(p, seed, draw, first_row, device)
 
 

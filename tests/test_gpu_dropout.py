@@ -201,3 +201,16 @@ def test_widest_rows():
     assert abs(float((y == 0).float().mean()) - 0.25) < 6 * (0.1875 / h) ** 0.5
     with pytest.raises(RuntimeError):
         itl.dropout_fwd(torch.empty(1, h + 8, dtype=torch.bfloat16, device=dev()), 0.25, SEED)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_without_a_seed(dtype):
+    """Nothing is dropped: x itself, or the sum rounded once; both gradients whole."""
+    x, xd = rows(5, 77, dtype, 1)
+    r, rd = rows(5, 77, dtype, 2)
+    assert torch.equal(itl.dropout_fwd(xd, 0.0, None), xd) and torch.equal(itl.dropout_bwd(xd, 0, None), xd)
+    a, b = xd.clone().requires_grad_(), rd.clone().requires_grad_()
+    y = itl.dropout(a, 0.0, None, residual=b)
+    assert torch.equal(y.cpu(), (x.float() + r.float()).to(TYPES[dtype]))
+    da, db = torch.autograd.grad(y, [a, b], xd)
+    assert torch.equal(da, xd) and torch.equal(db, xd)

@@ -216,3 +216,17 @@ def test_embedding_gradient_workspace_of_long_batches(L):
             (2 * ((n + 31) // 32) * 32 + 255) // 256 * 256
 
     assert keys(2048) == 0 and keys(2304) == 8 * 2304 and keys(16384) == 8 * 16384 and keys(16640) == 16 * 16640
+
+
+def test_dropout_without_a_seed():
+    """As in the layer norm: none is needed where nothing is dropped, and one is asked for
+    by name elsewhere (the rows' device is looked at next)."""
+    x = torch.zeros(2, 8)
+    for call in (itl.dropout_fwd, itl.dropout_bwd, itl.dropout):
+        for p in (0, 0.0):
+            with pytest.raises(ValueError, match="ROCm device"):
+                call(x, p, None)
+        for p in (0.5, NAN, -1.0):
+            with pytest.raises(ValueError, match="needs a seed"):
+                call(x, p, None)
+    assert layer_ops._dropout_args(0.0, None, 3, 4, x.device) == (0.0, 0, None, 3, 4)
