@@ -299,3 +299,50 @@ def test_graph_replays():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, c) for a, c in zip(out, step(SEED + k)))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("h", [6144, 6145, 24576, 24577, 32761, 32768])
+def test_forward_at_more_ends_of_the_teams(h, dtype):
+    """Chunks a thread on both sides of three and four; the longest rows in registers."""
+    test_forward(h, dtype)
+
+
+# Rows of every team and chunk count of the gradient, whole chunks and not, more than twice
+# as many as there are teams (1024 of 64 threads, 512 or 256 of the others; 102 to 73 groups of
+# rows where they are read again, past 8192 elements in fp32 and 12288): a team walks two or
+# three rows, the next one's loads ahead.
+SEVERAL = [(2100, 505), (2100, 512), (2100, 1021), (2100, 1024), (1100, 2045), (1100, 2048), (1100, 4093), (1100, 4096),
+           (600, 5117), (600, 5120), (600, 8185), (600, 8192), (600, 8200), (600, 12281), (600, 12288), (160, 12297)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("n,h", SEVERAL)
+def test_gradient_of_several_rows_a_team(n, h, dtype):
+    s, sd = rows(n, h, dtype, h, 1.5, 0.3)
+    dy, dyd = rows(n, h, dtype, h + 1)
+    ds, dsd = rows(n, h, dtype, h + 2)
+    w = weights(h, dtype)[0]
+    wd = w.to(dev())
+    _, _, mean, rstd = itl.layer_norm_fwd(sd, wd, eps=EPS, return_stats=True)
+
+    def run(g, d, p, **kw):
+        return itl.layer_norm_bwd(sd, wd, mean, rstd, g, d, dropout=p, seed=SEED, draw=6, **kw)
+
+    got = run(dyd, dsd, 0.3)
+    check_gradient(got, s, w, dy, ds, dtype, 0.3, 6)
+    assert all(torch.equal(a, c) for a, c in zip(run(dyd, dsd, 0.3), got))
+    g2, d2 = dyd.clone(), dsd.clone()
+    assert all(torch.equal(a, c) for a, c in zip(run(g2, d2, 0.3, dx_out=g2, dresidual_out=d2), got))
+    # without dropout: dx is what dresidual is with it; the sums over the rows are the same
+    plain = run(dyd, dsd, 0.0)
+    assert torch.equal(plain[0], got[1]) and torch.equal(plain[2], got[2]) and torch.equal(plain[3], got[3])
+    # a row alone, the last and one in the middle
+    for r in (n // 2 + 1, n - 1):
+        one = itl.layer_norm_bwd(sd[r:r + 1], wd, mean[r:r + 1], rstd[r:r + 1], dyd[r:r + 1], dsd[r:r + 1], dropout=0.3,
+                                 seed=SEED, draw=6, first_row=r)
+        assert torch.equal(one[0], got[0][r:r + 1]) and torch.equal(one[1], got[1][r:r + 1])
+    # nothing but y was used
+    only = run(dyd, None, 0.0)
+    check_gradient((only[0][-4:], None, None, None), s[-4:], w, dy[-4:], None, dtype)
+    assert torch.equal(only[2], got[2]) and torch.equal(only[3], got[3])
