@@ -242,3 +242,89 @@ def test_head_captured_and_on_two_streams(n):
     torch.cuda.synchronize()
     same(outs[0], out)
     same(outs[1], out)
+
+
+def alike(a, b):
+    """same, any NaN being like another."""
+    for x, y, name in zip(a, b, a._fields):
+        if x is not None:
+            assert torch.equal(x.isnan(), y.isnan()) and torch.equal(x[~x.isnan()], y[~y.isnan()]), name
+
+
+@pytest.mark.parametrize("n", [4, 20, 40, 100, 470])
+@pytest.mark.parametrize("h", [128, 192])
+@pytest.mark.parametrize("lo,hi,codes", [(0, 0, 0xFF), (1, 1, 0xFF), (0, 3, 0xFF), (2, 2, 0xFF), (127, 128, 0xFF), (126, 129, 0xFF),
+                                         (199, 202, 0xFF), (252, 252, 0xFF), (249, 252, 0xFF), (253, 253, 0xBB), (251, 254, 0xBB)])
+def test_every_scale_reaches_the_logits(lo, hi, codes, h, n):
+    """All groups of all columns have scale bytes from lo to hi, and the hidden rows a
+    power of two that brings the logits near 1 to 100 (past 252 magnitudes up to 3/2: greater
+    ones pass the range).  Hidden values are eighths and codes halves of powers of two: with
+    three bits of the scales' span a logit is a sum of 192 multiples of a unit, each at most 15
+    * 12 * 8 of it, so below 2^24 units and exact in fp32, whatever the order.  So
+    log-probabilities are off by the stated 1e-5 + 1e-5 of the value and by the rounding of
+    the log-sum-exp, 2^-24 of it."""
+    v = 300
+    gen = torch.Generator().manual_seed(lo + h)
+    data = torch.randint(0, 256, (v, h // 2), generator=gen, dtype=torch.uint8) & codes
+    scale = torch.randint(lo, hi + 1, (v, h // 32), generator=gen, dtype=torch.uint8)
+    values = fp4_values(data, scale)
+    w = values.bfloat16()
+    assert torch.equal(w.double(), values)
+    power = min(max(124 - hi, -125), 124)
+    x = torch.randint(8, 16, (n, h), generator=gen) * (2 * torch.randint(0, 2, (n, h), generator=gen) - 1)
+    x = (x.double() * 2.0 ** (power - 3)).bfloat16()
+    z = x.double() @ values.T
+    assert (z != 0).float().mean() > 0.9 and torch.equal(z.float().double(), z) and 0.1 < z.abs().max() < 1000
+    tok = given(n, v, 3)
+    kw = dict(top_k=64, return_entropy=True)
+    got = itl.linear_token_logp_fwd(x.to(dev()), itl.Fp4Rows(data.to(dev()), scale.to(dev())), tok, **kw)
+    same(got, itl.linear_token_logp_fwd(x.to(dev()), w.to(dev()), tok, **kw))
+    ref = token_scores(z, tok, 64)
+    for name in ("logp", "lse", "top_logp"):
+        a, b = getattr(got, name).double().cpu(), ref[name]
+        assert ((a - b).abs() <= 1e-5 + 1e-5 * b.abs() + 2.0 ** -24 * ref["lse"].abs().view(-1, *[1] * (b.dim() - 1))).all(), name
+
+
+@pytest.mark.parametrize("n", [4, 20, 40, 100, 470])
+@pytest.mark.parametrize("b,least", [(253, 4), (254, 2)])
+def test_values_past_the_range_are_infinities(b, least, n):
+    """Under the scale bytes 253 and 254 magnitudes from 4 and from 2 on: their column's
+    logit is an infinity, or a NaN where both signs meet; others keep theirs."""
+    h, v = 128, 300
+    q, _ = table(v, h)
+    code = {2: 4, 4: 6}[least]
+    x = rows(n, h).abs().clamp(min=0.25)
+    tok = torch.tensor([[3, 7, 8, 200]]).repeat(n, 1).to(dev())
+    without = itl.linear_token_logp_fwd(x.to(dev()), q, tok, top_k=20)
+    q.scale[7], q.data[7] = b, 0x11 * (code | 8)  # an infinity below
+    got = itl.linear_token_logp_fwd(x.to(dev()), q, tok, top_k=20, return_entropy=True)
+    w = fp4_values(q.data, q.scale).bfloat16().to(dev())
+    assert (w[7] == -torch.inf).all() and w[:7].isfinite().all() and w[8:].isfinite().all()
+    alike(got, itl.linear_token_logp_fwd(x.to(dev()), w, tok, top_k=20, return_entropy=True))
+    assert (got.logp[:, 1] == -torch.inf).all() and got.logp[:, [0, 2, 3]].isfinite().all() and got.lse.isfinite().all()
+    assert (got.top_ids != 7).all() and (got.lse <= without.lse).all()
+    for data in (0x11 * code, code | 0x80 | code << 4):  # above; both
+        q.data[7] = data
+        w = fp4_values(q.data, q.scale).bfloat16().to(dev())
+        got = itl.linear_token_logp_fwd(x.to(dev()), q, tok, top_k=20, return_entropy=True)
+        alike(got, itl.linear_token_logp_fwd(x.to(dev()), w, tok, top_k=20, return_entropy=True))
+        assert not got.lse.isfinite().any()
+    # one step below the least such magnitude stays in the range
+    q.data[7] = 0x11 * (code - 1)
+    assert fp4_values(q.data, q.scale)[7].bfloat16().isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_lookup_at_the_ends_of_the_scales(dtype):
+    """Values are decoded in fp32, where they are exact or, past its range (bytes 253 and 254), an
+    infinity that the call's scale leaves one."""
+    data = torch.arange(256, dtype=torch.uint8).view(8, 32).repeat(1, 2)[:, :64]
+    codes = torch.arange(256, dtype=torch.uint8).repeat(8)[:8 * 64].view(8, 64)
+    scale = torch.tensor([0, 1, 2, 127, 252, 253, 254, 255], dtype=torch.uint8).repeat_interleave(4).view(8, 4)
+    for data in (data, codes):
+        q = itl.Fp4Rows(data.to(dev()), scale.to(dev()))
+        values = fp4_values(data, scale).float()
+        for by in (1.0, 0.5, 2.0 ** 60):
+            got = itl.embedding_fwd(torch.arange(8, device=dev()), q, scale=by, out_dtype=TYPES[dtype]).cpu()
+            want = (values * torch.tensor(by)).to(TYPES[dtype])
+            assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got[:7], want[:7]) and got[7].isnan().all()
