@@ -253,3 +253,31 @@ def test_lookup_fp4_many_rows():
     live = (ids >= 0) & (ids < 1000)
     assert torch.equal(y[live], fp4_values(data, scale)[ids[live]]) and not y[7].any()
     assert y[~live & (ids != -100)].isnan().all()
+
+
+@pytest.mark.parametrize("dtype,h,ld", [("fp32", 100, 105), ("bf16", 101, 103), ("fp16", 96, 104)])
+@pytest.mark.parametrize("n", [0, 1000, 5000])
+def test_gradient_into_a_large_table_with_gaps(n, dtype, h, ld):
+    """More rows than are cleared beside the sort and the merge (40 and 32 MB): the absent ones
+    of the rest go row by row.  Gaps stay as they are, and the rows behind the table."""
+    v = 2 ** 27 // (h * (4 if dtype == "fp32" else 2)) + 37
+    gen = torch.Generator().manual_seed(n + h)
+    ids = torch.randint(0, v, (n,), generator=gen)
+    if n:
+        ids[:8] = torch.tensor([0, v - 1, v - 2, v - 64, v - 65, v // 2, v // 2, -100])
+        ids[100:140] = v - 5  # several pieces among absent rows
+        ids[200:264] = torch.arange(v - 300, v - 236)  # a whole block of 64 present
+    grid = (torch.randint(-15, 16, (n, h), generator=gen).float() / 16).to(TYPES[dtype])
+    live = ids >= 0
+    want = torch.zeros(v, h).index_add_(0, ids[live], grid[live].float())  # exact: few sixteenths a sum
+    wide = torch.full((v + 2, ld), 3.0, dtype=TYPES[dtype], device=dev())
+    got = itl.embedding_bwd(ids.to(dev()), grid.to(dev()), v, dweight_out=wide[:v, :h])
+    assert got.data_ptr() == wide.data_ptr() and torch.equal(got.cpu(), want.to(TYPES[dtype]))
+    assert (wide[:, h:] == 3).all() and (wide[v:] == 3).all()
+    # the same sums without gaps
+    assert torch.equal(itl.embedding_bwd(ids.to(dev()), grid.to(dev()), v), got)
+    # added: absent rows stay too
+    wide.fill_(3.0)
+    itl.embedding_bwd(ids.to(dev()), grid.to(dev()), v, dweight_out=wide[:v, :h], accumulate=True)
+    assert torch.equal(wide[:v, :h].cpu(), (want + 3).to(TYPES[dtype]))
+    assert (wide[:, h:] == 3).all() and (wide[v:] == 3).all()
