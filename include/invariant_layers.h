@@ -42,7 +42,8 @@ int32_t embedding_fwd(const void* table, int64_t ld_t, int64_t v, int64_t h, int
 /*
  * The same from 4-bit rows (fp4_quantize): data [v, ld_d] and scales [v, ld_s]
  * bytes, out of out_dtype.  h a multiple of 32; 16-byte aligned data rows
- * (LOGP_ERR_ALIGN).
+ * (LOGP_ERR_ALIGN).  Table values are those of fp32: exact, or an infinity where
+ * scale bytes 253 and 254 pass its range.
  */
 int32_t embedding_fp4_fwd(const void* data, int64_t ld_d, const void* scales, int64_t ld_s,
                           int64_t v, int64_t h, const void* tokens, int32_t token_dtype, int64_t n,
@@ -85,7 +86,8 @@ int32_t embedding_bwd(const void* dy, int64_t ld_y, int32_t dtype, const void* t
  * of out without a residual; that of the residual is the gradient of out.
  *   x [n, ld_x], residual [n, ld_r] (NULL: none), out [n, ld_o] of dtype;
  *   out may be exactly x or residual.  h at most 2^24 (LOGP_ERR_SHAPE).
- *   p in [0, 1], draw in [0, 2^32), first_row >= 0 (LOGP_ERR_VALUE).
+ *   p in [0, 1], draw in [0, 2^32), first_row from 0 to 2^63 - 2^31
+ *   (LOGP_ERR_VALUE).
  *   seed_at NULL, or the seed's address on the device, which is read in place of
  *   `seed` when the kernel runs (a captured graph draws anew as it changes).
  */

@@ -1,7 +1,8 @@
 // 4-bit rows: two e2m1 values a byte (the even column in the low half) and one
 // scale byte b, for 2^(b - 127), a group of 32 columns.  e2m1 stands for 0,
-// 1/2, 1, 3/2, 2, 3, 4, 6 and their negatives.  Every value is exact in bf16
-// unless it is subnormal there (b below 2) or past its range (b above 252).
+// 1/2, 1, 3/2, 2, 3, 4, 6 and their negatives.  Every value is exact in bf16, where
+// it is subnormal too (b of 0 and 1: multiples of 2^-128), but for magnitudes past
+// its range, which become infinities (from 4 on under b = 253, from 2 under 254).
 #pragma once
 
 #include <hip/hip_runtime.h>

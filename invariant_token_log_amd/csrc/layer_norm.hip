@@ -9,11 +9,12 @@
 //
 // Bound by memory: every element is read and written once, so a row stays in
 // the registers of the team of threads that owns it: 64 threads for rows of up
-// to 1024 elements, 256 up to 8192 and 1024 beyond, thread t holding the chunks
-// of 8 elements t, t + TEAM, ...  The mean comes first and the squares are of
-// differences from it, so a row far from zero loses nothing.  Rows too long for
-// the registers (forward past 32768 elements, 16384 in fp32, gradient past 12288)
-// are read again instead, from the caches.
+// to 1024 elements, 256 up to 8192 and beyond that 1024 in the forward, 512 in
+// the gradient, thread t holding the chunks of 8 elements t, t + TEAM, ...  The
+// mean comes first and the squares are of differences from it, so a row far from
+// zero loses nothing.  Rows too long for the registers (forward past 32768
+// elements, 16384 in fp32; gradient past 12288, 8192 in fp32) are read again
+// instead, from the caches.
 // Each thread adds its elements in ascending order, the lanes of a wave follow
 // in a butterfly and the waves in order: a row's results depend on h and the
 // row alone.
@@ -22,10 +23,15 @@
 // fp32 44, 2048 x 16384 bf16 46, 8192 x 1024 bf16 15 (4.5); 2047 x 5117 fp16, rows off
 // 16 bytes, 24 (3.5); behind a gradient, whose output the caches still write back,
 // 50 to 55 for the first four.  (Mean and squares in one exchange a row, the squares
-// from every wave's own mean: 44 with dropout, 78 for the longest.)  Gradient, with
-// the gradient of s: 55 to 58 (4.8), with dropout 66 to 76 (4.8), 57, 66, 30 for the
-// columns and 53, 25, and 45; the sum over the rows is 4 to 6 more.  Rows two ahead,
-// one exchange a row and the masks before it made no difference to the gradient.
+// from every wave's own mean: 44 with dropout, 78 for the longest.)
+// Gradient, with the gradient of s, and with dropout and both gradients of it:
+// 8192 x 4096 bf16 51 (5.2) and 71 (4.8), 4096 x 4096 fp32 51 (5.2) and 66 (5.1), 4096
+// x 8192 bf16 61 (4.4) and 73 (4.6), 8192 x 1024 bf16 22 (3.1) and 26 (3.3): four waves
+// a CU, each with its partial sums; 2048 x 16384 bf16 51 and 69, and 27 for the columns
+// (3.5): read again; 2047 x 5117 fp16, rows off 16 bytes, 43 (1.9) and 51 (2.1): element
+// by element in the chunks that are not whole.  The sum over the rows is 4 to 5
+// more.  Rows two ahead, one exchange a row and the masks before it made no
+// difference.
 #include "layer_norm.h"
 
 #include "launch.h"
@@ -431,9 +437,10 @@ __global__ __launch_bounds__(256) void layer_norm_columns_kernel(GradRows<T> g, 
     }
 }
 
-// dweight and dbias = rne(sum over the P partial rows): 32 columns (whole lines) a
-// workgroup, 32 groups of rows, each in ascending order, then the groups in order.
-// 512 rows of 2 x 4096: 4.9 us (16 columns: every line read twice, 7.8; 64: 5.2).
+// dweight and dbias = rne(sum over the P partial rows): 32 columns (whole lines
+// where h is a multiple of 32; else every line is read twice) a workgroup, 32
+// groups of rows, each in ascending order, then the groups in order.  512 rows of
+// 2 x 4096: 4.9 us (16 columns: every line read twice, 7.8; 64: 5.2).
 constexpr int kSumCols = 32, kSumGroups = 32;
 
 template <typename T>

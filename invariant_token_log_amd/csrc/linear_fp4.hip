@@ -29,7 +29,7 @@
 // beside the products of the step, 20 vector instructions to 32 products.  A wave
 // holds a step's hidden rows in two halves, one read while the other's products
 // run: whole steps ahead, as the bf16 head holds them, do not fit its registers
-// beside the decoding.  1000 rows: 840 to 890 us (1.4 to 1.48 PFLOP/s), what the
+// beside the decoding.  1000 rows: 850 to 890 us (1.4 to 1.46 PFLOP/s), what the
 // bf16 head takes on a decoded copy of the weight, whose making took 256 more.
 #include "linear_fp4.h"
 
