@@ -13,6 +13,7 @@ import math
 
 import pytest
 import torch
+import torch.utils.checkpoint
 
 import invariant_token_log_amd as itl
 from gpu_helpers import dev
@@ -200,3 +201,50 @@ def test_saved_tensors_that_hooks_move():
     want = grads(contextlib.nullcontext())
     got = grads(torch.autograd.graph.save_on_cpu())
     assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+
+@pytest.mark.parametrize("p", [0.0, 0.3])
+def test_one_tensor_in_two_places(p):
+    """Rows that are their own residual: their gradient is the sum of both, and two leaves get
+    buffers of their own; the sum over the rows in place of both."""
+    gen = torch.Generator().manual_seed(6)
+    x, g = torch.randn(2, 37, 520, generator=gen).to(dev())
+    w = torch.randn(520, generator=gen).to(dev())
+    a, b, c = (x.clone().requires_grad_() for _ in range(3))
+    y, s = itl.layer_norm(a, w, w, residual=a, dropout=p, seed=3)
+    d, = torch.autograd.grad([y, s], a, [g, g])
+    torch.autograd.backward(itl.layer_norm(b, w, w, residual=c, dropout=p, seed=3), [g, g])
+    assert torch.equal(d, b.grad + c.grad) and b.grad.data_ptr() != c.grad.data_ptr()
+    i = x.clone()
+    y2, _, _, _ = itl.layer_norm_fwd(i, w, w, residual=i, dropout=p, seed=3, sum_out=i)
+    assert torch.equal(y2, y) and torch.equal(i, s)
+    d, = torch.autograd.grad(itl.dropout(a, p, 3, residual=a), a, g)
+    assert torch.equal(d, itl.dropout_bwd(g, p, 3) + g)
+
+
+def test_autograd_on_streams_and_again():
+    """Forward on a side stream and backward on another, a graph used twice, a forward that is
+    run again for its backward: the same gradient every time."""
+    gen = torch.Generator().manual_seed(7)
+    table = torch.randn(500, 520, generator=gen).to(dev()).requires_grad_()
+    w = torch.randn(520, generator=gen).to(dev())
+    ids = torch.randint(0, 500, (3000,), generator=gen).to(dev())
+    g = torch.randn(3000, 520, generator=gen).to(dev())
+
+    def step():
+        e = itl.embedding(ids, table, 2.0)
+        return itl.dropout(itl.layer_norm(e, w, w), 0.2, 9, residual=e)
+
+    out = step()
+    want, = torch.autograd.grad(out, table, g, retain_graph=True)
+    got = [torch.autograd.grad(out, table, g)[0],
+           torch.autograd.grad(torch.utils.checkpoint.checkpoint(step, use_reentrant=False), table, g)[0]]
+    main = torch.cuda.current_stream()
+    for side in [torch.cuda.Stream() for _ in range(2)]:
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            out = step()
+        main.wait_stream(side)
+        got.append(torch.autograd.grad(out, table, g)[0])
+    torch.cuda.synchronize()
+    assert all(torch.equal(d, want) for d in got)
